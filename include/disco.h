@@ -261,6 +261,81 @@ disco_status disco_mix_weight(int B, int C_in, int C_out, int groups, int K, lon
                               const void* dout, const void* y, void* dw, void* dbias, void* workspace, size_t ws_bytes,
                               void* stream);
 
+/* Layer norm of a field over its channels, forward and backward (the pages have no counterpart:
+ * it is the norm that stands between two layers of a model).  x is (B, C, npts), the layout of
+ * the convolution's input and output with the points of a plane contiguous; for every point n of
+ * every batch element, over its C channels,
+ *
+ *   mean = sum_c x / C,  var = sum_c (x - mean)^2 / C,  r = 1 / sqrt(var + eps)
+ *   disco_norm:           out[b,c,n] = gain[c] * xh + bias[c],   xh = (x - mean) * r
+ *   disco_norm_backward:  with e = gain[c] * dout,
+ *                         dx = r * (e - sum_c e / C - xh * sum_c (e * xh) / C)
+ *                         dgain[c] = sum_{b,n} dout * xh,  dbias[c] = sum_{b,n} dout
+ *
+ * x, gain, bias, out, dout, dx, dgain and dbias are in `dtype`; statistics and sums are fp32.
+ *   gain, bias : may be NULL (ones, zeros).
+ *   stats      : 2 x (B * npts) floats, all means and then all r.  disco_norm writes them (NULL:
+ *                it does not), disco_norm_backward reads them.
+ *   dx, dgain, dbias : each may be NULL (not computed), not all three.
+ *   out may be x; dx may be dout or x.  No other overlap.
+ * Pointers need the alignment of their elements only; 16-byte aligned tensors whose npts is a
+ * multiple of 16 bytes run fastest.  disco_norm_backward takes scratch through `workspace`, at
+ * least disco_norm_workspace_size bytes, 4-byte aligned (not needed when dgain and dbias are NULL).
+ * Both are asynchronous on `stream` and allocate nothing; the gradients' order of addition is
+ * fixed (the same bits every time on the same kind of GPU).  Errors: DISCO_ERR_INVALID_ARG for a
+ * non-positive size, a negative or non-finite eps, a NULL required pointer, a pointer off its
+ * element's alignment, an unknown dtype or a missing or short workspace; DISCO_ERR_UNSUPPORTED
+ * for C above 16384 or npts above 2^31 - 1; DISCO_ERR_CUDA for a failed launch. */
+disco_status disco_norm_workspace_size(int B, int C, long long npts, disco_dtype dtype, size_t* bytes);
+disco_status disco_norm(int B, int C, long long npts, disco_dtype dtype, const void* x, const void* gain,
+                        const void* bias, double eps, void* out, float* stats, void* stream);
+disco_status disco_norm_backward(int B, int C, long long npts, disco_dtype dtype, const void* dout, const void* x,
+                                 const float* stats, const void* gain, void* dx, void* dgain, void* dbias,
+                                 void* workspace, size_t ws_bytes, void* stream);
+
+/* The orthogonalised update of the layers' weights (the Muon rule; the pages have no counterpart).
+ *
+ * A weight of the convolution is (C_out, C_in/groups, K); the rows of one group are one matrix of
+ * rows = C_out/groups and cols = C_in/groups * K.  A call takes n tensors of one shape, each
+ * groups x rows x cols values, dense, and treats every matrix by itself:
+ *
+ *   X = U / (|U|_F + eps), then `steps` times  X <- a X + b (X X^T) X + c (X X^T)^2 X
+ *
+ * (the odd polynomial acts on each singular value; with the usual a = 3.4445, b = -4.775,
+ * c = 2.0315 five steps bring all but the smallest near 1, which leaves about U (U^T U)^(-1/2)).
+ *
+ *   disco_orthogonalize:  out = X with U = update.
+ *   disco_muon:           m' = momentum * m + grad;  U = grad + momentum * m' (nesterov) or m';
+ *                         w' = (1 - lr * weight_decay) * w - lr * sqrt(max(1, rows / cols)) * X
+ *
+ * update, out, w, grad and w_out are in `dtype`, m and m_out fp32.  The pointer arrays are HOST
+ * arrays of n device pointers, read before the call returns.  out[i] may be update[i], w_out[i]
+ * may be w[i] and m_out[i] may be m[i]; no other overlap.  The iterates are held as fp16 pairs
+ * (hi + lo, 22 bits), products are summed in fp32 and the Frobenius norm in fp64.
+ * An update of zeros gives zeros; infinities and NaN spread over their own matrix only; an
+ * iterate above 16 in magnitude (coefficients that diverge) ends as infinities or NaN.
+ * Pointers need the alignment of their elements only.  Scratch comes in through `workspace`, at
+ * least disco_orthogonalize_workspace_size bytes for the same n, groups, rows and cols, 256-byte
+ * aligned.  Both calls are asynchronous on `stream`, allocate nothing and give the same bits every
+ * time.  Errors: DISCO_ERR_INVALID_ARG for a non-positive size, a NULL pointer or one off its
+ * element's alignment, an unknown dtype, steps outside 1..32, a coefficient that is not finite or
+ * above 32 in magnitude, eps not positive, a scalar that is not finite, momentum outside [0, 1),
+ * or a missing or short workspace; DISCO_ERR_UNSUPPORTED for n * groups above 65535 or a matrix
+ * side above 32768; DISCO_ERR_CUDA for a failed launch. */
+typedef struct {
+  int steps;
+  double a, b, c;
+  double eps;
+} disco_newton_schulz_t;
+disco_status disco_orthogonalize_workspace_size(int n, int groups, int rows, int cols, size_t* bytes);
+disco_status disco_orthogonalize(int n, int groups, int rows, int cols, disco_dtype dtype,
+                                 const disco_newton_schulz_t* ns, const void* const* update, void* const* out,
+                                 void* workspace, size_t ws_bytes, void* stream);
+disco_status disco_muon(int n, int groups, int rows, int cols, disco_dtype dtype, const disco_newton_schulz_t* ns,
+                        double lr, double momentum, int nesterov, double weight_decay, const void* const* w,
+                        const void* const* grad, const float* const* m, void* const* w_out, float* const* m_out,
+                        void* workspace, size_t ws_bytes, void* stream);
+
 /* Weight gradient that allocates nothing (the pages have no counterpart to this entry point).
  *
  * disco_bwd_weight needs a caller-provided workspace for its split-K partial sums.  Some

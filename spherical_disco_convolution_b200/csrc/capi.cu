@@ -15,7 +15,9 @@
 #include "../../include/disco.h"
 #include "gather_common.cuh"
 #include "kernels.h"
+#include "muon.h"
 #include "psi_builder.h"
+#include "status.h"
 
 namespace disco {
 namespace {
@@ -36,6 +38,13 @@ disco_status fail(disco_status s, const std::string& msg) {
 disco_status cuda_fail(cudaError_t e, const char* where) {
   return fail(DISCO_ERR_CUDA, std::string(where) + ": " + cudaGetErrorString(e));
 }
+
+}  // namespace
+
+disco_status disco::set_error(disco_status s, const char* msg) { return fail(s, msg); }
+disco_status disco::set_cuda_error(cudaError_t e, const char* where) { return cuda_fail(e, where); }
+
+namespace {
 
 struct DevPlan {
   disco::RowPlan* rows = nullptr;
@@ -783,7 +792,7 @@ disco_status disco_sync_status(void* stream) {
   cudaError_t e = cudaStreamSynchronize(static_cast<cudaStream_t>(stream));
   if (e != cudaSuccess) return cuda_fail(e, "stream synchronisation");
   if (disco::take_mix_tc_status() | disco::take_fused_tc_status() | disco::take_contract_tc_status() |
-      disco::take_contract_ring_status() | disco::take_contract_ring2_status())
+      disco::take_contract_ring_status() | disco::take_contract_ring2_status() | disco::take_muon_status())
     return fail(DISCO_ERR_TIMEOUT, "a bounded device-side wait expired");
   return DISCO_OK;
 }

@@ -1,0 +1,509 @@
+// The orthogonalised update of weights: Newton-Schulz products on tensor cores.
+//
+// For each (rows x cols) matrix U of a call (transposed if rows > cols, so that R <= L):
+//   X = U / (|U|_F + eps), then `steps` times
+//   A = X X^T,  B = a I + b A + c A A,  X <- B X
+// which is the odd polynomial a s + b s^3 + c s^5 on each singular value s.
+//
+// Numbers.  A small singular value is multiplied by `a` in every step, and a rounding error of X
+// in its direction with it: an X rounded to 8 or 11 bits would leave the weak directions of an
+// update wrong by per cents.  So every matrix is kept as an fp16 pair hi + lo (22 bits) under a
+// power-of-two scale, and a product takes three MMAs, hi hi + hi lo + lo hi; what is left out,
+// lo lo, is below 2^-22.  The two small products go into an accumulator of their own, and no
+// accumulator runs over more than 512 values of a sum of squares (kMaxChain), because the tensor
+// core cuts what it adds instead of rounding it.  Scales: X by 2^12, A by 2^11, B by 2^9, so
+// that |X| <= 16, |A| <= 32, |B| <= 128 stay finite in fp16; lo by 2^11 more, which puts it at hi's
+// size, so that it keeps its bits for entries far below the largest.
+#include <cuda.h>
+#include <cuda_fp16.h>
+
+#include <algorithm>
+
+#include "common.cuh"
+#include "kernels.h"
+#include "muon.h"
+#include "tc_common.cuh"
+
+namespace disco {
+namespace {
+
+constexpr float kSx = 4096.0f, kSa = 2048.0f, kSb = 512.0f, kSl = 2048.0f;
+constexpr int kTile = 128;       // output tile of a product
+constexpr int kBk = 64;          // K values per stage: one 128-byte swizzle row of fp16
+constexpr int kMaxChain = 512;   // K values of one accumulation of X X^T
+constexpr int kStages = 3;
+constexpr uint32_t kOperand = kTile * 128;   // one [128][64] fp16 operand tile, bytes
+constexpr uint32_t kStageBytes = 4 * kOperand;
+constexpr int kTensors = 64;     // tensors of one set of launches (pointers travel as arguments)
+constexpr int kNormBlocks = 32;  // partial sums of squares per matrix, at most
+
+struct Pointers {
+  const void* in[kTensors];
+  const void* w[kTensors];
+  const float* m[kTensors];
+  void* out[kTensors];
+  float* m_out[kTensors];
+};
+
+struct Shape {
+  int groups, rows, cols;
+  int R, L, Rp, Lp;  // iterated matrix (R <= L) and its padded sides, multiples of 128
+  bool tr;           // iterated on the transposed matrix
+  int nm;            // matrices
+};
+
+struct Rule {
+  bool step, nesterov;
+  float momentum, keep, rate;
+};
+
+// hi + lo / kSl = v to 22 bits (v within fp16's range).
+__device__ __forceinline__ void split(float v, __half& hi, __half& lo) {
+  hi = __float2half_rn(v);
+  lo = __float2half_rn((v - __half2float(hi)) * kSl);
+}
+
+__device__ __forceinline__ double warp_sum(double v) {
+#pragma unroll
+  for (int m = 16; m; m >>= 1) v += __shfl_xor_sync(~0u, v, m);
+  return v;
+}
+
+// Sums of squares of a slice of each matrix; for a whole step the momentum is updated on the way.
+// fp64: no update is too large or too small for its square.
+template <typename T>
+__global__ void __launch_bounds__(256) ns_norm_kernel(const __grid_constant__ Pointers p, Shape s, Rule r,
+                                                      double* __restrict__ part) {
+  __shared__ double warps[8];
+  const int mi = blockIdx.y, t = mi / s.groups, g = mi % s.groups;
+  const size_t n = (size_t)s.rows * s.cols, base = g * n;
+  const T* in = static_cast<const T*>(p.in[t]) + base;
+  const float* m = r.step ? p.m[t] + base : nullptr;
+  float* mo = r.step ? p.m_out[t] + base : nullptr;
+  double sum = 0.0;
+  for (size_t i = (size_t)blockIdx.x * 256 + threadIdx.x; i < n; i += (size_t)gridDim.x * 256) {
+    float u = to_f32(in[i]);
+    if (r.step) {
+      const float mv = fmaf(r.momentum, m[i], u);
+      mo[i] = mv;
+      u = r.nesterov ? fmaf(r.momentum, mv, u) : mv;
+    }
+    sum += (double)u * (double)u;
+  }
+  sum = warp_sum(sum);
+  if ((threadIdx.x & 31) == 0) warps[threadIdx.x >> 5] = sum;
+  __syncthreads();
+  if (threadIdx.x == 0) {
+    double v = 0.0;
+    for (int k = 0; k < 8; ++k) v += warps[k];
+    part[(size_t)mi * gridDim.x + blockIdx.x] = v;
+  }
+}
+
+// X = U / (|U|_F + eps) as hi and lo planes [2][nm][Rp][Lp], zero in the padding.
+template <typename T>
+__global__ void __launch_bounds__(256) ns_load_kernel(const __grid_constant__ Pointers p, Shape s, Rule r, double eps,
+                                                      const double* __restrict__ part, int parts,
+                                                      __half* __restrict__ x) {
+  __shared__ float tile[32][33];
+  __shared__ float scale;
+  const int mi = blockIdx.z, t = mi / s.groups, g = mi % s.groups;
+  const int tx = threadIdx.x & 31, ty = threadIdx.x >> 5;
+  if (ty == 0) {
+    double v = 0.0;
+    for (int k = tx; k < parts; k += 32) v += part[(size_t)mi * parts + k];
+    v = warp_sum(v);
+    if (tx == 0) scale = (float)((double)kSx / (sqrt(v) + eps));
+  }
+  const size_t n = (size_t)s.rows * s.cols, base = g * n;
+  const T* in = static_cast<const T*>(p.in[t]) + base;
+  const float* mo = r.step ? p.m_out[t] + base : nullptr;
+  const int l0 = blockIdx.x * 32, r0 = blockIdx.y * 32;
+  // a row of the tile is read along the tensor's columns
+  for (int k = ty; k < 32; k += 8) {
+    const int row = s.tr ? l0 + k : r0 + k, col = s.tr ? r0 + tx : l0 + tx;
+    float u = 0.0f;
+    if (row < s.rows && col < s.cols) {
+      const size_t i = (size_t)row * s.cols + col;
+      u = to_f32(in[i]);
+      if (r.step) u = r.nesterov ? fmaf(r.momentum, mo[i], u) : mo[i];
+    }
+    tile[k][tx] = u;
+  }
+  __syncthreads();
+  const size_t plane = (size_t)s.nm * s.Rp * s.Lp;
+  for (int k = ty; k < 32; k += 8) {
+    const float v = (s.tr ? tile[tx][k] : tile[k][tx]) * scale;
+    __half hi, lo;
+    split(v, hi, lo);
+    const size_t at = ((size_t)mi * s.Rp + r0 + k) * s.Lp + l0 + tx;
+    x[at] = hi;
+    x[plane + at] = lo;
+  }
+}
+
+// ------------------------------------------------------------------ the products
+
+enum Product { kGram, kSquare, kUpdate, kFinal };
+
+struct ProductArgs {
+  Shape s;
+  float a, b, c;
+  int tn, S, chunks, chunk0;  // tiles along N, splits along K, K chunks in all and per split
+  float* part;                // kGram: [S][nm][Rp][Rp]
+  const __half* am;           // kSquare: A planes
+  __half* dst;                // kSquare: B planes, kUpdate: the next X
+  Rule r;
+};
+
+__device__ __forceinline__ uint8_t* align1024(uint8_t* p) {
+  return reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(p) + 1023) & ~uintptr_t(1023));
+}
+
+// Instruction descriptor: fp16 x fp16 -> fp32, M x N, A K-major.
+__host__ __device__ constexpr uint32_t idesc_f16(int M, int N, bool b_mn_major) {
+  return (1u << 4) | ((b_mn_major ? 1u : 0u) << 16) | ((uint32_t)(N >> 3) << 17) | ((uint32_t)(M >> 4) << 24);
+}
+
+__device__ __forceinline__ void load16(const __half* p, float (&v)[16]) {
+  alignas(16) const uint4 q[2] = {reinterpret_cast<const uint4*>(p)[0], reinterpret_cast<const uint4*>(p)[1]};
+  const __half2* h = reinterpret_cast<const __half2*>(q);
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {
+    const float2 f = __half22float2(h[i]);
+    v[2 * i] = f.x;
+    v[2 * i + 1] = f.y;
+  }
+}
+
+// 16 values as hi and lo, 32 bytes of each plane.
+__device__ __forceinline__ void store16(__half* hi, __half* lo, const float (&v)[16]) {
+  alignas(16) __half h[16], l[16];
+#pragma unroll
+  for (int i = 0; i < 16; ++i) split(v[i], h[i], l[i]);
+#pragma unroll
+  for (int i = 0; i < 2; ++i) {
+    reinterpret_cast<uint4*>(hi)[i] = reinterpret_cast<const uint4*>(h)[i];
+    reinterpret_cast<uint4*>(lo)[i] = reinterpret_cast<const uint4*>(l)[i];
+  }
+}
+
+// One 128 x 128 tile of a product of hi + lo matrices: D = P Q^T (kGram, kSquare; both K-major)
+// or D = P Q (kUpdate, kFinal; Q is read as an MN-major operand).  Warp 4 streams the four operand
+// tiles of each K chunk by TMA, warp 5 issues the MMAs, warps 0..3 drain the accumulators (TMEM
+// lane = row of the tile).
+template <typename T, Product MODE>
+__global__ void __launch_bounds__(192, 1) ns_product_kernel(const __grid_constant__ CUtensorMap map_p,
+                                                            const __grid_constant__ CUtensorMap map_q,
+                                                            const __grid_constant__ Pointers ptr,
+                                                            const __grid_constant__ ProductArgs a) {
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* smem = align1024(smem_raw);
+  uint64_t* full = reinterpret_cast<uint64_t*>(smem + kStages * kStageBytes);
+  uint64_t* empty = full + kStages;
+  uint64_t* done = empty + kStages;
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(done + 1);
+  constexpr bool kMn = MODE == kUpdate || MODE == kFinal;
+  const Shape& s = a.s;
+  const int n0 = (blockIdx.x % a.tn) * kTile, m0 = (blockIdx.x / a.tn) * kTile;
+  const int mi = blockIdx.y, split_k = blockIdx.z;
+  const int k_lo = split_k * a.chunk0, k_hi = min(a.chunks, k_lo + a.chunk0);
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+
+  if (threadIdx.x == 0) {
+    tc::prefetch_map(&map_p);
+    tc::prefetch_map(&map_q);
+    for (int i = 0; i < kStages; ++i) {
+      tc::mbar_init(&full[i], 1);
+      tc::mbar_init(&empty[i], 1);
+    }
+    tc::mbar_init(done, 1);
+    tc::fence_barrier_init();
+  }
+  if (warp == 5) {
+    tc::tmem_alloc(tmem_slot, 2 * kTile);
+    tc::tmem_relinquish();
+  }
+  tc::fence_before_sync();
+  __syncthreads();
+  tc::fence_after_sync();
+  const uint32_t tmem = *tmem_slot;
+
+  if (warp == 4 && lane == 0) {
+    for (int k = k_lo; k < k_hi; ++k) {
+      const int i = k - k_lo, st = i % kStages;
+      if (i >= kStages && !tc::mbar_wait(&empty[st], ((i / kStages) & 1) ^ 1)) break;
+      uint8_t* base = smem + st * kStageBytes;
+      tc::mbar_arrive_expect_tx(&full[st], kStageBytes);
+#pragma unroll
+      for (int pl = 0; pl < 2; ++pl) {
+        const int z = pl * s.nm + mi;
+        uint8_t* pp = base + pl * kOperand;
+        uint8_t* qq = base + (2 + pl) * kOperand;
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+          tc::tma_load_3d(pp + h * (kOperand / 2), &map_p, &full[st], k * kBk, m0 + 64 * h, z);
+          if (kMn) tc::tma_load_3d(qq + h * (kOperand / 2), &map_q, &full[st], n0 + 64 * h, k * kBk, z);
+          else tc::tma_load_3d(qq + h * (kOperand / 2), &map_q, &full[st], k * kBk, n0 + 64 * h, z);
+        }
+      }
+    }
+  } else if (warp == 5 && lane == 0) {
+    constexpr uint32_t idesc = idesc_f16(kTile, kTile, kMn);
+    for (int k = k_lo; k < k_hi; ++k) {
+      const int i = k - k_lo, st = i % kStages;
+      if (!tc::mbar_wait(&full[st], (i / kStages) & 1)) break;
+      tc::fence_after_sync();
+      const uint32_t p0 = tc::smem_u32(smem + st * kStageBytes), q0 = p0 + 2 * kOperand;
+#pragma unroll
+      for (int kk = 0; kk < kBk / 16; ++kk) {
+        const uint64_t ph = tc::desc_sw128(p0 + kk * 32, 16, 1024);
+        const uint64_t pl = tc::desc_sw128(p0 + kOperand + kk * 32, 16, 1024);
+        const uint64_t qh = kMn ? tc::desc_sw128(q0 + kk * 2048, kOperand / 2, 1024)
+                                : tc::desc_sw128(q0 + kk * 32, 16, 1024);
+        const uint64_t ql = kMn ? tc::desc_sw128(q0 + kOperand + kk * 2048, kOperand / 2, 1024)
+                                : tc::desc_sw128(q0 + kOperand + kk * 32, 16, 1024);
+        const uint32_t more = (i | kk) != 0;
+        tc::mma_bf16(tmem, ph, qh, idesc, more);
+        tc::mma_bf16(tmem + kTile, ph, ql, idesc, more);
+        tc::mma_bf16(tmem + kTile, pl, qh, idesc, 1);
+      }
+      tc::mma_commit(&empty[st]);
+    }
+    tc::mma_commit(done);
+  }
+  __syncwarp();
+  if (warp < 4) {
+    const bool ok = tc::mbar_wait(done, 0);
+    tc::fence_after_sync();
+    const int row = m0 + warp * 32 + lane;
+    const uint32_t tw = tmem + ((uint32_t)(warp * 32) << 16);
+    if (ok) {
+      for (int c = 0; c < kTile; c += 16) {
+        float v[16], e[16];
+        tc::tmem_ld16(tw + c, v);
+        tc::tmem_ld16(tw + kTile + c, e);
+#pragma unroll
+        for (int i = 0; i < 16; ++i) v[i] = fmaf(e[i], 1.0f / kSl, v[i]);
+        const int col = n0 + c;
+        if constexpr (MODE == kGram) {
+          float4* dst = reinterpret_cast<float4*>(a.part + (((size_t)split_k * s.nm + mi) * s.Rp + row) * s.Rp + col);
+#pragma unroll
+          for (int i = 0; i < 4; ++i) dst[i] = make_float4(v[4 * i], v[4 * i + 1], v[4 * i + 2], v[4 * i + 3]);
+        } else if constexpr (MODE == kSquare) {
+          const size_t plane = (size_t)s.nm * s.Rp * s.Rp, at = ((size_t)mi * s.Rp + row) * s.Rp + col;
+          float ah[16], al[16];
+          load16(a.am + at, ah);
+          load16(a.am + plane + at, al);
+#pragma unroll
+          for (int i = 0; i < 16; ++i) {
+            const float av = fmaf(al[i], 1.0f / kSl, ah[i]) * (1.0f / kSa);
+            v[i] = kSb * fmaf(a.c, v[i] * (1.0f / (kSa * kSa)), fmaf(a.b, av, row == col + i ? a.a : 0.0f));
+          }
+          store16(a.dst + at, a.dst + plane + at, v);
+        } else if constexpr (MODE == kUpdate) {
+          const size_t plane = (size_t)s.nm * s.Rp * s.Lp, at = ((size_t)mi * s.Rp + row) * s.Lp + col;
+#pragma unroll
+          for (int i = 0; i < 16; ++i) v[i] *= 1.0f / kSb;
+          store16(a.dst + at, a.dst + plane + at, v);
+        } else {
+          const int t = mi / s.groups;
+          const size_t base = (size_t)(mi % s.groups) * s.rows * s.cols;
+          T* out = static_cast<T*>(ptr.out[t]) + base;
+          const T* w = a.r.step ? static_cast<const T*>(ptr.w[t]) + base : nullptr;
+#pragma unroll
+          for (int i = 0; i < 16; ++i) {
+            if (row >= s.R || col + i >= s.L) continue;
+            const size_t at = s.tr ? (size_t)(col + i) * s.cols + row : (size_t)row * s.cols + col + i;
+            float o = v[i] * (1.0f / (kSb * kSx));
+            if (a.r.step) o = fmaf(a.r.keep, to_f32(w[at]), -a.r.rate * o);
+            out[at] = from_f32<T>(o);
+          }
+        }
+      }
+    }
+    tc::fence_before_sync();
+  }
+  __syncthreads();
+  if (warp == 5) tc::tmem_dealloc(tmem, 2 * kTile);
+}
+
+// A from the partial products of X X^T, in a fixed order.
+__global__ void __launch_bounds__(256) ns_reduce_kernel(const float* __restrict__ part, int S, size_t n,
+                                                        __half* __restrict__ am) {
+  const size_t i = ((size_t)blockIdx.x * 256 + threadIdx.x) * 4;
+  if (i >= n) return;
+  float4 v = *reinterpret_cast<const float4*>(part + i);
+  for (int k = 1; k < S; ++k) {
+    const float4 q = *reinterpret_cast<const float4*>(part + k * n + i);
+    v.x += q.x;
+    v.y += q.y;
+    v.z += q.z;
+    v.w += q.w;
+  }
+  const float f[4] = {v.x, v.y, v.z, v.w};
+  alignas(8) __half h[4], l[4];
+#pragma unroll
+  for (int k = 0; k < 4; ++k) split(f[k] * (kSa / (kSx * kSx)), h[k], l[k]);
+  *reinterpret_cast<uint2*>(am + i) = *reinterpret_cast<const uint2*>(h);
+  *reinterpret_cast<uint2*>(am + n + i) = *reinterpret_cast<const uint2*>(l);
+}
+
+// ------------------------------------------------------------------ host side
+
+int up(int v, int to) { return (v + to - 1) / to * to; }
+
+Shape shape_of(int n, int groups, int rows, int cols) {
+  Shape s{};
+  s.groups = groups;
+  s.rows = rows;
+  s.cols = cols;
+  s.tr = rows > cols;
+  s.R = std::min(rows, cols);
+  s.L = std::max(rows, cols);
+  s.Rp = up(s.R, kTile);
+  s.Lp = up(s.L, kTile);
+  s.nm = n * groups;
+  return s;
+}
+
+int splits_of(const Shape& s) { return (s.Lp + kMaxChain - 1) / kMaxChain; }
+
+size_t align256(size_t v) { return (v + 255) & ~size_t(255); }
+
+struct Layout {
+  size_t x[2], a, b, part, norm, total;
+};
+
+Layout layout_of(const Shape& s) {
+  Layout l{};
+  size_t at = 0;
+  auto take = [&](size_t bytes) {
+    const size_t r = at;
+    at += align256(bytes);
+    return r;
+  };
+  const size_t nx = (size_t)s.nm * s.Rp * s.Lp, na = (size_t)s.nm * s.Rp * s.Rp;
+  l.x[0] = take(4 * nx);
+  l.x[1] = take(4 * nx);
+  l.a = take(4 * na);
+  l.b = take(4 * na);
+  l.part = take(4 * na * splits_of(s));
+  l.norm = take(sizeof(double) * s.nm * kNormBlocks);
+  l.total = at;
+  return l;
+}
+
+// fp16 map of [z][rows][cols] with boxes of 64 x 64.
+bool plane_map(CUtensorMap* m, const void* base, int cols, int rows, int z) {
+  tc::EncodeTiledFn f = tc::encode_tiled_fn();
+  if (!f) return false;
+  const cuuint64_t dims[3] = {(cuuint64_t)cols, (cuuint64_t)rows, (cuuint64_t)z};
+  const cuuint64_t strides[2] = {(cuuint64_t)cols * 2, (cuuint64_t)cols * rows * 2};
+  const cuuint32_t box[3] = {64, 64, 1}, es[3] = {1, 1, 1};
+  return f(m, CU_TENSOR_MAP_DATA_TYPE_FLOAT16, 3, const_cast<void*>(base), dims, strides, box, es,
+           CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+           CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+constexpr size_t kProductSmem = kStages * kStageBytes + 1024 + 128;
+
+template <typename T, Product MODE>
+cudaError_t product(const CUtensorMap& p, const CUtensorMap& q, const Pointers& ptr, const ProductArgs& a,
+                    cudaStream_t st) {
+  auto k = ns_product_kernel<T, MODE>;
+  cudaError_t e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kProductSmem);
+  if (e != cudaSuccess) return e;
+  k<<<dim3(a.s.Rp / kTile * a.tn, a.s.nm, a.S), 192, kProductSmem, st>>>(p, q, ptr, a);
+  count_launch();
+  return cudaGetLastError();
+}
+
+template <typename T>
+cudaError_t run_chunk(const MuonArgs& a, int t0, int n, char* ws, cudaStream_t st) {
+  const Shape s = shape_of(n, a.groups, a.rows, a.cols);
+  const Layout l = layout_of(s);
+  Pointers ptr{};
+  for (int i = 0; i < n; ++i) {
+    ptr.in[i] = a.in[t0 + i];
+    ptr.out[i] = a.out[t0 + i];
+    if (a.step) {
+      ptr.w[i] = a.w[t0 + i];
+      ptr.m[i] = a.m[t0 + i];
+      ptr.m_out[i] = a.m_out[t0 + i];
+    }
+  }
+  Rule r{a.step, a.nesterov, a.momentum, a.keep, a.rate};
+  __half* x[2] = {reinterpret_cast<__half*>(ws + l.x[0]), reinterpret_cast<__half*>(ws + l.x[1])};
+  __half* am = reinterpret_cast<__half*>(ws + l.a);
+  __half* bm = reinterpret_cast<__half*>(ws + l.b);
+  float* part = reinterpret_cast<float*>(ws + l.part);
+  double* norm = reinterpret_cast<double*>(ws + l.norm);
+  CUtensorMap mx[2], ma, mb;
+  if (!plane_map(&mx[0], x[0], s.Lp, s.Rp, 2 * s.nm) || !plane_map(&mx[1], x[1], s.Lp, s.Rp, 2 * s.nm) ||
+      !plane_map(&ma, am, s.Rp, s.Rp, 2 * s.nm) || !plane_map(&mb, bm, s.Rp, s.Rp, 2 * s.nm))
+    return cudaErrorInvalidValue;
+  cudaError_t e;
+  const int blocks = (int)std::min<size_t>(kNormBlocks, ((size_t)a.rows * a.cols + 1023) / 1024);
+  ns_norm_kernel<T><<<dim3(blocks, s.nm), 256, 0, st>>>(ptr, s, r, norm);
+  count_launch();
+  if ((e = cudaGetLastError()) != cudaSuccess) return e;
+  ns_load_kernel<T><<<dim3(s.Lp / 32, s.Rp / 32, s.nm), 256, 0, st>>>(ptr, s, r, a.eps, norm, blocks, x[0]);
+  count_launch();
+  if ((e = cudaGetLastError()) != cudaSuccess) return e;
+  const int S = splits_of(s);
+  const size_t na = (size_t)s.nm * s.Rp * s.Rp;
+  ProductArgs g{};
+  g.s = s;
+  g.a = a.a;
+  g.b = a.b;
+  g.c = a.c;
+  g.r = r;
+  for (int k = 0; k < a.steps; ++k) {
+    const int now = k & 1;
+    g.part = part;
+    g.tn = s.Rp / kTile;
+    g.chunks = s.Lp / kBk;
+    g.chunk0 = kMaxChain / kBk;
+    g.S = S;
+    if ((e = product<T, kGram>(mx[now], mx[now], ptr, g, st)) != cudaSuccess) return e;
+    ns_reduce_kernel<<<(unsigned)((na / 4 + 255) / 256), 256, 0, st>>>(part, S, na, am);
+    count_launch();
+    if ((e = cudaGetLastError()) != cudaSuccess) return e;
+    g.S = 1;
+    g.chunks = g.chunk0 = s.Rp / kBk;
+    g.am = am;
+    g.dst = bm;
+    if ((e = product<T, kSquare>(ma, ma, ptr, g, st)) != cudaSuccess) return e;
+    g.tn = s.Lp / kTile;
+    g.dst = x[now ^ 1];
+    e = k + 1 < a.steps ? product<T, kUpdate>(mb, mx[now], ptr, g, st) : product<T, kFinal>(mb, mx[now], ptr, g, st);
+    if (e != cudaSuccess) return e;
+  }
+  return cudaSuccess;
+}
+
+}  // namespace
+
+size_t muon_workspace(int n, int groups, int rows, int cols) {
+  return layout_of(shape_of(std::min(n, kTensors), groups, rows, cols)).total;
+}
+
+cudaError_t launch_muon(const MuonArgs& a, void* workspace, cudaStream_t st) {
+  for (int t0 = 0; t0 < a.n; t0 += kTensors) {
+    const int n = std::min(kTensors, a.n - t0);
+    char* ws = static_cast<char*>(workspace);
+    cudaError_t e = a.bf16 ? run_chunk<__nv_bfloat16>(a, t0, n, ws, st) : run_chunk<float>(a, t0, n, ws, st);
+    if (e != cudaSuccess) return e;
+  }
+  return cudaSuccess;
+}
+
+int take_muon_status() {
+  int v = 0, z = 0;
+  cudaMemcpyFromSymbol(&v, g_device_status, sizeof(int));
+  if (v) cudaMemcpyToSymbol(g_device_status, &z, sizeof(int));
+  return v;
+}
+
+}  // namespace disco

@@ -65,6 +65,11 @@ class disco_spec_t(ctypes.Structure):
     ]
 
 
+class disco_newton_schulz_t(ctypes.Structure):
+    _fields_ = [("steps", ctypes.c_int), ("a", ctypes.c_double), ("b", ctypes.c_double), ("c", ctypes.c_double),
+                ("eps", ctypes.c_double)]
+
+
 def make_spec(nlat_in, nlon_in, nlat_out, nlon_out, kernel_shape, theta_cutoff,
               grid_in=DISCO_GRID_EQUIANGULAR, grid_out=DISCO_GRID_EQUIANGULAR,
               basis_type=DISCO_BASIS_PIECEWISE_LINEAR, basis_norm_mode=DISCO_NORM_NODAL) -> disco_spec_t:
@@ -87,6 +92,7 @@ def _load():
     P, I, LL, Z = ctypes.c_void_p, ctypes.c_int, ctypes.c_longlong, ctypes.c_size_t
     IP = ctypes.POINTER(ctypes.c_int)
     DP = ctypes.POINTER(ctypes.c_double)
+    PP = ctypes.POINTER(ctypes.c_void_p)
     sig = {
         "disco_psi_build": [ctypes.POINTER(disco_spec_t), I, ctypes.POINTER(P)],
         "disco_psi_build_band": [ctypes.POINTER(disco_spec_t), I, I, I, ctypes.POINTER(P), IP, IP],
@@ -108,6 +114,13 @@ def _load():
         "disco_mix": [I, I, I, I, I, LL, I, P, P, P, P, P],
         "disco_mix_adjoint": [I, I, I, I, I, LL, I, P, P, P, P, Z, P],
         "disco_mix_weight": [I, I, I, I, I, LL, I, P, P, P, P, P, Z, P],
+        "disco_norm_workspace_size": [I, I, LL, I, ctypes.POINTER(Z)],
+        "disco_norm": [I, I, LL, I, P, P, P, ctypes.c_double, P, P, P],
+        "disco_norm_backward": [I, I, LL, I, P, P, P, P, P, P, P, P, Z, P],
+        "disco_orthogonalize_workspace_size": [I, I, I, I, ctypes.POINTER(Z)],
+        "disco_orthogonalize": [I, I, I, I, I, ctypes.POINTER(disco_newton_schulz_t), PP, PP, P, Z, P],
+        "disco_muon": [I, I, I, I, I, ctypes.POINTER(disco_newton_schulz_t), ctypes.c_double, ctypes.c_double, I,
+                       ctypes.c_double, PP, PP, PP, PP, PP, P, Z, P],
         "disco_plan_info": [P, I, IP],
         "disco_sync_status": [P],
         "disco_wait_selftest": [ctypes.c_uint, P],
@@ -357,3 +370,47 @@ def disco_mix_weight(B, C_in, C_out, groups, K, npts, dtype, dout, y, dw, dbias,
                      stream) -> None:
     _check(_lib.disco_mix_weight(B, C_in, C_out, groups, K, npts, dtype, dout, y, dw, dbias, workspace, ws_bytes,
                                  stream))
+
+
+def disco_norm_workspace_size(B, C, npts, dtype) -> int:
+    n = ctypes.c_size_t()
+    _check(_lib.disco_norm_workspace_size(B, C, npts, dtype, ctypes.byref(n)))
+    return n.value
+
+
+def disco_norm(B, C, npts, dtype, x, gain, bias, eps, out, stats, stream) -> None:
+    _check(_lib.disco_norm(B, C, npts, dtype, x, gain, bias, eps, out, stats, stream))
+
+
+def disco_norm_backward(B, C, npts, dtype, dout, x, stats, gain, dx, dgain, dbias, workspace, ws_bytes,
+                        stream) -> None:
+    _check(_lib.disco_norm_backward(B, C, npts, dtype, dout, x, stats, gain, dx, dgain, dbias, workspace, ws_bytes,
+                                    stream))
+
+
+def newton_schulz(steps, coefficients, eps) -> disco_newton_schulz_t:
+    return disco_newton_schulz_t(steps, *(float(v) for v in coefficients), float(eps))
+
+
+def _pointers(ps):
+    return (ctypes.c_void_p * len(ps))(*ps)
+
+
+def disco_orthogonalize_workspace_size(n, groups, rows, cols) -> int:
+    size = ctypes.c_size_t()
+    _check(_lib.disco_orthogonalize_workspace_size(n, groups, rows, cols, ctypes.byref(size)))
+    return size.value
+
+
+def disco_orthogonalize(groups, rows, cols, dtype, ns, update, out, workspace, ws_bytes, stream) -> None:
+    """update and out: lists of n device pointers."""
+    _check(_lib.disco_orthogonalize(len(update), groups, rows, cols, dtype, ctypes.byref(ns), _pointers(update),
+                                    _pointers(out), workspace, ws_bytes, stream))
+
+
+def disco_muon(groups, rows, cols, dtype, ns, lr, momentum, nesterov, weight_decay, w, grad, m, w_out, m_out,
+               workspace, ws_bytes, stream) -> None:
+    """w, grad, m, w_out and m_out: lists of n device pointers."""
+    _check(_lib.disco_muon(len(w), groups, rows, cols, dtype, ctypes.byref(ns), lr, momentum, int(nesterov),
+                           weight_decay, _pointers(w), _pointers(grad), _pointers(m), _pointers(w_out),
+                           _pointers(m_out), workspace, ws_bytes, stream))

@@ -1,0 +1,155 @@
+"""The Muon update of the layers' weights, on the libdisco C ABI.
+
+A weight of a DISCO layer is (C_out, C_in / groups, K); the rows of one group are one matrix of
+C_out / groups rows and C_in / groups * K columns, and the update of each matrix is made nearly
+orthogonal by Newton-Schulz products before it is applied (K. Jordan et al., "Muon: an optimizer
+for hidden layers in neural networks", 2024).  Any tensor of two or more axes works the same way,
+its first axis the rows.  Everything runs in libdisco's CUDA kernels (there is no CPU path), for
+all tensors of one shape together.  fp32 or bf16; momentum is always fp32.
+"""
+
+from __future__ import annotations
+
+import torch
+
+from . import disco as D
+from .conv import _dtype_code, _need_cuda, _ptr, _shape, _stream
+
+COEFFICIENTS = (3.4445, -4.7750, 2.0315)
+
+
+def _matrix(t, groups):
+    if t.dim() < 2 or t.numel() == 0:
+        raise ValueError(f"a tensor of shape {tuple(t.shape)} is no matrix: two axes or more, none empty")
+    if groups <= 0 or t.shape[0] % groups:
+        raise ValueError(f"groups={groups} must divide the first axis, {t.shape[0]}")
+    return t.shape[0] // groups, t.numel() // t.shape[0]
+
+
+def _as_list(ts, what):
+    if isinstance(ts, torch.Tensor):
+        return [ts], True
+    ts = list(ts)
+    if not ts:
+        raise ValueError(f"{what} is an empty list")
+    return ts, False
+
+
+def _buckets(ts):
+    """Indices of the tensors that one call can take together."""
+    by = {}
+    for i, t in enumerate(ts):
+        by.setdefault((tuple(t.shape), t.dtype, t.device), []).append(i)
+    return by.values()
+
+
+def _workspace(n, groups, rows, cols, device):
+    nb = D.disco_orthogonalize_workspace_size(n, groups, rows, cols)
+    return torch.empty(nb, dtype=torch.uint8, device=device), nb
+
+
+def orthogonalize(update, groups: int = 1, steps: int = 5, coefficients=COEFFICIENTS, eps: float = 1e-7):
+    """The nearly orthogonal factor of each group's matrix of `update` (one tensor, or a list):
+    X = U / (|U| + eps), then `steps` times X <- a X + b (X X^T) X + c (X X^T)^2 X."""
+    ts, single = _as_list(update, "update")
+    for t in ts:
+        _need_cuda(t)
+        _matrix(t, groups)
+        _dtype_code(t)
+    ns = D.newton_schulz(steps, coefficients, eps)
+    outs = [torch.empty_like(t, requires_grad=False) for t in ts]
+    for at in _buckets(ts):
+        first = ts[at[0]]
+        rows, cols = _matrix(first, groups)
+        ws, nb = _workspace(len(at), groups, rows, cols, first.device)
+        with torch.cuda.device(first.device):
+            D.disco_orthogonalize(groups, rows, cols, _dtype_code(first), ns, [_ptr(ts[i]) for i in at],
+                                  [_ptr(outs[i]) for i in at], _ptr(ws), nb, _stream(first.device))
+    return outs[0] if single else outs
+
+
+def muon_update(weight, grad, momentum_buffer, lr: float, momentum: float = 0.95, nesterov: bool = True,
+                weight_decay: float = 0.0, groups: int = 1, steps: int = 5, coefficients=COEFFICIENTS,
+                eps: float = 1e-7, inplace: bool = False):
+    """(weight', momentum_buffer') of one step (one tensor each, or lists of equal length):
+    m' = momentum * m + grad, U = grad + momentum * m' (nesterov) or m', and
+    w' = (1 - lr * weight_decay) * w - lr * sqrt(max(1, rows / cols)) * orthogonalize(U).
+    momentum_buffer is fp32.  inplace writes both results into the tensors given."""
+    ws_, single = _as_list(weight, "weight")
+    gs, _ = _as_list(grad, "grad")
+    ms, _ = _as_list(momentum_buffer, "momentum_buffer")
+    if not len(ws_) == len(gs) == len(ms):
+        raise ValueError(f"{len(ws_)} weights, {len(gs)} gradients and {len(ms)} momentum buffers")
+    for w, g, m in zip(ws_, gs, ms):
+        _need_cuda(w, g)
+        _need_cuda(m)
+        _matrix(w, groups)
+        _dtype_code(w)
+        _shape(g, w.shape, "grad")
+        _shape(m, w.shape, "momentum_buffer")
+        if m.dtype != torch.float32:
+            raise TypeError(f"momentum_buffer is float32, not {m.dtype}")
+        if not w.device == g.device == m.device:
+            raise ValueError("weight, grad and momentum_buffer lie on different devices")
+    if inplace and len({_ptr(t) for t in ws_ + ms}) < 2 * len(ws_):
+        raise ValueError("a tensor is given twice: each is updated once")
+    ns = D.newton_schulz(steps, coefficients, eps)
+    w_out = ws_ if inplace else [torch.empty_like(t, requires_grad=False) for t in ws_]
+    m_out = ms if inplace else [torch.empty_like(t, requires_grad=False) for t in ms]
+    for at in _buckets(ws_):
+        first = ws_[at[0]]
+        rows, cols = _matrix(first, groups)
+        ws, nb = _workspace(len(at), groups, rows, cols, first.device)
+        ptrs = [[_ptr(ts[i]) for i in at] for ts in (ws_, gs, ms, w_out, m_out)]
+        with torch.cuda.device(first.device):
+            D.disco_muon(groups, rows, cols, _dtype_code(first), ns, float(lr), float(momentum), nesterov,
+                         float(weight_decay), *ptrs, _ptr(ws), nb, _stream(first.device))
+    return (w_out[0], m_out[0]) if single else (w_out, m_out)
+
+
+class Muon(torch.optim.Optimizer):
+    """Muon for the weights of DISCO layers (and other parameters of two or more axes).
+
+    A parameter group may set `groups` to its layers' group count.  Vectors (biases, norms) belong
+    to another optimizer.  The rate and the other scalars are read at every step, and become
+    constants of a CUDA graph that captures it."""
+
+    def __init__(self, params, lr: float = 0.02, momentum: float = 0.95, nesterov: bool = True,
+                 weight_decay: float = 0.0, groups: int = 1, steps: int = 5, coefficients=COEFFICIENTS,
+                 eps: float = 1e-7):
+        super().__init__(params, dict(lr=lr, momentum=momentum, nesterov=nesterov, weight_decay=weight_decay,
+                                      groups=groups, steps=steps, coefficients=tuple(coefficients), eps=eps))
+        for group in self.param_groups:
+            for p in group["params"]:
+                _matrix(p, group["groups"])
+                _dtype_code(p)
+                if not p.is_contiguous():
+                    raise ValueError("Muon takes contiguous parameters")
+
+    @torch.no_grad()
+    def step(self, closure=None):
+        loss = None
+        if closure is not None:
+            with torch.enable_grad():
+                loss = closure()
+        for group in self.param_groups:
+            ps = [p for p in group["params"] if p.grad is not None]
+            if not ps:
+                continue
+            for p in ps:
+                if "momentum_buffer" not in self.state[p]:
+                    self.state[p]["momentum_buffer"] = torch.zeros_like(p, dtype=torch.float32)
+            muon_update(ps, [p.grad.contiguous() for p in ps], [self.state[p]["momentum_buffer"] for p in ps],
+                        group["lr"], group["momentum"], group["nesterov"], group["weight_decay"], group["groups"],
+                        group["steps"], group["coefficients"], group["eps"], inplace=True)
+        return loss
+
+    def load_state_dict(self, state_dict):
+        super().load_state_dict(state_dict)
+        # the base class casts state to the parameter's type; momentum stays fp32
+        ids = [i for g in state_dict["param_groups"] for i in g["params"]]
+        params = [p for g in self.param_groups for p in g["params"]]
+        for i, p in zip(ids, params):
+            saved = state_dict["state"].get(i, {}).get("momentum_buffer")
+            if saved is not None:
+                self.state[p]["momentum_buffer"] = saved.detach().to(device=p.device, dtype=torch.float32, copy=True)

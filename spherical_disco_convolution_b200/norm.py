@@ -1,0 +1,117 @@
+"""Layer norm of a field over its channels, on the libdisco C ABI.
+
+The norm between two DISCO layers: the field is (B, C, nlat, nlon), as the convolution takes and
+gives it, and every grid point is normalised over its C channels.  Everything runs in libdisco's
+CUDA kernels (there is no CPU path); PyTorch supplies memory, streams and autograd bookkeeping.
+fp32 or bf16, all tensors of a call in one type; statistics and sums are fp32.
+"""
+
+from __future__ import annotations
+
+import math
+
+import torch
+
+from . import disco as D
+from .conv import _dtype_code, _need_cuda, _ptr, _shape, _stream
+
+
+def _one_device(*ts):
+    devs = {t.device for t in ts if t is not None}
+    if len(devs) > 1:
+        raise ValueError(f"tensors on several devices: {sorted(map(str, devs))}")
+
+
+def _field(x):
+    if x.dim() < 2 or x.numel() == 0:
+        raise ValueError(f"x has shape {tuple(x.shape)}, expected (B, C, *points) without an empty axis")
+    return x.shape[0], x.shape[1], math.prod(x.shape[2:])
+
+
+def _stats_shape(x):
+    return (2, x.shape[0]) + tuple(x.shape[2:])
+
+
+def layer_norm(x: torch.Tensor, gain=None, bias=None, eps: float = 1e-5):
+    """(out, stats) of x (B, C, *points): out = gain * (x - mean) * r + bias with mean and r =
+    1 / sqrt(var + eps) over the channels of each point; stats (2, B, *points) holds mean and r in
+    fp32, which layer_norm_backward takes.  gain and bias are (C,), in x's type, or None."""
+    _need_cuda(x, gain, bias)
+    _one_device(x, gain, bias)
+    B, C, n = _field(x)
+    _shape(gain, (C,), "gain")
+    _shape(bias, (C,), "bias")
+    dt = _dtype_code(x)
+    out = torch.empty_like(x)
+    stats = torch.empty(_stats_shape(x), dtype=torch.float32, device=x.device)
+    with torch.cuda.device(x.device):
+        D.disco_norm(B, C, n, dt, _ptr(x), _ptr(gain), _ptr(bias), float(eps), _ptr(out), _ptr(stats),
+                     _stream(x.device))
+    return out, stats
+
+
+def layer_norm_backward(dout: torch.Tensor, x: torch.Tensor, stats: torch.Tensor, gain=None, need_input: bool = True,
+                        need_gain: bool = True, need_bias: bool = True):
+    """(dx, dgain, dbias) of layer_norm from the field it took and the stats it returned; None for
+    each one not needed."""
+    _need_cuda(dout, x, gain)
+    _one_device(dout, x, stats, gain)
+    B, C, n = _field(x)
+    _shape(dout, x.shape, "dout")
+    _shape(gain, (C,), "gain")
+    _shape(stats, _stats_shape(x), "stats")
+    if stats.dtype != torch.float32 or not stats.is_contiguous():
+        raise ValueError("stats is the contiguous fp32 tensor that layer_norm returned")
+    if not (need_input or need_gain or need_bias):
+        return None, None, None
+    dt = _dtype_code(x)
+    dx = torch.empty_like(x) if need_input else None
+    dgain = torch.empty((C,), dtype=x.dtype, device=x.device) if need_gain else None
+    dbias = torch.empty((C,), dtype=x.dtype, device=x.device) if need_bias else None
+    ws, nb = None, 0
+    if need_gain or need_bias:
+        nb = D.disco_norm_workspace_size(B, C, n, dt)
+        ws = torch.empty(nb, dtype=torch.uint8, device=x.device)
+    with torch.cuda.device(x.device):
+        D.disco_norm_backward(B, C, n, dt, _ptr(dout), _ptr(x), _ptr(stats), _ptr(gain), _ptr(dx), _ptr(dgain),
+                              _ptr(dbias), _ptr(ws), nb, _stream(x.device))
+    return dx, dgain, dbias
+
+
+class _LayerNormFn(torch.autograd.Function):
+    @staticmethod
+    def forward(ctx, x, gain, bias, eps):
+        x = x.contiguous()
+        gain = None if gain is None else gain.contiguous()
+        out, stats = layer_norm(x, gain, None if bias is None else bias.contiguous(), eps)
+        ctx.save_for_backward(x, stats, gain)
+        return out
+
+    @staticmethod
+    @torch.autograd.function.once_differentiable
+    def backward(ctx, dout):
+        x, stats, gain = ctx.saved_tensors
+        need = ctx.needs_input_grad
+        return (*layer_norm_backward(dout.contiguous(), x, stats, gain, need[0], need[1], need[2]), None)
+
+
+class LayerNormS2(torch.nn.Module):
+    """Layer norm over the channels of every grid point of a (B, C, nlat, nlon) field.
+
+    On a grid split over ranks each rank norms the points it holds; the gradients of weight and
+    bias are then that rank's share of the sum over points, to be added over the ranks."""
+
+    def __init__(self, channels, eps=1e-5, affine=True, bias=True, device=None, dtype=torch.float32):
+        super().__init__()
+        if channels < 1:
+            raise ValueError(f"channels={channels} must be positive")
+        if dtype not in (torch.float32, torch.bfloat16):
+            raise TypeError(f"unsupported dtype {dtype}; use float32 or bfloat16")
+        self.channels, self.eps = channels, float(eps)
+        self.weight = torch.nn.Parameter(torch.ones(channels, device=device, dtype=dtype)) if affine else None
+        self.bias = torch.nn.Parameter(torch.zeros(channels, device=device, dtype=dtype)) if affine and bias else None
+
+    def forward(self, x):
+        if x.dim() < 2 or x.shape[1] != self.channels:
+            raise ValueError(f"x has shape {tuple(x.shape)}, expected (B, {self.channels}, *points)")
+        return _LayerNormFn.apply(x, self.weight, self.bias, self.eps)
