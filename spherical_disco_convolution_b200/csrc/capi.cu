@@ -16,6 +16,7 @@
 #include "gather_common.cuh"
 #include "kernels.h"
 #include "muon.h"
+#include "norm.h"
 #include "psi_builder.h"
 #include "status.h"
 
@@ -792,7 +793,8 @@ disco_status disco_sync_status(void* stream) {
   cudaError_t e = cudaStreamSynchronize(static_cast<cudaStream_t>(stream));
   if (e != cudaSuccess) return cuda_fail(e, "stream synchronisation");
   if (disco::take_mix_tc_status() | disco::take_fused_tc_status() | disco::take_contract_tc_status() |
-      disco::take_contract_ring_status() | disco::take_contract_ring2_status() | disco::take_muon_status())
+      disco::take_contract_ring_status() | disco::take_contract_ring2_status() | disco::take_muon_status() |
+      disco::take_norm_status())
     return fail(DISCO_ERR_TIMEOUT, "a bounded device-side wait expired");
   return DISCO_OK;
 }

@@ -513,6 +513,14 @@ cudaError_t fwd(const Plan& p, const NormArgs& a, cudaStream_t st) {
   return cudaGetLastError();
 }
 
+template <typename T>
+cudaError_t reduce(const NormArgs& a, int rows, cudaStream_t st) {
+  norm_reduce_kernel<T><<<(2 * a.C + 31) / 32, dim3(32, 32), 0, st>>>(a.part, rows, a.C, static_cast<T*>(a.dgain),
+                                                                      static_cast<T*>(a.dbias));
+  count_launch();
+  return cudaGetLastError();
+}
+
 template <typename T, int VEC, int NC>
 cudaError_t bwd(const Plan& p, const NormArgs& a, int rows, cudaStream_t st) {
   const size_t smem = p.red * sizeof(float2) + (NC == 0 ? 2 * (size_t)p.g.C * sizeof(float) : 0);
@@ -527,10 +535,7 @@ cudaError_t bwd(const Plan& p, const NormArgs& a, int rows, cudaStream_t st) {
   count_launch();
   cudaError_t e = cudaGetLastError();
   if (e != cudaSuccess || !(a.dgain || a.dbias)) return e;
-  norm_reduce_kernel<T><<<(2 * a.C + 31) / 32, dim3(32, 32), 0, st>>>(a.part, rows, a.C, static_cast<T*>(a.dgain),
-                                                                      static_cast<T*>(a.dbias));
-  count_launch();
-  return cudaGetLastError();
+  return reduce<T>(a, rows, st);
 }
 
 template <typename T, int VEC>
@@ -560,6 +565,9 @@ cudaError_t pick_bwd(const Plan& p, const NormArgs& a, int rows, cudaStream_t st
 int norm_partials(int sms) { return sms * kBwdCtasPerSm; }
 
 cudaError_t launch_norm(bool bf16, const NormArgs& a, int sms, cudaStream_t st) {
+  int r = 0;
+  cudaError_t err;
+  if (launch_norm_ring(bf16, a, false, sms, st, &r, &err)) return err;
   const int es = bf16 ? 2 : 4;
   const int vec = vec_of(es, a.npts, {a.x, a.out});
   const Plan p = plan_of(es, vec, a.B, a.C, a.npts, sms);
@@ -579,6 +587,12 @@ cudaError_t launch_norm(bool bf16, const NormArgs& a, int sms, cudaStream_t st) 
 }
 
 cudaError_t launch_norm_backward(bool bf16, const NormArgs& a, int sms, cudaStream_t st) {
+  int r = 0;
+  cudaError_t err;
+  if (launch_norm_ring(bf16, a, true, sms, st, &r, &err)) {
+    if (err != cudaSuccess || !(a.dgain || a.dbias)) return err;
+    return bf16 ? reduce<__nv_bfloat16>(a, r, st) : reduce<float>(a, r, st);
+  }
   const int es = bf16 ? 2 : 4;
   const int vec = vec_of(es, a.npts, {a.x, a.dout, a.dx});
   const Plan p = plan_of(es, vec, a.B, a.C, a.npts, sms);
