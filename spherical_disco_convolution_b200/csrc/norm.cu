@@ -562,8 +562,6 @@ cudaError_t pick_bwd(const Plan& p, const NormArgs& a, int rows, cudaStream_t st
 
 }  // namespace
 
-int norm_partials(int sms) { return sms * kBwdCtasPerSm; }
-
 cudaError_t launch_norm(bool bf16, const NormArgs& a, int sms, cudaStream_t st) {
   int r = 0;
   cudaError_t err;
@@ -596,7 +594,7 @@ cudaError_t launch_norm_backward(bool bf16, const NormArgs& a, int sms, cudaStre
   const int es = bf16 ? 2 : 4;
   const int vec = vec_of(es, a.npts, {a.x, a.dout, a.dx});
   const Plan p = plan_of(es, vec, a.B, a.C, a.npts, sms);
-  const int rows = (int)std::min<long long>(p.tiles, norm_partials(sms));
+  const int rows = (int)std::min<long long>(p.tiles, (long long)kBwdCtasPerSm * sms);
   if (bf16) {
     switch (vec) {
       case 8: return pick_bwd<__nv_bfloat16, 8>(p, a, rows, st);

@@ -2,21 +2,24 @@
 // shared memory.  Formulas and sums as in norm.cu.
 //
 // What bounds both passes is HBM, and what kept the register form below it was latency: its
-// loads are only in flight between two barriers of a CTA.  Here the ring is kept full of
-// tiles of C channels x LPR * VEC points (one TMA box, or one bulk copy per channel row where
-// rows do not start on 16 bytes) while two groups of eight warps take tiles in turn, so that one
-// group computes while the other waits at its barriers.  A tile is read from HBM once and from
-// shared memory twice, for the sums and for the result.  LPR = 32 or 16 lanes take a channel
-// row, VEC points each (16 warps and none besides leave a thread 128 registers: the first warp of
-// the group that has done with a tile loads the next one into its place), so a group has 8 or 16 rows of lanes and row r takes the channels r,
-// r + rows, ...; the sums over channels cross the rows through shared memory.
+// loads are only in flight between two barriers of a CTA.  Here a ring of tiles of C channels x
+// LPR * VEC points is kept full while G groups of W = 8 or 16 warps take the tiles in turn.  A tile
+// is read from HBM once and from shared memory once: its sums are added on the way into registers
+// (at most 32 of packed values a thread), the stage is free for the next tile at once, and the
+// result is formed from the registers after the sums over channels have crossed the group.
+// LPR = 32 or 16 lanes take a channel row, VEC points each, so a group has W or 2 W rows of lanes
+// and row r takes the channels r, r + rows, ....
+//
+// Loads.  GRAN = 16 (every plane starts on 16 bytes): one TMA box of C rows per array, issued by
+// the first warp of the group that has read the stage.  GRAN = 4 or 2 (planes start on any
+// 4 or 2 bytes): every row of lanes copies its own channels' rows of its group's next tile with
+// cp.async, as the 16-byte blocks that hold a value of the row's piece (so a copy may take in up to
+// 15 bytes before and behind it, never a block without a value), and reads them from their own
+// offset, GRAN bytes at a time.  No other warp reads these rows, so they need no barrier.
 //
 // Forward sums in one pass: a row of lanes adds v = x - k and v^2 about the value k of its first
 // channel.  k is one of the n values it adds, so (mean - k)^2 is at most n times their variance and
 // m2 = sum v^2 - (sum v)^2 / n loses at most log2(n) + 1 bits; the rows then combine as in norm.cu.
-//
-// Rows that do not start on 16 bytes: the copy takes every 16-byte block that holds a value of
-// the row's piece, and the row is read from its own offset, one element at a time.
 #include <cuda.h>
 #include <cuda_runtime.h>
 
@@ -30,43 +33,21 @@
 namespace disco {
 namespace {
 
-constexpr int kWarps = 8;                     // of a group
-constexpr int kGroup = kWarps * 32;
-constexpr int kGroups = 2;
-constexpr int kThreads = kGroups * kGroup;
-constexpr int kMaxStages = 8;
-constexpr size_t kRingSmem = 225 * 1024;      // of 227 KB
+constexpr int kThreads = 512;  // 128 registers a thread
+constexpr int kMaxStages = 12;
+constexpr size_t kRingSmem = 225 * 1024;  // of 227 KB
 
-// Two fp32 values in one 64-bit register pair (sm_100's packed fp32 arithmetic).
+// Two fp32 values of neighbouring points.
 struct F2 {
-  unsigned long long v;
+  float x, y;
 };
-__device__ __forceinline__ F2 pack(float a, float b) {
-  F2 r;
-  asm("mov.b64 %0, {%1, %2};" : "=l"(r.v) : "f"(a), "f"(b));
-  return r;
-}
-__device__ __forceinline__ float2 unpack(F2 a) {
-  float2 r;
-  asm("mov.b64 {%0, %1}, %2;" : "=f"(r.x), "=f"(r.y) : "l"(a.v));
-  return r;
-}
-__device__ __forceinline__ F2 add2(F2 a, F2 b) {
-  F2 r;
-  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r.v) : "l"(a.v), "l"(b.v));
-  return r;
-}
-__device__ __forceinline__ F2 mul2(F2 a, F2 b) {
-  F2 r;
-  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r.v) : "l"(a.v), "l"(b.v));
-  return r;
-}
-__device__ __forceinline__ F2 fma2(F2 a, F2 b, F2 c) {
-  F2 r;
-  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r.v) : "l"(a.v), "l"(b.v), "l"(c.v));
-  return r;
-}
-__device__ __forceinline__ F2 neg2(F2 a) { return F2{a.v ^ 0x8000000080000000ull}; }
+__device__ __forceinline__ F2 pack(float a, float b) { return F2{a, b}; }
+__device__ __forceinline__ F2 twice(float a) { return F2{a, a}; }
+__device__ __forceinline__ float2 unpack(F2 a) { return make_float2(a.x, a.y); }
+__device__ __forceinline__ F2 add2(F2 a, F2 b) { return F2{a.x + b.x, a.y + b.y}; }
+__device__ __forceinline__ F2 mul2(F2 a, F2 b) { return F2{a.x * b.x, a.y * b.y}; }
+__device__ __forceinline__ F2 fma2(F2 a, F2 b, F2 c) { return F2{fmaf(a.x, b.x, c.x), fmaf(a.y, b.y, c.y)}; }
+__device__ __forceinline__ F2 neg2(F2 a) { return F2{-a.x, -a.y}; }
 
 struct RingArgs {
   int B, C;
@@ -74,7 +55,7 @@ struct RingArgs {
   int tiles_per_plane;
   long long tiles;
   int stages, stage_bytes;
-  int dout_off, stat_off;      // byte offsets in a stage: dout rows, statistics rows
+  int dout_off, stat_off;      // byte offsets in a stage: dout rows, statistics rows (GRAN 16)
   int boxes, box_rows;         // TMA boxes per array
   const void* x;
   const void* dout;
@@ -87,84 +68,92 @@ struct RingArgs {
   float* part;
 };
 
-// A lane's points of one channel row, as VEC / 2 pairs (VEC = 1: one pair, its upper half 0).
-// SHIFT rows hold point lane + LPR e in element e, others VEC consecutive points.
-template <typename T, int VEC, int LPR, bool SHIFT>
-__device__ __forceinline__ void read_row(const uint8_t* row, int lane, F2 (&v)[(VEC + 1) / 2]) {
-  constexpr int kBytes = VEC * (int)sizeof(T);
-  if constexpr (SHIFT || VEC == 1) {
-    const T* p = reinterpret_cast<const T*>(row) + lane;
-    float f[VEC + 1];
-    f[VEC] = 0.0f;
+// The form of a kernel: its lanes and groups, and which points of the tile a lane's values are.
+// FULL: every row of lanes has exactly NC channels, so no channel needs a guard.
+template <typename T_, int VEC_, int LPR_, int W_, int NC_, int GRAN_, bool FULL_ = false>
+struct Form {
+  using T = T_;
+  static constexpr int VEC = VEC_, LPR = LPR_, W = W_, GRAN = GRAN_;
+  static constexpr int NC = NC_;  // channels per row of lanes, at most
+  static constexpr int kGroup = W * 32, G = kThreads / kGroup;
+  static constexpr int kPts = LPR * VEC, NP = (VEC + 1) / 2;
+  static constexpr int kRows = W * (32 / LPR);
+  static constexpr bool kTma = GRAN == 16, kFull = FULL_;
+  using Filled = Form<T_, VEC_, LPR_, W_, NC_, GRAN_, true>;
+  static constexpr int kWords = VEC * (int)sizeof(T) / 4;  // packed values of a lane and channel
+  // consecutive points a lane reads at once
+  static constexpr int kRun = kTma ? VEC : (GRAN < (int)sizeof(T) ? 1 : GRAN / (int)sizeof(T));
+  static constexpr int kPitch = kPts * (int)sizeof(T) + (kTma ? 0 : 16);
+  // the sums of a point are joined by kJoin lanes; rows of sums are kSumPitch apart, which keeps
+  // those lanes on different banks
+  static constexpr int kJoin = kGroup / kPts, kSumPitch = kPts + 16 / kJoin;
+  static_assert(VEC % kRun == 0 && kJoin >= 1 && kJoin <= 16 && kRows % kJoin == 0, "shape");
+  // the tile's point that value e of a lane is
+  static __device__ __forceinline__ int point(int lane, int e) {
+    return (lane + LPR * (e / kRun)) * kRun + e % kRun;
+  }
+};
+
+template <typename F>
+__device__ __forceinline__ void read_row(const uint8_t* row, int lane, uint32_t (&v)[F::kWords]) {
+  using T = typename F::T;
+  constexpr int kBytes = F::kRun * (int)sizeof(T);
 #pragma unroll
-    for (int e = 0; e < VEC; ++e) f[e] = to_f32(p[LPR * e]);
-#pragma unroll
-    for (int k = 0; k < (VEC + 1) / 2; ++k) v[k] = pack(f[2 * k], f[2 * k + 1]);
-  } else {
-    const uint8_t* p = row + lane * kBytes;
-    uint32_t w[kBytes / 4];
-    if constexpr (kBytes == 4) w[0] = *reinterpret_cast<const uint32_t*>(p);
-    else if constexpr (kBytes == 8) {
+  for (int g = 0; g < F::VEC / F::kRun; ++g) {
+    const uint8_t* p = row + (lane + F::LPR * g) * kBytes;
+    if constexpr (kBytes == 2) {
+      const uint32_t h = *reinterpret_cast<const uint16_t*>(p);
+      if (g % 2 == 0) v[g / 2] = h;
+      else v[g / 2] |= h << 16;
+    } else if constexpr (kBytes == 4) {
+      v[g] = *reinterpret_cast<const uint32_t*>(p);
+    } else if constexpr (kBytes == 8) {
       const uint2 q = *reinterpret_cast<const uint2*>(p);
-      w[0] = q.x;
-      w[1] = q.y;
+      v[0] = q.x;
+      v[1] = q.y;
     } else {
       const uint4 q = *reinterpret_cast<const uint4*>(p);
-      w[0] = q.x;
-      w[1] = q.y;
-      w[2] = q.z;
-      w[3] = q.w;
-    }
-#pragma unroll
-    for (int k = 0; k < VEC / 2; ++k) {
-      if constexpr (sizeof(T) == 2) v[k] = pack(__uint_as_float(w[k] << 16), __uint_as_float(w[k] & 0xffff0000u));
-      else v[k] = pack(__uint_as_float(w[2 * k]), __uint_as_float(w[2 * k + 1]));
+      v[0] = q.x;
+      v[1] = q.y;
+      v[2] = q.z;
+      v[3] = q.w;
     }
   }
 }
 
-template <typename T, int VEC, int LPR, bool SHIFT>
-__device__ __forceinline__ void write_row(T* dst, int lane, int valid, const F2 (&v)[(VEC + 1) / 2]) {
-  constexpr int kBytes = VEC * (int)sizeof(T);
-  float f[VEC + 1];
+// Pair k of a lane's values.
+template <typename F>
+__device__ __forceinline__ F2 pair_of(const uint32_t (&v)[F::kWords], int k) {
+  if constexpr (sizeof(typename F::T) == 2) return pack(__uint_as_float(v[k] << 16), __uint_as_float(v[k] & 0xffff0000u));
+  else if constexpr (F::VEC == 1) return pack(__uint_as_float(v[0]), 0.0f);
+  else return pack(__uint_as_float(v[2 * k]), __uint_as_float(v[2 * k + 1]));
+}
+
+template <typename F>
+__device__ __forceinline__ void write_row(typename F::T* dst, int lane, int valid, const F2 (&v)[F::NP]) {
+  using T = typename F::T;
+  constexpr int kBytes = F::kRun * (int)sizeof(T);
+  uint32_t w[F::kWords];
 #pragma unroll
-  for (int k = 0; k < (VEC + 1) / 2; ++k) {
+  for (int k = 0; k < F::NP; ++k) {
     const float2 q = unpack(v[k]);
-    f[2 * k] = q.x;
-    f[2 * k + 1] = q.y;
-  }
-  if constexpr (SHIFT || VEC == 1) {
-#pragma unroll
-    for (int e = 0; e < VEC; ++e)
-      if (lane + LPR * e < valid) dst[lane + LPR * e] = from_f32<T>(f[e]);
-  } else {
-    if (lane * VEC >= valid) return;
-    uint32_t w[kBytes / 4];
-#pragma unroll
-    for (int k = 0; k < kBytes / 4; ++k) {
-      if constexpr (sizeof(T) == 2) {
-        const __nv_bfloat162 h = __floats2bfloat162_rn(f[2 * k], f[2 * k + 1]);
-        w[k] = *reinterpret_cast<const uint32_t*>(&h);
-      } else {
-        w[k] = __float_as_uint(f[k]);
-      }
+    if constexpr (sizeof(T) == 2) {
+      const __nv_bfloat162 h = __floats2bfloat162_rn(q.x, q.y);
+      w[k] = *reinterpret_cast<const uint32_t*>(&h);
+    } else {
+      w[2 * k] = __float_as_uint(q.x);
+      if constexpr (F::VEC > 1) w[2 * k + 1] = __float_as_uint(q.y);
     }
-    T* p = dst + lane * VEC;
-    if constexpr (kBytes == 4) *reinterpret_cast<uint32_t*>(p) = w[0];
-    else if constexpr (kBytes == 8) *reinterpret_cast<uint2*>(p) = make_uint2(w[0], w[1]);
-    else *reinterpret_cast<uint4*>(p) = make_uint4(w[0], w[1], w[2], w[3]);
   }
-}
-
-template <typename T, int PTS, bool SHIFT>
-constexpr int kPitch = PTS * (int)sizeof(T) + (SHIFT ? 16 : 0);
-template <int PTS, bool SHIFT>
-constexpr int kStatPitch = PTS * 4 + (SHIFT ? 16 : 0);
-
-// Bytes by which element `at` of an array at `base` lies past a 16-byte boundary.
-template <typename T>
-__device__ __forceinline__ uint32_t past16(const T* base, size_t at) {
-  return (uint32_t)(reinterpret_cast<uintptr_t>(base + at) & 15);
+#pragma unroll
+  for (int g = 0; g < F::VEC / F::kRun; ++g) {
+    const int p = (lane + F::LPR * g) * F::kRun;
+    if (p >= valid) continue;  // planes are whole runs long
+    if constexpr (kBytes == 2) *reinterpret_cast<uint16_t*>(dst + p) = (uint16_t)(w[g / 2] >> (16 * (g % 2)));
+    else if constexpr (kBytes == 4) *reinterpret_cast<uint32_t*>(dst + p) = w[g];
+    else if constexpr (kBytes == 8) *reinterpret_cast<uint2*>(dst + p) = make_uint2(w[0], w[1]);
+    else *reinterpret_cast<uint4*>(dst + p) = make_uint4(w[0], w[1], w[2], w[3]);
+  }
 }
 
 struct Ring {
@@ -173,83 +162,88 @@ struct Ring {
   uint64_t* empty;
 };
 
-// One warp: tile k of this CTA into stage k % stages, which is free.
-template <typename T, int kPts, bool SHIFT, bool BWD>
-__device__ __forceinline__ void load_tile(const RingArgs& a, const CUtensorMap* map_x, const CUtensorMap* map_d,
-                                          const Ring& r, int k) {
+struct Tile {
+  int b, p0, valid;
+  size_t at;  // of channel 0
+};
+
+template <typename F>
+__device__ __forceinline__ Tile tile_of(const RingArgs& a, long long tile) {
+  Tile t;
+  t.b = (int)(tile / a.tiles_per_plane);
+  t.p0 = (int)(tile % a.tiles_per_plane) * F::kPts;
+  t.valid = min(F::kPts, a.npts - t.p0);
+  t.at = (size_t)t.b * a.C * a.npts + t.p0;
+  return t;
+}
+
+// GRAN 16, one warp: tile k of this CTA into stage k % stages, which is free.
+template <typename F, bool BWD>
+__device__ __forceinline__ void load_boxes(const RingArgs& a, const CUtensorMap* map_x, const CUtensorMap* map_d,
+                                           const Ring& r, int k) {
   const long long tile = blockIdx.x + (long long)k * gridDim.x;
-  if (tile >= a.tiles) return;
-  const int lane = threadIdx.x & 31, st = k % a.stages;
-  const int b = (int)(tile / a.tiles_per_plane), p0 = (int)(tile % a.tiles_per_plane) * kPts;
-  const int valid = min(kPts, a.npts - p0);
+  if (tile >= a.tiles || (threadIdx.x & 31) != 0) return;
+  const int st = k % a.stages;
+  const Tile t = tile_of<F>(a, tile);
   uint8_t* base = r.stage + (size_t)st * a.stage_bytes;
-  if constexpr (!SHIFT) {
-    if (lane == 0) {
-      const uint32_t rows = (uint32_t)(a.boxes * a.box_rows * kPitch<T, kPts, SHIFT>);
-      tc::mbar_arrive_expect_tx(&r.full[st], BWD ? 2 * rows + 8u * valid : rows);
-      for (int i = 0; i < a.boxes; ++i) {
-        tc::tma_load_3d(base + i * a.box_rows * kPitch<T, kPts, SHIFT>, map_x, &r.full[st], p0, i * a.box_rows, b);
-        if (BWD)
-          tc::tma_load_3d(base + a.dout_off + i * a.box_rows * kPitch<T, kPts, SHIFT>, map_d, &r.full[st], p0,
-                          i * a.box_rows, b);
-      }
-      if (BWD) {
-        const float* s = a.stats_in + (size_t)b * a.npts + p0;
-        tc::bulk_load(base + a.stat_off, s, 4 * valid, &r.full[st]);
-        tc::bulk_load(base + a.stat_off + kStatPitch<kPts, SHIFT>, s + (size_t)a.B * a.npts, 4 * valid, &r.full[st]);
-      }
-    }
-  } else {
-    const int rows = BWD ? 2 * a.C + 2 : a.C;
-    auto piece = [&](int row, const uint8_t** src, uint32_t* bytes, uint8_t** dst) {
-      const uint8_t* from;
-      uint32_t len;
-      if (row < 2 * a.C && (BWD || row < a.C)) {
-        const bool d = row >= a.C;
-        const int c = d ? row - a.C : row;
-        const T* p = static_cast<const T*>(d ? a.dout : a.x) + ((size_t)b * a.C + c) * a.npts + p0;
-        from = reinterpret_cast<const uint8_t*>(p);
-        len = valid * (uint32_t)sizeof(T);
-        *dst = base + (d ? a.dout_off : 0) + c * kPitch<T, kPts, SHIFT>;
-      } else {
-        const int s = row - 2 * a.C;
-        from = reinterpret_cast<const uint8_t*>(a.stats_in + ((size_t)s * a.B + b) * a.npts + p0);
-        len = valid * 4u;
-        *dst = base + a.stat_off + s * kStatPitch<kPts, SHIFT>;
-      }
-      const uint32_t off = (uint32_t)(reinterpret_cast<uintptr_t>(from) & 15);
-      *src = from - off;
-      *bytes = (off + len + 15) & ~15u;
-    };
-    uint32_t total = 0;
-    const uint8_t* src;
-    uint8_t* dst;
-    uint32_t bytes;
-    for (int row = lane; row < rows; row += 32) {
-      piece(row, &src, &bytes, &dst);
-      total += bytes;
-    }
-    tc::mbar_arrive_expect_tx(&r.full[st], total);
-    for (int row = lane; row < rows; row += 32) {
-      piece(row, &src, &bytes, &dst);
-      tc::bulk_load(dst, src, bytes, &r.full[st]);
-    }
+  const uint32_t rows = (uint32_t)(a.boxes * a.box_rows * F::kPitch);
+  tc::mbar_arrive_expect_tx(&r.full[st], BWD ? 2 * rows + 8u * t.valid : rows);
+  for (int i = 0; i < a.boxes; ++i) {
+    tc::tma_load_3d(base + i * a.box_rows * F::kPitch, map_x, &r.full[st], t.p0, i * a.box_rows, t.b);
+    if (BWD)
+      tc::tma_load_3d(base + a.dout_off + i * a.box_rows * F::kPitch, map_d, &r.full[st], t.p0, i * a.box_rows, t.b);
+  }
+  if (BWD) {
+    const float* s = a.stats_in + (size_t)t.b * a.npts + t.p0;
+    tc::bulk_load(base + a.stat_off, s, 4 * t.valid, &r.full[st]);
+    tc::bulk_load(base + a.stat_off + 4 * F::kPts, s + (size_t)a.B * a.npts, 4 * t.valid, &r.full[st]);
   }
 }
 
-__device__ __forceinline__ Ring ring_setup(const RingArgs& a, uint8_t* smem, int loaders) {
+// GRAN < 16: this row of lanes' channels of tile k, one group of asynchronous copies per call.
+template <typename F, bool BWD>
+__device__ __forceinline__ void load_rows(const RingArgs& a, const Ring& r, int k, int lane, int w) {
+  using T = typename F::T;
+  const long long tile = blockIdx.x + (long long)k * gridDim.x;
+  if (tile < a.tiles) {
+    const Tile t = tile_of<F>(a, tile);
+    uint8_t* base = r.stage + (size_t)(k % a.stages) * a.stage_bytes;
+    auto copy = [&](const T* from, uint8_t* to) {
+      const uint8_t* p = reinterpret_cast<const uint8_t*>(from);
+      const uint32_t off = (uint32_t)(reinterpret_cast<uintptr_t>(p) & 15);
+      const int blocks = (int)(off + t.valid * (uint32_t)sizeof(T) + 15) >> 4;
+      for (int i = lane; i < blocks; i += F::LPR) tc::cp_async16(to + 16 * i, p - off + 16 * i, 16);
+    };
+    for (int c = w; c < a.C; c += F::kRows) {
+      copy(static_cast<const T*>(a.x) + t.at + (size_t)c * a.npts, base + c * F::kPitch);
+      if (BWD) copy(static_cast<const T*>(a.dout) + t.at + (size_t)c * a.npts, base + a.dout_off + c * F::kPitch);
+    }
+  }
+  tc::cp_async_commit();
+}
+
+// Waits until at most `most` of this thread's groups of copies are in flight.
+__device__ __forceinline__ void wait_rows(int most) {
+  if (most <= 0) tc::cp_async_wait<0>();
+  else if (most == 1) tc::cp_async_wait<1>();
+  else if (most == 2) tc::cp_async_wait<2>();
+  else tc::cp_async_wait<3>();
+  __syncwarp();
+}
+
+template <typename F>
+__device__ __forceinline__ Ring ring_setup(const RingArgs& a, uint8_t* smem) {
   Ring r;
   r.stage = smem;
   r.full = reinterpret_cast<uint64_t*>(smem + (size_t)a.stages * a.stage_bytes);
   r.empty = r.full + kMaxStages;
-  if (threadIdx.x == 0) {
+  if (F::kTma && threadIdx.x == 0) {
     for (int i = 0; i < a.stages; ++i) {
-      tc::mbar_init(&r.full[i], loaders);
-      tc::mbar_init(&r.empty[i], kWarps);
+      tc::mbar_init(&r.full[i], 1);
+      tc::mbar_init(&r.empty[i], F::W);
     }
     tc::fence_barrier_init();
   }
-  __syncthreads();
   return r;
 }
 
@@ -259,93 +253,135 @@ __device__ __forceinline__ uint8_t* align128(uint8_t* p) {
 
 // Shared memory behind the ring: barriers, gain and bias of every channel, and per group two
 // sums per point of each row of lanes and one row of results.
-constexpr size_t ring_tail(int C, int pts, int lpr) {
-  return 2 * kMaxStages * 8 + 8 * (size_t)C + (size_t)kGroups * (kWarps * (32 / lpr) + 1) * pts * 8;
+template <typename F>
+constexpr size_t ring_tail(int C) {
+  return 2 * kMaxStages * 8 + 16 * (size_t)C + (size_t)F::G * (F::kRows * F::kSumPitch + F::kPts) * 8;
 }
 
-template <typename T, int VEC, int LPR, bool SHIFT>
-__global__ void __launch_bounds__(kThreads, 1) norm_ring_fwd_kernel(const __grid_constant__ CUtensorMap map_x,
-                                                                    RingArgs a) {
-  constexpr int kPts = LPR * VEC, NP = (VEC + 1) / 2, kRows = kWarps * (32 / LPR);
+// Bytes by which element `at` of an array at `base` lies past a 16-byte boundary (0 for GRAN 16).
+template <typename F>
+__device__ __forceinline__ uint32_t past16(const void* base, size_t at) {
+  if (F::kTma) return 0;
+  return ((uint32_t)reinterpret_cast<uintptr_t>(base) + (uint32_t)at * (uint32_t)sizeof(typename F::T)) & 15u;
+}
+
+// What a group does when it has read stage st: the next tile comes into its place.
+template <typename F, bool BWD>
+__device__ __forceinline__ void release(const RingArgs& a, const CUtensorMap* map_x, const CUtensorMap* map_d,
+                                        const Ring& r, int k, int st, int t, int lane, int w) {
+  __syncwarp();
+  if (F::kTma) {
+    if ((threadIdx.x & 31) == 0) tc::mbar_arrive(&r.empty[st]);
+    if (t < 32 && tc::mbar_wait(&r.empty[st], (k / a.stages) & 1)) load_boxes<F, BWD>(a, map_x, map_d, r, k + a.stages);
+  } else {
+    load_rows<F, BWD>(a, r, k + a.stages, lane, w);
+  }
+}
+
+template <typename F, bool BWD>
+__device__ __forceinline__ void fill_ring(const RingArgs& a, const CUtensorMap* map_x, const CUtensorMap* map_d,
+                                          const Ring& r, int group, int lane, int w) {
+  if (F::kTma) {
+    if (threadIdx.x < 32)
+      for (int k = 0; k < a.stages; ++k) load_boxes<F, BWD>(a, map_x, map_d, r, k);
+  } else {
+    for (int k = group; k < a.stages; k += F::G) load_rows<F, BWD>(a, r, k, lane, w);
+  }
+}
+
+template <typename F>
+__device__ __forceinline__ float join(float v) {
+#pragma unroll
+  for (int m = 1; m < F::kJoin; m <<= 1) v += __shfl_xor_sync(~0u, v, m);
+  return v;
+}
+
+template <typename F>
+__global__ void __launch_bounds__(kThreads, 1)
+    norm_ring_fwd_kernel(const __grid_constant__ CUtensorMap map_x, const __grid_constant__ RingArgs a) {
+  using T = typename F::T;
+  constexpr int NP = F::NP, VEC = F::VEC, LPR = F::LPR, kPts = F::kPts, kRows = F::kRows, G = F::G, NC = F::NC;
   extern __shared__ uint8_t smem_raw[];
-  uint8_t* smem = align128(smem_raw);
-  const Ring ring = ring_setup(a, smem, SHIFT ? 32 : 1);
+  const Ring ring = ring_setup<F>(a, align128(smem_raw));
   float2* par = reinterpret_cast<float2*>(ring.empty + kMaxStages);
-  float2* red = par + a.C;
   const T* gain = static_cast<const T*>(a.gain);
   const T* bias = static_cast<const T*>(a.bias);
   for (int c = threadIdx.x; c < a.C; c += kThreads)
     par[c] = make_float2(gain ? to_f32(gain[c]) : 1.0f, bias ? to_f32(bias[c]) : 0.0f);
   __syncthreads();
-  const int warp = threadIdx.x >> 5;
-  if (warp == 0)
-    for (int k = 0; k < a.stages; ++k) load_tile<T, kPts, SHIFT, false>(a, &map_x, nullptr, ring, k);
-  const int group = warp / kWarps, t = threadIdx.x - group * kGroup;
+  const int group = threadIdx.x / F::kGroup, t = threadIdx.x % F::kGroup;
   const int lane = threadIdx.x % LPR, w = t / LPR;  // row of lanes
-  red += group * (kRows + 1) * kPts;
-  float2* fin = red + kRows * kPts;
+  fill_ring<F, false>(a, &map_x, nullptr, ring, group, lane, w);
+  float2* red = reinterpret_cast<float2*>(par + a.C) + group * (kRows * F::kSumPitch + kPts);
+  float2* fin = red + kRows * F::kSumPitch;
   const int nch = w < a.C ? (a.C - w + kRows - 1) / kRows : 0;
   const float inv_own = nch > 0 ? 1.0f / (float)nch : 0.0f;
   const float inv_c = 1.0f / (float)a.C;
   const int n_lo = a.C / kRows, extra = a.C % kRows;
   int k = group;
   for (long long tile = blockIdx.x + (long long)group * gridDim.x; tile < a.tiles;
-       tile += (long long)kGroups * gridDim.x, k += kGroups) {
+       tile += (long long)G * gridDim.x, k += G) {
     const int st = k % a.stages;
-    const int b = (int)(tile / a.tiles_per_plane), p0 = (int)(tile % a.tiles_per_plane) * kPts;
-    const int valid = min(kPts, a.npts - p0);
+    const Tile tl = tile_of<F>(a, tile);
     const uint8_t* rows = ring.stage + (size_t)st * a.stage_bytes;
-    const size_t at0 = (size_t)b * a.C * a.npts + p0;
-    auto row_of = [&](int c) {
-      const uint8_t* p = rows + c * kPitch<T, kPts, SHIFT>;
-      if (SHIFT) p += past16(static_cast<const T*>(a.x), at0 + (size_t)c * a.npts);
-      return p;
-    };
-    tc::mbar_wait(&ring.full[st], (k / a.stages) & 1);
+    if (F::kTma) tc::mbar_wait(&ring.full[st], (k / a.stages) & 1);
+    else wait_rows(a.stages / G - 1);
+    uint32_t raw[NC][F::kWords];
     F2 s[NP], q[NP], first[NP];
 #pragma unroll
     for (int i = 0; i < NP; ++i) s[i] = q[i] = first[i] = pack(0.0f, 0.0f);
-    if (nch > 0) {
-      read_row<T, VEC, LPR, SHIFT>(row_of(w), lane, first);
 #pragma unroll
-      for (int i = 0; i < NP; ++i) first[i] = neg2(first[i]);
+    for (int j = 0; j < NC; ++j) {
+      const int c = w + kRows * j;
+      if (F::kFull || c < a.C) read_row<F>(rows + c * F::kPitch + past16<F>(a.x, tl.at + (size_t)c * a.npts), lane, raw[j]);
     }
-#pragma unroll 4
-    for (int c = w + kRows; c < a.C; c += kRows) {
-      F2 v[NP];
-      read_row<T, VEC, LPR, SHIFT>(row_of(c), lane, v);
+    release<F, false>(a, &map_x, nullptr, ring, k, st, t, lane, w);
+    if (F::kFull || nch > 0) {
 #pragma unroll
-      for (int i = 0; i < NP; ++i) {
-        v[i] = add2(v[i], first[i]);
-        s[i] = add2(s[i], v[i]);
-        q[i] = fma2(v[i], v[i], q[i]);
+      for (int i = 0; i < NP; ++i) first[i] = neg2(pair_of<F>(raw[0], i));
+    }
+#pragma unroll
+    for (int j = 1; j < NC; ++j) {
+      if (F::kFull || j < nch) {
+#pragma unroll
+        for (int i = 0; i < NP; ++i) {
+          const F2 v = add2(pair_of<F>(raw[j], i), first[i]);
+          s[i] = add2(s[i], v);
+          q[i] = fma2(v, v, q[i]);
+        }
       }
     }
-    // point e of a lane sits at e * LPR + lane: free of bank conflicts both ways
+    // value e of a lane sits at e * LPR + lane
 #pragma unroll
     for (int i = 0; i < NP; ++i) {
-      const F2 mean = fma2(s[i], pack(inv_own, inv_own), neg2(first[i]));   // of the row's channels
-      const F2 m2 = fma2(mul2(s[i], pack(-inv_own, -inv_own)), s[i], q[i]);
+      const F2 mean = fma2(s[i], twice(inv_own), neg2(first[i]));  // of the row's channels
+      const F2 m2 = fma2(mul2(s[i], twice(-inv_own)), s[i], q[i]);
       const float2 mv = unpack(mean), qv = unpack(m2);
-      red[w * kPts + 2 * i * LPR + lane] = make_float2(mv.x, fmaxf(qv.x, 0.0f));
-      if (2 * i + 1 < VEC) red[w * kPts + (2 * i + 1) * LPR + lane] = make_float2(mv.y, fmaxf(qv.y, 0.0f));
+      red[w * F::kSumPitch + 2 * i * LPR + lane] = make_float2(mv.x, qv.x);
+      if (2 * i + 1 < VEC) red[w * F::kSumPitch + (2 * i + 1) * LPR + lane] = make_float2(mv.y, qv.y);
     }
-    tc::named_bar_sync(1 + group, kGroup);
-    for (int p = t; p < kPts; p += kGroup) {
-      float S = 0.0f;
+    tc::named_bar_sync(1 + group, F::kGroup);
+    {
+      const int p = t / F::kJoin, sub = t % F::kJoin;
+      float2 e[kRows / F::kJoin];
+      float S = 0.0f, M = 0.0f;
 #pragma unroll
-      for (int r = 0; r < kRows; ++r) S = fmaf(red[r * kPts + p].x, (float)(n_lo + (r < extra)), S);
-      const float mean = S * inv_c;
-      float M = 0.0f;
-#pragma unroll
-      for (int r = 0; r < kRows; ++r) {
-        const float2 e = red[r * kPts + p];
-        const float d = e.x - mean;
-        M += fmaf(d * d, (float)(n_lo + (r < extra)), e.y);
+      for (int r = 0; r < kRows / F::kJoin; ++r) {
+        const int row = sub + F::kJoin * r;
+        e[r] = red[row * F::kSumPitch + p];
+        S = fmaf(e[r].x, (float)(n_lo + (row < extra)), S);
       }
-      fin[p] = make_float2(mean, 1.0f / sqrtf(fmaf(M, inv_c, a.eps)));
+      const float mean = join<F>(S) * inv_c;
+#pragma unroll
+      for (int r = 0; r < kRows / F::kJoin; ++r) {
+        const float n = (float)(n_lo + (sub + F::kJoin * r < extra)), d = n > 0.0f ? e[r].x - mean : 0.0f;
+        // rounding may leave m2 of equal values a little below zero
+        M += fmaf(d * d, n, e[r].y < 0.0f ? 0.0f : e[r].y);
+      }
+      M = join<F>(M);
+      if (sub == 0) fin[p] = make_float2(mean, 1.0f / sqrtf(fmaf(M, inv_c, a.eps)));
     }
-    tc::named_bar_sync(1 + group, kGroup);
+    tc::named_bar_sync(1 + group, F::kGroup);
     F2 mr[NP], rr[NP];
     {
       float mean[2 * NP], r[2 * NP];
@@ -358,128 +394,143 @@ __global__ void __launch_bounds__(kThreads, 1) norm_ring_fwd_kernel(const __grid
 #pragma unroll
       for (int i = 0; i < NP; ++i) {
         rr[i] = pack(r[2 * i], r[2 * i + 1]);
-        mr[i] = pack(-mean[2 * i], -mean[2 * i + 1]);
+        mr[i] = pack(-mean[2 * i] * r[2 * i], -mean[2 * i + 1] * r[2 * i + 1]);
       }
       if (a.stats && w < 2) {
-        float* dst = a.stats + ((size_t)w * a.B + b) * a.npts + p0;
+        float* dst = a.stats + ((size_t)w * a.B + tl.b) * a.npts + tl.p0;
+        float v[2 * NP];
 #pragma unroll
-        for (int e = 0; e < VEC; ++e) {
-          const int p = SHIFT ? lane + LPR * e : lane * VEC + e;
-          if (p < valid) dst[p] = w == 0 ? mean[e] : r[e];
+        for (int e = 0; e < 2 * NP; ++e) v[e] = w == 0 ? mean[e] : r[e];
+        if constexpr (F::kTma) {  // planes are whole vectors long
+          if (lane * VEC < tl.valid) {
+#pragma unroll
+            for (int e = 0; e < VEC; e += (VEC < 4 ? 2 : 4)) {
+              if constexpr (VEC < 4) *reinterpret_cast<float2*>(dst + lane * VEC + e) = make_float2(v[e], v[e + 1]);
+              else *reinterpret_cast<float4*>(dst + lane * VEC + e) = make_float4(v[e], v[e + 1], v[e + 2], v[e + 3]);
+            }
+          }
+        } else {
+#pragma unroll
+          for (int e = 0; e < VEC; ++e)
+            if (F::point(lane, e) < tl.valid) dst[F::point(lane, e)] = v[e];
         }
       }
     }
-#pragma unroll 4
-    for (int c = w; c < a.C; c += kRows) {
-      F2 v[NP];
-      read_row<T, VEC, LPR, SHIFT>(row_of(c), lane, v);
-      const float2 g = par[c];
-      const F2 ga = pack(g.x, g.x), bi = pack(g.y, g.y);
+    T* out = static_cast<T*>(a.out) + tl.at;
 #pragma unroll
-      for (int i = 0; i < NP; ++i) v[i] = fma2(mul2(add2(v[i], mr[i]), rr[i]), ga, bi);
-      write_row<T, VEC, LPR, SHIFT>(static_cast<T*>(a.out) + at0 + (size_t)c * a.npts, lane, valid, v);
+    for (int j = 0; j < NC; ++j) {
+      const int c = w + kRows * j;
+      if (F::kFull || c < a.C) {
+        const float2 g = par[c];
+        const F2 ga = twice(g.x), bi = twice(g.y);
+        F2 v[NP];
+#pragma unroll
+        for (int i = 0; i < NP; ++i) v[i] = fma2(fma2(pair_of<F>(raw[j], i), rr[i], mr[i]), ga, bi);
+        write_row<F>(out + (size_t)c * a.npts, lane, tl.valid, v);
+      }
     }
-    __syncwarp();
-    if ((threadIdx.x & 31) == 0) tc::mbar_arrive(&ring.empty[st]);
-    if (t < 32 && tc::mbar_wait(&ring.empty[st], (k / a.stages) & 1))
-      load_tile<T, kPts, SHIFT, false>(a, &map_x, nullptr, ring, k + a.stages);
   }
 }
 
-// NC: channels per row of lanes, at most.
-template <typename T, int VEC, int LPR, int NC, bool SHIFT>
-__global__ void __launch_bounds__(kThreads, 1) norm_ring_bwd_kernel(const __grid_constant__ CUtensorMap map_x,
-                                                                    const __grid_constant__ CUtensorMap map_d,
-                                                                    RingArgs a) {
-  constexpr int kPts = LPR * VEC, NP = (VEC + 1) / 2, kRows = kWarps * (32 / LPR);
+template <typename F>
+__global__ void __launch_bounds__(kThreads, 1)
+    norm_ring_bwd_kernel(const __grid_constant__ CUtensorMap map_x, const __grid_constant__ CUtensorMap map_d,
+                         const __grid_constant__ RingArgs a) {
+  using T = typename F::T;
+  constexpr int NP = F::NP, VEC = F::VEC, LPR = F::LPR, kPts = F::kPts, kRows = F::kRows, G = F::G, NC = F::NC;
   extern __shared__ uint8_t smem_raw[];
-  uint8_t* smem = align128(smem_raw);
-  const Ring ring = ring_setup(a, smem, SHIFT ? 32 : 1);
+  const Ring ring = ring_setup<F>(a, align128(smem_raw));
   float* par = reinterpret_cast<float*>(ring.empty + kMaxStages);
-  float2* red = reinterpret_cast<float2*>(par + 2 * a.C);
   const T* gain = static_cast<const T*>(a.gain);
   for (int c = threadIdx.x; c < a.C; c += kThreads) par[c] = gain ? to_f32(gain[c]) : 1.0f;
   __syncthreads();
-  const int warp = threadIdx.x >> 5;
-  if (warp == 0)
-    for (int k = 0; k < a.stages; ++k) load_tile<T, kPts, SHIFT, true>(a, &map_x, &map_d, ring, k);
-  const int group = warp / kWarps, t = threadIdx.x - group * kGroup;
+  const int group = threadIdx.x / F::kGroup, t = threadIdx.x % F::kGroup;
   const int lane = threadIdx.x % LPR, w = t / LPR;  // row of lanes
-  red += group * (kRows + 1) * kPts;
-  float2* fin = red + kRows * kPts;
+  fill_ring<F, true>(a, &map_x, &map_d, ring, group, lane, w);
+  float2* red = reinterpret_cast<float2*>(par + 2 * a.C) + group * (kRows * F::kSumPitch + kPts);
+  float2* fin = red + kRows * F::kSumPitch;
   const float inv_c = 1.0f / (float)a.C;
   float ag[NC], ab[NC];
 #pragma unroll
   for (int i = 0; i < NC; ++i) ag[i] = ab[i] = 0.0f;
+  // GRAN < 16: the statistics of a tile are fetched while the tile before it is finished
+  float mean[2 * NP], rstd[2 * NP];
+  auto fetch_stats = [&](long long tile) {
+    const Tile tl = tile_of<F>(a, tile);
+    const float* p = a.stats_in + (size_t)tl.b * a.npts + tl.p0;
+#pragma unroll
+    for (int e = 0; e < 2 * NP; ++e) {
+      const bool in = tile < a.tiles && e < VEC && F::point(lane, e) < tl.valid;
+      mean[e] = in ? p[F::point(lane, e)] : 0.0f;
+      rstd[e] = in ? p[(size_t)a.B * a.npts + F::point(lane, e)] : 0.0f;
+    }
+  };
   int k = group;
-  for (long long tile = blockIdx.x + (long long)group * gridDim.x; tile < a.tiles; tile += (long long)kGroups * gridDim.x, k += kGroups) {
+  const long long tile0 = blockIdx.x + (long long)group * gridDim.x;
+  if (!F::kTma) fetch_stats(tile0);
+  for (long long tile = tile0; tile < a.tiles; tile += (long long)G * gridDim.x, k += G) {
     const int st = k % a.stages;
-    const int b = (int)(tile / a.tiles_per_plane), p0 = (int)(tile % a.tiles_per_plane) * kPts;
-    const int valid = min(kPts, a.npts - p0);
+    const Tile tl = tile_of<F>(a, tile);
     const uint8_t* rows = ring.stage + (size_t)st * a.stage_bytes;
-    const size_t at0 = (size_t)b * a.C * a.npts + p0;
-    tc::mbar_wait(&ring.full[st], (k / a.stages) & 1);
+    if (F::kTma) {
+      tc::mbar_wait(&ring.full[st], (k / a.stages) & 1);
+      const float* sm = reinterpret_cast<const float*>(rows + a.stat_off) + lane * VEC;
+      const bool in = lane * VEC < tl.valid;  // planes are whole vectors long
+#pragma unroll
+      for (int e = 0; e < VEC; e += 2) {
+        const float2 m = *reinterpret_cast<const float2*>(sm + e);
+        const float2 r = *reinterpret_cast<const float2*>(sm + kPts + e);
+        mean[e] = in ? m.x : 0.0f;
+        mean[e + 1] = in ? m.y : 0.0f;
+        rstd[e] = in ? r.x : 0.0f;
+        rstd[e + 1] = in ? r.y : 0.0f;
+      }
+    } else {
+      wait_rows(a.stages / G - 1);
+    }
     // xh = x r - mean r; points behind the plane's end have r = mean = 0
     F2 rr[NP], mr[NP], s1[NP], s2[NP];
-    {
-      float r[2 * NP], m[2 * NP];
 #pragma unroll
-      for (int e = 0; e < 2 * NP; ++e) {
-        r[e] = m[e] = 0.0f;
-        const int p = SHIFT ? lane + LPR * e : lane * VEC + e;
-        if (e < VEC && p < valid) {
-          const uint8_t* sm = rows + a.stat_off;
-          const uint8_t* sr = sm + kStatPitch<kPts, SHIFT>;
-          if (SHIFT) {
-            sm += past16(a.stats_in, (size_t)b * a.npts + p0);
-            sr += past16(a.stats_in, ((size_t)a.B + b) * a.npts + p0);
-          }
-          r[e] = reinterpret_cast<const float*>(sr)[p];
-          m[e] = -reinterpret_cast<const float*>(sm)[p] * r[e];
-        }
-      }
-#pragma unroll
-      for (int i = 0; i < NP; ++i) {
-        rr[i] = pack(r[2 * i], r[2 * i + 1]);
-        mr[i] = pack(m[2 * i], m[2 * i + 1]);
-        s1[i] = s2[i] = pack(0.0f, 0.0f);
-      }
+    for (int i = 0; i < NP; ++i) {
+      rr[i] = pack(rstd[2 * i], rstd[2 * i + 1]);
+      mr[i] = pack(-mean[2 * i] * rstd[2 * i], -mean[2 * i + 1] * rstd[2 * i + 1]);
+      s1[i] = s2[i] = pack(0.0f, 0.0f);
     }
-    auto read = [&](int c, F2 (&x)[NP], F2 (&u)[NP]) {
-      const uint8_t* px = rows + c * kPitch<T, kPts, SHIFT>;
-      const uint8_t* pu = px + a.dout_off;
-      if (SHIFT) {
-        const size_t at = at0 + (size_t)c * a.npts;
-        px += past16(static_cast<const T*>(a.x), at);
-        pu += past16(static_cast<const T*>(a.dout), at);
-      }
-      read_row<T, VEC, LPR, SHIFT>(px, lane, x);
-      read_row<T, VEC, LPR, SHIFT>(pu, lane, u);
-      if (valid < kPts) {  // whatever lies behind the plane's end counts as zero
-#pragma unroll
-        for (int i = 0; i < NP; ++i) {
-          const int pa = SHIFT ? lane + 2 * LPR * i : lane * VEC + 2 * i, pb = SHIFT ? pa + LPR : pa + 1;
-          const float2 fx = unpack(x[i]), fu = unpack(u[i]);
-          x[i] = pack(pa < valid ? fx.x : 0.0f, pb < valid ? fx.y : 0.0f);
-          u[i] = pack(pa < valid ? fu.x : 0.0f, pb < valid ? fu.y : 0.0f);
-        }
-      }
-    };
+    uint32_t x[NC][F::kWords], u[NC][F::kWords];
 #pragma unroll
     for (int j = 0; j < NC; ++j) {
       const int c = w + kRows * j;
-      if (c < a.C) {
-        F2 x[NP], u[NP];
-        read(c, x, u);
-        const float g = par[c];
-        const F2 ga = pack(g, g);
+      if (F::kFull || c < a.C) {
+        const uint8_t* row = rows + c * F::kPitch;
+        const size_t at = tl.at + (size_t)c * a.npts;
+        read_row<F>(row + past16<F>(a.x, at), lane, x[j]);
+        read_row<F>(row + a.dout_off + past16<F>(a.dout, at), lane, u[j]);
+        if (tl.valid < kPts) {  // whatever lies behind the plane's end counts as zero
+#pragma unroll
+          for (int e = 0; e < VEC; ++e)
+            if (F::point(lane, e) >= tl.valid) {
+              const uint32_t keep = sizeof(T) == 4 ? 0u : (e % 2 ? 0xffffu : 0xffff0000u);
+              constexpr int per = 4 / (int)sizeof(T);
+              x[j][e / per] &= keep;
+              u[j][e / per] &= keep;
+            }
+        }
+      }
+    }
+    release<F, true>(a, &map_x, &map_d, ring, k, st, t, lane, w);
+#pragma unroll
+    for (int j = 0; j < NC; ++j) {
+      const int c = w + kRows * j;
+      if (F::kFull || c < a.C) {
+        const F2 ga = twice(par[c]);
         F2 tg = pack(ag[j], 0.0f), tb = pack(ab[j], 0.0f);
 #pragma unroll
         for (int i = 0; i < NP; ++i) {
-          const F2 xh = fma2(x[i], rr[i], mr[i]);
-          const F2 e = mul2(u[i], ga);
-          tg = fma2(u[i], xh, tg);
-          tb = add2(tb, u[i]);
+          const F2 ui = pair_of<F>(u[j], i);
+          const F2 xh = fma2(pair_of<F>(x[j], i), rr[i], mr[i]);
+          const F2 e = mul2(ui, ga);
+          tg = fma2(ui, xh, tg);
+          tb = add2(tb, ui);
           s1[i] = add2(s1[i], e);
           s2[i] = fma2(e, xh, s2[i]);
         }
@@ -488,54 +539,55 @@ __global__ void __launch_bounds__(kThreads, 1) norm_ring_bwd_kernel(const __grid
         ab[j] = q.x + q.y;
       }
     }
-    if (a.out) {
+    if (!F::kTma) fetch_stats(tile + (long long)G * gridDim.x);
+    if (!a.out) continue;
 #pragma unroll
-      for (int i = 0; i < NP; ++i) {
-        const float2 p = unpack(s1[i]), q = unpack(s2[i]);
-        red[w * kPts + 2 * i * LPR + lane] = make_float2(p.x, q.x);
-        if (2 * i + 1 < VEC) red[w * kPts + (2 * i + 1) * LPR + lane] = make_float2(p.y, q.y);
-      }
-      tc::named_bar_sync(1 + group, kGroup);
-      for (int p = t; p < kPts; p += kGroup) {
-        float x = 0.0f, y = 0.0f;
+    for (int i = 0; i < NP; ++i) {
+      const float2 p = unpack(s1[i]), q = unpack(s2[i]);
+      red[w * F::kSumPitch + 2 * i * LPR + lane] = make_float2(p.x, q.x);
+      if (2 * i + 1 < VEC) red[w * F::kSumPitch + (2 * i + 1) * LPR + lane] = make_float2(p.y, q.y);
+    }
+    tc::named_bar_sync(1 + group, F::kGroup);
+    {
+      const int p = t / F::kJoin, sub = t % F::kJoin;
+      float y = 0.0f, z = 0.0f;
 #pragma unroll
-        for (int r = 0; r < kRows; ++r) {
-          const float2 e = red[r * kPts + p];
-          x += e.x;
-          y += e.y;
-        }
-        fin[p] = make_float2(x * inv_c, y * inv_c);
+      for (int r = 0; r < kRows / F::kJoin; ++r) {
+        const float2 e = red[(sub + F::kJoin * r) * F::kSumPitch + p];
+        y += e.x;
+        z += e.y;
       }
-      tc::named_bar_sync(1 + group, kGroup);
+      y = join<F>(y);
+      z = join<F>(z);
+      if (sub == 0) fin[p] = make_float2(y * inv_c, z * inv_c);
+    }
+    tc::named_bar_sync(1 + group, F::kGroup);
 #pragma unroll
-      for (int i = 0; i < NP; ++i) {
-        const float2 p = fin[2 * i * LPR + lane];
-        const float2 q = 2 * i + 1 < VEC ? fin[(2 * i + 1) * LPR + lane] : make_float2(0.0f, 0.0f);
-        s1[i] = pack(-p.x, -q.x);
-        s2[i] = pack(-p.y, -q.y);
-      }
-#pragma unroll 4
-      for (int c = w; c < a.C; c += kRows) {
-        F2 x[NP], u[NP];
-        read(c, x, u);
-        const float g = par[c];
-        const F2 ga = pack(g, g);
+    for (int i = 0; i < NP; ++i) {
+      const float2 p = fin[2 * i * LPR + lane];
+      const float2 q = 2 * i + 1 < VEC ? fin[(2 * i + 1) * LPR + lane] : make_float2(0.0f, 0.0f);
+      s1[i] = pack(-p.x, -q.x);
+      s2[i] = pack(-p.y, -q.y);
+    }
+    T* out = static_cast<T*>(a.out) + tl.at;
+#pragma unroll
+    for (int j = 0; j < NC; ++j) {
+      const int c = w + kRows * j;
+      if (F::kFull || c < a.C) {
+        const F2 ga = twice(par[c]);
+        F2 o[NP];
 #pragma unroll
         for (int i = 0; i < NP; ++i) {
-          const F2 xh = fma2(x[i], rr[i], mr[i]);
-          x[i] = mul2(rr[i], fma2(xh, s2[i], fma2(u[i], ga, s1[i])));
+          const F2 xh = fma2(pair_of<F>(x[j], i), rr[i], mr[i]);
+          o[i] = mul2(rr[i], fma2(xh, s2[i], fma2(pair_of<F>(u[j], i), ga, s1[i])));
         }
-        write_row<T, VEC, LPR, SHIFT>(static_cast<T*>(a.out) + at0 + (size_t)c * a.npts, lane, valid, x);
+        write_row<F>(out + (size_t)c * a.npts, lane, tl.valid, o);
       }
     }
-    __syncwarp();
-    if ((threadIdx.x & 31) == 0) tc::mbar_arrive(&ring.empty[st]);
-    if (t < 32 && tc::mbar_wait(&ring.empty[st], (k / a.stages) & 1))
-      load_tile<T, kPts, SHIFT, true>(a, &map_x, &map_d, ring, k + a.stages);
   }
   if (!a.part) return;
   // one row of 2C sums per group
-  float* row = a.part + ((size_t)blockIdx.x * kGroups + group) * 2 * a.C;
+  float* row = a.part + ((size_t)blockIdx.x * G + group) * 2 * a.C;
 #pragma unroll
   for (int j = 0; j < NC; ++j) {
     const int c = w + kRows * j;
@@ -554,65 +606,6 @@ __global__ void __launch_bounds__(kThreads, 1) norm_ring_bwd_kernel(const __grid
 
 // ------------------------------------------------------------------ host side
 
-struct RingPlan {
-  bool ok = false;
-  int vec = 0, lpr = 0;
-  bool shift = false;
-  RingArgs a{};
-  size_t smem = 0;
-  int grid = 0;
-};
-
-template <typename T>
-RingPlan plan_tile(const NormArgs& n, bool bwd, bool shift, int vec, int lpr, int sms) {
-  RingPlan p;
-  const int es = (int)sizeof(T), arrays = bwd ? 2 : 1;
-  const int pts = vec * lpr;
-  const int pitch = pts * es + (shift ? 16 : 0), stat = bwd ? 2 * (pts * 4 + (shift ? 16 : 0)) : 0;
-  p.vec = vec;
-  p.lpr = lpr;
-  p.shift = shift;
-  RingArgs& a = p.a;
-  a.boxes = n.C > 256 ? 2 : 1;
-  if (n.C > 512) return p;
-  a.box_rows = (n.C + a.boxes - 1) / a.boxes;
-  const int rows = shift ? n.C : a.boxes * a.box_rows;
-  auto up128 = [](int v) { return (v + 127) & ~127; };
-  a.dout_off = bwd ? up128(rows * pitch) : 0;
-  a.stat_off = up128(rows * pitch) * arrays;
-  a.stage_bytes = up128(a.stat_off + stat);
-  const size_t tail = ring_tail(n.C, pts, lpr) + 128;
-  if (tail >= kRingSmem) return p;
-  a.stages = (int)std::min<size_t>(kMaxStages, (kRingSmem - tail) / a.stage_bytes);
-  a.B = n.B;
-  a.C = n.C;
-  a.npts = (int)n.npts;
-  a.tiles_per_plane = (int)((n.npts + pts - 1) / pts);
-  a.tiles = (long long)n.B * a.tiles_per_plane;
-  p.smem = (size_t)a.stages * a.stage_bytes + tail;
-  p.grid = (int)std::min<long long>(sms, a.tiles);
-  // a row of lanes of the backward pass has registers for 16 channels
-  p.ok = a.stages >= 3 && (!bwd || n.C <= 16 * kWarps * (32 / lpr));
-  return p;
-}
-
-template <typename T>
-RingPlan plan_ring(const NormArgs& n, bool bwd, int sms) {
-  const int es = (int)sizeof(T);
-  bool al = n.npts * es % 16 == 0;
-  for (const void* q : {n.x, (const void*)n.out, n.dout, (const void*)n.dx, (const void*)n.stats})
-    al = al && reinterpret_cast<uintptr_t>(q) % 16 == 0;
-  // the widest rows that leave three stages and every SM a tile
-  const int shapes[3][2] = {{16 / es, 32}, {16 / es, 16}, {8 / es, 16}};
-  RingPlan p;
-  for (const auto& v : shapes) {
-    RingPlan q = plan_tile<T>(n, bwd, !al, v[0], v[1], sms);
-    if (q.ok) p = q;
-    if (q.ok && q.a.tiles >= 2 * sms) break;
-  }
-  return p;
-}
-
 bool field_map(CUtensorMap* m, bool bf16, const void* base, const RingArgs& a, int pts) {
   tc::EncodeTiledFn f = tc::encode_tiled_fn();
   if (!f) return false;
@@ -625,79 +618,127 @@ bool field_map(CUtensorMap* m, bool bf16, const void* base, const RingArgs& a, i
            CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-template <typename K>
-cudaError_t allow_smem(K k, size_t bytes) {
-  return cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)bytes);
-}
+// What a call has chosen so far, and what it left to report.
+struct Call {
+  NormArgs n;
+  bool bwd;
+  int sms;
+  cudaStream_t st;
+  int rows = 0;
+  cudaError_t err = cudaSuccess;
+};
 
-template <typename T, int VEC, int LPR, bool SHIFT>
-cudaError_t run_fwd(const RingPlan& p, const CUtensorMap& mx, cudaStream_t st) {
-  auto k = norm_ring_fwd_kernel<T, VEC, LPR, SHIFT>;
-  cudaError_t e = allow_smem(k, p.smem);
-  if (e != cudaSuccess) return e;
-  k<<<p.grid, kThreads, p.smem, st>>>(mx, p.a);
-  count_launch();
-  return cudaGetLastError();
-}
-
-template <typename T, int VEC, int LPR, int NC, bool SHIFT>
-cudaError_t run_bwd(const RingPlan& p, const CUtensorMap& mx, const CUtensorMap& md, cudaStream_t st) {
-  auto k = norm_ring_bwd_kernel<T, VEC, LPR, NC, SHIFT>;
-  cudaError_t e = allow_smem(k, p.smem);
-  if (e != cudaSuccess) return e;
-  k<<<p.grid, kThreads, p.smem, st>>>(mx, md, p.a);
-  count_launch();
-  return cudaGetLastError();
-}
-
-template <typename T, int VEC, int LPR, bool SHIFT>
-cudaError_t run_shape(const RingPlan& p, bool bwd, const CUtensorMap& mx, const CUtensorMap& md, cudaStream_t st) {
-  if (!bwd) return run_fwd<T, VEC, LPR, SHIFT>(p, mx, st);
-  const int rows = kWarps * (32 / LPR), nc = (p.a.C + rows - 1) / rows;
-  if (nc <= 4) return run_bwd<T, VEC, LPR, 4, SHIFT>(p, mx, md, st);
-  if (nc <= 8) return run_bwd<T, VEC, LPR, 8, SHIFT>(p, mx, md, st);
-  return run_bwd<T, VEC, LPR, 16, SHIFT>(p, mx, md, st);
-}
-
-template <typename T, bool SHIFT>
-cudaError_t run_plan(const RingPlan& p, bool bwd, const CUtensorMap& mx, const CUtensorMap& md, cudaStream_t st) {
-  constexpr int es = (int)sizeof(T);
-  if (p.lpr == 32) return run_shape<T, 16 / es, 32, SHIFT>(p, bwd, mx, md, st);
-  if (p.vec * es == 16) return run_shape<T, 16 / es, 16, SHIFT>(p, bwd, mx, md, st);
-  return run_shape<T, 8 / es, 16, SHIFT>(p, bwd, mx, md, st);
-}
-
-template <typename T>
-bool ring_run(const NormArgs& n, bool bwd, int sms, cudaStream_t st, int* rows, cudaError_t* err) {
-  if (n.npts < 64 || (bwd && n.C > 16 * kWarps * 2)) return false;
-  RingPlan p = plan_ring<T>(n, bwd, sms);
-  if (!p.ok) return false;
-  RingArgs& a = p.a;
+// Runs form F if its tiles fit: NC channels per row of lanes, three stages (two per group where
+// rows are copied by their own lanes); `least` tiles per SM, or the caller tries a narrower form.
+template <typename F>
+bool try_form(Call& call, int least) {
+  using T = typename F::T;
+  const NormArgs& n = call.n;
+  if (n.C > F::kRows * F::NC) return false;
+  RingArgs a{};
+  a.boxes = n.C > 256 ? 2 : 1;
+  a.box_rows = (n.C + a.boxes - 1) / a.boxes;
+  const size_t rows = F::kTma ? (size_t)a.boxes * a.box_rows : n.C;
+  auto up128 = [](size_t v) { return (v + 127) & ~size_t(127); };
+  const size_t array = up128(rows * F::kPitch);
+  const size_t stage = up128(array * (call.bwd ? 2 : 1) + (call.bwd && F::kTma ? 8 * F::kPts : 0));
+  const size_t tail = ring_tail<F>(n.C) + 128;
+  int stages = (int)std::min<size_t>(kMaxStages, (kRingSmem - tail) / stage);
+  // rows copied by their own lanes stay with their group; at most four tiles of copies in flight
+  if (!F::kTma) stages = std::min(stages / F::G, 4) * F::G;
+  if (stages < (F::kTma ? 3 : 2 * F::G)) return false;
+  a.tiles_per_plane = (int)((n.npts + F::kPts - 1) / F::kPts);
+  a.tiles = (long long)n.B * a.tiles_per_plane;
+  if (a.tiles < (long long)least * call.sms) return false;
+  a.dout_off = (int)array;
+  a.stat_off = (int)(2 * array);
+  a.stage_bytes = (int)stage;
+  a.stages = stages;
+  a.B = n.B;
+  a.C = n.C;
+  a.npts = (int)n.npts;
   a.x = n.x;
   a.dout = n.dout;
   a.gain = n.gain;
   a.bias = n.bias;
   a.eps = n.eps;
-  a.out = bwd ? n.dx : n.out;
+  a.out = call.bwd ? n.dx : n.out;
   a.stats = n.stats;
   a.stats_in = n.stats;
   a.part = n.dgain || n.dbias ? n.part : nullptr;
-  CUtensorMap mx{}, md{};
+  const int grid = (int)std::min<long long>(call.sms, a.tiles);
+  const size_t smem = (size_t)stages * stage + tail;
   const bool bf16 = sizeof(T) == 2;
-  if (!p.shift && (!field_map(&mx, bf16, n.x, a, p.lpr * p.vec) || (bwd && !field_map(&md, bf16, n.dout, a, p.lpr * p.vec)))) {
-    *err = cudaErrorInvalidValue;
+  call.rows = F::G * grid;
+  CUtensorMap mx{}, md{};
+  if (F::kTma && (!field_map(&mx, bf16, n.x, a, F::kPts) || (call.bwd && !field_map(&md, bf16, n.dout, a, F::kPts)))) {
+    call.err = cudaErrorInvalidValue;
     return true;
   }
-  *rows = kGroups * p.grid;
-  *err = p.shift ? run_plan<T, true>(p, bwd, mx, md, st) : run_plan<T, false>(p, bwd, mx, md, st);
+  auto run = [&](auto k, auto... maps) {
+    cudaError_t e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+    if (e != cudaSuccess) return e;
+    k<<<grid, kThreads, smem, call.st>>>(maps..., a);
+    count_launch();
+    return cudaGetLastError();
+  };
+  if constexpr (F::kTma) {
+    if (n.C == F::kRows * F::NC) {
+      call.err = call.bwd ? run(norm_ring_bwd_kernel<typename F::Filled>, mx, md)
+                          : run(norm_ring_fwd_kernel<typename F::Filled>, mx);
+      return true;
+    }
+  }
+  call.err = call.bwd ? run(norm_ring_bwd_kernel<F>, mx, md) : run(norm_ring_fwd_kernel<F>, mx);
   return true;
+}
+
+// The forms of either pass, widest rows first (a wider row is a longer run of HBM).  A form has at
+// most 32 registers of packed values.
+template <typename T, int GRAN>
+bool run_forms(Call& c) {
+  constexpr int v16 = 16 / (int)sizeof(T), v8 = 8 / (int)sizeof(T);
+  for (int least = 2; least >= 0; least -= 2) {
+    if (!c.bwd) {
+      if (least && (try_form<Form<T, v16, 16, 4, 8, GRAN>>(c, least) || try_form<Form<T, v16, 16, 8, 8, GRAN>>(c, least)))
+        return true;
+      if (try_form<Form<T, v8, 16, 8, 4, GRAN>>(c, least) || try_form<Form<T, v8, 16, 8, 16, GRAN>>(c, least) ||
+          try_form<Form<T, v8, 16, 16, 16, GRAN>>(c, least))
+        return true;
+    } else {
+      if (least && try_form<Form<T, v8, 16, 4, 8, GRAN>>(c, least)) return true;
+      if (try_form<Form<T, v8, 16, 8, 4, GRAN>>(c, least) || try_form<Form<T, v8, 16, 8, 8, GRAN>>(c, least) ||
+          try_form<Form<T, v8, 16, 16, 8, GRAN>>(c, least))
+        return true;
+    }
+  }
+  return false;
+}
+
+// The widest of 16, 4 and 2 bytes that every plane starts on.
+int granule(const NormArgs& n, int es) {
+  int gran = 16;
+  for (const void* q : {n.x, (const void*)n.out, n.dout, (const void*)n.dx})
+    while (n.npts * es % gran || reinterpret_cast<uintptr_t>(q) % gran) gran >>= 1;
+  if (gran == 16 && reinterpret_cast<uintptr_t>(n.stats) % 16) gran = 8;
+  return gran == 8 ? 4 : gran;
 }
 
 }  // namespace
 
-bool launch_norm_ring(bool bf16, const NormArgs& a, bool bwd, int sms, cudaStream_t st, int* rows, cudaError_t* err) {
-  return bf16 ? ring_run<__nv_bfloat16>(a, bwd, sms, st, rows, err) : ring_run<float>(a, bwd, sms, st, rows, err);
+bool launch_norm_ring(bool bf16, const NormArgs& n, bool bwd, int sms, cudaStream_t st, int* rows, cudaError_t* err) {
+  if (n.npts < 64) return false;
+  Call c{n, bwd, sms, st};
+  const int gran = granule(n, bf16 ? 2 : 4);
+  bool ran;
+  if (bf16) ran = gran == 16 ? run_forms<__nv_bfloat16, 16>(c) : gran == 4 ? run_forms<__nv_bfloat16, 4>(c) : run_forms<__nv_bfloat16, 2>(c);
+  else ran = gran == 16 ? run_forms<float, 16>(c) : run_forms<float, 4>(c);
+  *rows = c.rows;
+  *err = c.err;
+  return ran;
 }
+
+int norm_partials(int sms) { return 4 * sms; }
 
 int take_norm_status() {
   int v = 0, z = 0;
