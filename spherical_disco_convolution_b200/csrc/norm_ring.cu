@@ -3,12 +3,13 @@
 //
 // What bounds both passes is HBM, and what kept the register form below it was latency: its
 // loads are only in flight between two barriers of a CTA.  Here a ring of tiles of C channels x
-// LPR * VEC points is kept full while G groups of W = 8 or 16 warps take the tiles in turn.  A tile
+// LPR * VEC points is kept full while G groups of W = 1 to 16 warps take the tiles in turn.  A tile
 // is read from HBM once and from shared memory once: its sums are added on the way into registers
 // (at most 32 of packed values a thread), the stage is free for the next tile at once, and the
 // result is formed from the registers after the sums over channels have crossed the group.
-// LPR = 32 or 16 lanes take a channel row, VEC points each, so a group has W or 2 W rows of lanes
-// and row r takes the channels r, r + rows, ....
+// LPR = 32, 16 or 8 lanes take a channel row, VEC points each, so a group has W * 32 / LPR rows of
+// lanes and row r takes the channels r, r + rows, ....  Few channels take small groups (one warp
+// has no barrier at all), many take large ones.
 //
 // Loads.  GRAN = 16 (every plane starts on 16 bytes): one TMA box of C rows per array, issued by
 // the first warp of the group that has read the stage.  GRAN = 4 or 2 (planes start on any
@@ -34,7 +35,7 @@ namespace disco {
 namespace {
 
 constexpr int kThreads = 512;  // 128 registers a thread
-constexpr int kMaxStages = 12;
+constexpr int kMaxStages = 32;
 constexpr size_t kRingSmem = 225 * 1024;  // of 227 KB
 
 // Two fp32 values of neighbouring points.
@@ -86,8 +87,8 @@ struct Form {
   static constexpr int kPitch = kPts * (int)sizeof(T) + (kTma ? 0 : 16);
   // the sums of a point are joined by kJoin lanes; rows of sums are kSumPitch apart, which keeps
   // those lanes on different banks
-  static constexpr int kJoin = kGroup / kPts, kSumPitch = kPts + 16 / kJoin;
-  static_assert(VEC % kRun == 0 && kJoin >= 1 && kJoin <= 16 && kRows % kJoin == 0, "shape");
+  static constexpr int kJoin = kGroup > kPts ? kGroup / kPts : 1, kSumPitch = kPts + (kJoin < 16 ? 16 / kJoin : 1);
+  static_assert(VEC % kRun == 0 && kJoin <= 32 && kRows % kJoin == 0 && kPts % (kGroup / kJoin) == 0, "shape");
   // the tile's point that value e of a lane is
   static __device__ __forceinline__ int point(int lane, int e) {
     return (lane + LPR * (e / kRun)) * kRun + e % kRun;
@@ -208,15 +209,23 @@ __device__ __forceinline__ void load_rows(const RingArgs& a, const Ring& r, int 
   if (tile < a.tiles) {
     const Tile t = tile_of<F>(a, tile);
     uint8_t* base = r.stage + (size_t)(k % a.stages) * a.stage_bytes;
-    auto copy = [&](const T* from, uint8_t* to) {
-      const uint8_t* p = reinterpret_cast<const uint8_t*>(from);
-      const uint32_t off = (uint32_t)(reinterpret_cast<uintptr_t>(p) & 15);
-      const int blocks = (int)(off + t.valid * (uint32_t)sizeof(T) + 15) >> 4;
-      for (int i = lane; i < blocks; i += F::LPR) tc::cp_async16(to + 16 * i, p - off + 16 * i, 16);
-    };
-    for (int c = w; c < a.C; c += F::kRows) {
-      copy(static_cast<const T*>(a.x) + t.at + (size_t)c * a.npts, base + c * F::kPitch);
-      if (BWD) copy(static_cast<const T*>(a.dout) + t.at + (size_t)c * a.npts, base + a.dout_off + c * F::kPitch);
+    // the 32 / LPR rows of lanes of a warp have neighbouring channels; all its lanes copy together
+    constexpr int kBlocks = F::kPitch / 16, kSide = 32 / F::LPR;
+    const int wlane = threadIdx.x & 31;
+    for (int c0 = w - (wlane / F::LPR); c0 < a.C; c0 += F::kRows) {
+#pragma unroll
+      for (int i = wlane; i < kBlocks * kSide; i += 32) {
+        const int c = c0 + i / kBlocks, blk = i % kBlocks;
+        if (c >= a.C) break;
+#pragma unroll
+        for (int arr = 0; arr < (BWD ? 2 : 1); ++arr) {
+          const uint8_t* p =
+              reinterpret_cast<const uint8_t*>(static_cast<const T*>(arr ? a.dout : a.x) + t.at + (size_t)c * a.npts);
+          const uint32_t off = (uint32_t)(reinterpret_cast<uintptr_t>(p) & 15);
+          if (16 * blk < (int)(off + t.valid * (uint32_t)sizeof(T)))
+            tc::cp_async16(base + (arr ? a.dout_off : 0) + c * F::kPitch + 16 * blk, p - off + 16 * blk, 16);
+        }
+      }
     }
   }
   tc::cp_async_commit();
@@ -290,6 +299,12 @@ __device__ __forceinline__ void fill_ring(const RingArgs& a, const CUtensorMap* 
 }
 
 template <typename F>
+__device__ __forceinline__ void group_sync(int group) {
+  if constexpr (F::W == 1) __syncwarp();
+  else tc::named_bar_sync(1 + group, F::kGroup);
+}
+
+template <typename F>
 __device__ __forceinline__ float join(float v) {
 #pragma unroll
   for (int m = 1; m < F::kJoin; m <<= 1) v += __shfl_xor_sync(~0u, v, m);
@@ -360,9 +375,10 @@ __global__ void __launch_bounds__(kThreads, 1)
       red[w * F::kSumPitch + 2 * i * LPR + lane] = make_float2(mv.x, qv.x);
       if (2 * i + 1 < VEC) red[w * F::kSumPitch + (2 * i + 1) * LPR + lane] = make_float2(mv.y, qv.y);
     }
-    tc::named_bar_sync(1 + group, F::kGroup);
-    {
-      const int p = t / F::kJoin, sub = t % F::kJoin;
+    group_sync<F>(group);
+#pragma unroll
+    for (int p = t / F::kJoin; p < kPts; p += F::kGroup / F::kJoin) {
+      const int sub = t % F::kJoin;
       float2 e[kRows / F::kJoin];
       float S = 0.0f, M = 0.0f;
 #pragma unroll
@@ -381,7 +397,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       M = join<F>(M);
       if (sub == 0) fin[p] = make_float2(mean, 1.0f / sqrtf(fmaf(M, inv_c, a.eps)));
     }
-    tc::named_bar_sync(1 + group, F::kGroup);
+    group_sync<F>(group);
     F2 mr[NP], rr[NP];
     {
       float mean[2 * NP], r[2 * NP];
@@ -396,11 +412,11 @@ __global__ void __launch_bounds__(kThreads, 1)
         rr[i] = pack(r[2 * i], r[2 * i + 1]);
         mr[i] = pack(-mean[2 * i] * r[2 * i], -mean[2 * i + 1] * r[2 * i + 1]);
       }
-      if (a.stats && w < 2) {
-        float* dst = a.stats + ((size_t)w * a.B + tl.b) * a.npts + tl.p0;
+      for (int which = w; a.stats && which < 2; which += kRows) {
+        float* dst = a.stats + ((size_t)which * a.B + tl.b) * a.npts + tl.p0;
         float v[2 * NP];
 #pragma unroll
-        for (int e = 0; e < 2 * NP; ++e) v[e] = w == 0 ? mean[e] : r[e];
+        for (int e = 0; e < 2 * NP; ++e) v[e] = which == 0 ? mean[e] : r[e];
         if constexpr (F::kTma) {  // planes are whole vectors long
           if (lane * VEC < tl.valid) {
 #pragma unroll
@@ -547,9 +563,10 @@ __global__ void __launch_bounds__(kThreads, 1)
       red[w * F::kSumPitch + 2 * i * LPR + lane] = make_float2(p.x, q.x);
       if (2 * i + 1 < VEC) red[w * F::kSumPitch + (2 * i + 1) * LPR + lane] = make_float2(p.y, q.y);
     }
-    tc::named_bar_sync(1 + group, F::kGroup);
-    {
-      const int p = t / F::kJoin, sub = t % F::kJoin;
+    group_sync<F>(group);
+#pragma unroll
+    for (int p = t / F::kJoin; p < kPts; p += F::kGroup / F::kJoin) {
+      const int sub = t % F::kJoin;
       float y = 0.0f, z = 0.0f;
 #pragma unroll
       for (int r = 0; r < kRows / F::kJoin; ++r) {
@@ -561,7 +578,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       z = join<F>(z);
       if (sub == 0) fin[p] = make_float2(y * inv_c, z * inv_c);
     }
-    tc::named_bar_sync(1 + group, F::kGroup);
+    group_sync<F>(group);
 #pragma unroll
     for (int i = 0; i < NP; ++i) {
       const float2 p = fin[2 * i * LPR + lane];
@@ -636,8 +653,9 @@ bool try_form(Call& call, int least) {
   const NormArgs& n = call.n;
   if (n.C > F::kRows * F::NC) return false;
   RingArgs a{};
-  a.boxes = n.C > 256 ? 2 : 1;
-  a.box_rows = (n.C + a.boxes - 1) / a.boxes;
+  a.boxes = (n.C + 255) / 256;
+  // an even number of rows: a box lands on 128 bytes, and a row may have 64
+  a.box_rows = ((n.C + a.boxes - 1) / a.boxes + 1) & ~1;
   const size_t rows = F::kTma ? (size_t)a.boxes * a.box_rows : n.C;
   auto up128 = [](size_t v) { return (v + 127) & ~size_t(127); };
   const size_t array = up128(rows * F::kPitch);
@@ -693,22 +711,27 @@ bool try_form(Call& call, int least) {
   return true;
 }
 
-// The forms of either pass, widest rows first (a wider row is a longer run of HBM).  A form has at
-// most 32 registers of packed values.
+// The forms of either pass, few channels first.  A form has at most 32 registers of packed values;
+// of those that hold the channels the first ones have the longer rows (runs of HBM) and the
+// smaller groups (cheaper barriers).
 template <typename T, int GRAN>
 bool run_forms(Call& c) {
   constexpr int v16 = 16 / (int)sizeof(T), v8 = 8 / (int)sizeof(T);
   for (int least = 2; least >= 0; least -= 2) {
     if (!c.bwd) {
-      if (least && (try_form<Form<T, v16, 16, 4, 8, GRAN>>(c, least) || try_form<Form<T, v16, 16, 8, 8, GRAN>>(c, least)))
+      if (least && (try_form<Form<T, v16, 32, 1, 8, GRAN>>(c, least) || try_form<Form<T, v16, 16, 1, 8, GRAN>>(c, least) ||
+                    try_form<Form<T, v16, 16, 2, 8, GRAN>>(c, least) || try_form<Form<T, v16, 16, 4, 8, GRAN>>(c, least) ||
+                    try_form<Form<T, v16, 16, 8, 8, GRAN>>(c, least)))
         return true;
       if (try_form<Form<T, v8, 16, 8, 4, GRAN>>(c, least) || try_form<Form<T, v8, 16, 8, 16, GRAN>>(c, least) ||
-          try_form<Form<T, v8, 16, 16, 16, GRAN>>(c, least))
+          try_form<Form<T, v8, 16, 16, 16, GRAN>>(c, least) || try_form<Form<T, v8, 8, 16, 16, GRAN>>(c, least))
         return true;
     } else {
-      if (least && try_form<Form<T, v8, 16, 4, 8, GRAN>>(c, least)) return true;
+      if (least && (try_form<Form<T, v8, 32, 1, 8, GRAN>>(c, least) || try_form<Form<T, v8, 16, 1, 8, GRAN>>(c, least) ||
+                    try_form<Form<T, v8, 16, 2, 8, GRAN>>(c, least) || try_form<Form<T, v8, 16, 4, 8, GRAN>>(c, least)))
+        return true;
       if (try_form<Form<T, v8, 16, 8, 4, GRAN>>(c, least) || try_form<Form<T, v8, 16, 8, 8, GRAN>>(c, least) ||
-          try_form<Form<T, v8, 16, 16, 8, GRAN>>(c, least))
+          try_form<Form<T, v8, 16, 16, 8, GRAN>>(c, least) || try_form<Form<T, v8, 8, 16, 8, GRAN>>(c, least))
         return true;
     }
   }
@@ -738,7 +761,8 @@ bool launch_norm_ring(bool bf16, const NormArgs& n, bool bwd, int sms, cudaStrea
   return ran;
 }
 
-int norm_partials(int sms) { return 4 * sms; }
+// One row per group of the backward pass's forms.
+int norm_partials(int C, int sms) { return (C <= 16 ? 16 : C <= 32 ? 8 : C <= 64 ? 4 : 2) * sms; }
 
 int take_norm_status() {
   int v = 0, z = 0;

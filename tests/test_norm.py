@@ -167,7 +167,10 @@ def check_backward(dout, x, gain, eps):
 SHAPES = [(1, 1, 1, 1), (1, 4, 1, 1), (3, 5, 1, 1), (700, 33, 1, 1), (1, 2, 3, 3), (2, 3, 7, 9), (1, 4, 17, 32),
           (2, 8, 5, 8), (1, 9, 4, 6), (3, 50, 61, 121), (2, 63, 12, 20), (2, 64, 12, 20), (1, 65, 9, 20),
           (1, 128, 33, 34), (1, 129, 16, 16), (2, 256, 19, 36), (1, 257, 8, 9), (1, 511, 6, 11), (1, 512, 16, 24),
-          (1, 513, 6, 8), (2, 1500, 3, 5), (1, 64, 181, 360), (4, 32, 91, 180), (1, 77, 91, 181)]
+          (1, 513, 6, 8), (2, 1500, 3, 5), (1, 64, 181, 360), (4, 32, 91, 180), (1, 77, 91, 181),
+          (1, 1, 181, 424), (2, 5, 181, 424), (1, 8, 181, 424), (1, 8, 181, 423), (2, 13, 140, 300), (2, 16, 140, 300),
+          (1, 30, 183, 426), (1, 128, 181, 360), (1, 130, 181, 361), (1, 256, 120, 180), (1, 300, 120, 180),
+          (1, 512, 90, 120), (1, 700, 64, 128), (1, 1024, 32, 72), (1, 1025, 16, 20)]
 
 
 @gpu
