@@ -349,6 +349,402 @@ __global__ void __launch_bounds__(256) ns_reduce_kernel(const float* __restrict_
   *reinterpret_cast<uint2*>(am + n + i) = *reinterpret_cast<const uint2*>(l);
 }
 
+// ------------------------------------------------------------------ small matrices: one launch
+//
+// Matrices of up to 128 rows stay in shared memory for all steps.  A cluster of S CTAs takes one
+// matrix, each CTA a run of 64-column chunks of X.  Per step every CTA adds its columns' share of
+// X X^T, the shares are summed by blocks of columns (CTA q sums the q-th block of everybody's share)
+// and each block goes to all CTAs; A A and B are formed by every CTA for itself, and B X for its
+// own columns.  What bounds it is latency: 15 products that wait for one another, each a few
+// hundred cycles of tensor core, and two cluster barriers a step.
+//
+// X chunk: [RP rows][64 columns] fp16, rows of 128 bytes in the 128-byte swizzle.  The same tile is
+// the K-major operand of X X^T (K = columns) and the MN-major operand of B X (K = rows).  MMAs have
+// M = 128; with RP = 64 rows 64..127 of an operand are whatever follows the tile, and the rows of the
+// result they make are not read.
+
+constexpr int kSmallThreads = 256;
+constexpr int kSmallMaxCluster = 8;
+constexpr size_t kSmallSmem = 226 * 1024;      // of 227 KB
+constexpr size_t kSmallLeast = 120 * 1024;     // more than half of an SM: one CTA (and its TMEM) per SM
+
+struct SmallArgs {
+  Shape s;
+  Rule r;
+  float a, b, c;
+  double eps;
+  int steps, S, nc, max_chunks;
+};
+
+// Byte offsets of a CTA's shared memory.
+struct SmallLayout {
+  uint32_t xl, ah, al, recv, misc, total;
+};
+__host__ __device__ constexpr SmallLayout small_layout(int rp, int S, int max_chunks) {
+  SmallLayout l{};
+  const uint32_t chunk = rp * 128, a = (rp / 64) * chunk;
+  l.xl = max_chunks * chunk;
+  l.ah = 2 * l.xl;
+  l.al = l.ah + a;
+  l.recv = l.al + a;
+  l.misc = l.recv + (S > 1 ? rp * rp * 4 : 0);
+  l.total = l.misc + 1024 + (rp < 128 ? 8192 : 0);
+  return l;
+}
+
+__device__ __forceinline__ uint32_t sw128(int row, int col_byte) {
+  return (uint32_t)row * 128u + ((uint32_t)col_byte ^ (((uint32_t)row & 7u) << 4));
+}
+__device__ __forceinline__ uint32_t cluster_rank() {
+  uint32_t r;
+  asm volatile("mov.u32 %0, %cluster_ctarank;" : "=r"(r));
+  return r;
+}
+__device__ __forceinline__ void cluster_sync() {
+  asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
+}
+__device__ __forceinline__ uint32_t at_rank(uint32_t addr, uint32_t rank) {
+  uint32_t r;
+  asm("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(r) : "r"(addr), "r"(rank));
+  return r;
+}
+__device__ __forceinline__ void st_remote(uint32_t addr, float v) {
+  asm volatile("st.shared::cluster.f32 [%0], %1;" ::"r"(addr), "f"(v) : "memory");
+}
+__device__ __forceinline__ void st_remote(uint32_t addr, double v) {
+  asm volatile("st.shared::cluster.f64 [%0], %1;" ::"r"(addr), "d"(v) : "memory");
+}
+__device__ __forceinline__ void st_remote(uint32_t addr, uint4 v) {
+  asm volatile("st.shared::cluster.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(addr), "r"(v.x), "r"(v.y), "r"(v.z), "r"(v.w)
+               : "memory");
+}
+// Generic-proxy writes to shared memory of the whole cluster before later async-proxy reads.
+__device__ __forceinline__ void fence_proxy_async_all() { asm volatile("fence.proxy.async;" ::: "memory"); }
+
+// 8 values as 16 bytes of hi and of lo.
+__device__ __forceinline__ void split8(const float (&v)[8], uint4& hi, uint4& lo) {
+  alignas(16) __half h[8], l[8];
+#pragma unroll
+  for (int i = 0; i < 8; ++i) split(v[i], h[i], l[i]);
+  hi = *reinterpret_cast<const uint4*>(h);
+  lo = *reinterpret_cast<const uint4*>(l);
+}
+__device__ __forceinline__ void join8(uint4 hi, uint4 lo, float (&v)[8]) {
+  const __half2* h = reinterpret_cast<const __half2*>(&hi);
+  const __half2* l = reinterpret_cast<const __half2*>(&lo);
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const float2 x = __half22float2(h[i]), y = __half22float2(l[i]);
+    v[2 * i] = fmaf(y.x, 1.0f / kSl, x.x);
+    v[2 * i + 1] = fmaf(y.y, 1.0f / kSl, x.y);
+  }
+}
+
+// Sum of main and small products, 16 columns of a lane's row.
+__device__ __forceinline__ void drain16(uint32_t main, uint32_t small, float (&v)[16]) {
+  float e[16];
+  tc::tmem_ld16(main, v);
+  tc::tmem_ld16(small, e);
+#pragma unroll
+  for (int i = 0; i < 16; ++i) v[i] = fmaf(e[i], 1.0f / kSl, v[i]);
+}
+
+template <typename T, int RP>
+__global__ void __launch_bounds__(kSmallThreads, 1)
+    ns_small_kernel(const __grid_constant__ Pointers ptr, const __grid_constant__ SmallArgs a) {
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* smem = align1024(smem_raw);
+  constexpr uint32_t kChunk = RP * 128;
+  const SmallLayout lay = small_layout(RP, a.S, a.max_chunks);
+  uint8_t *xh = smem, *xl = smem + lay.xl, *ah = smem + lay.ah, *al = smem + lay.al;
+  float* recv = reinterpret_cast<float*>(smem + lay.recv);
+  double* norms = reinterpret_cast<double*>(smem + lay.misc);  // [cluster]
+  double* warps = norms + kSmallMaxCluster;                    // [8]
+  uint64_t* done = reinterpret_cast<uint64_t*>(warps + 8);
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(done + 1);
+  const Shape& s = a.s;
+  const int t = threadIdx.x, warp = t >> 5, lane = t & 31;
+  const int S = a.S, q = S > 1 ? (int)cluster_rank() : 0, mi = blockIdx.x / S;
+  const int c_lo = a.nc * q / S, mine = a.nc * (q + 1) / S - c_lo;
+  const int quarter = (warp & 3) * 32, side = warp >> 2;  // TMEM lanes and half of the columns
+  const int row = quarter + lane;
+  const bool live = quarter < RP;
+
+  if (t == 0) {
+    tc::mbar_init(done, 1);
+    tc::fence_barrier_init();
+  }
+  if (warp == 0) {
+    tc::tmem_alloc(tmem_slot, 512);
+    tc::tmem_relinquish();
+  }
+  tc::fence_before_sync();
+  __syncthreads();
+  tc::fence_after_sync();
+  const uint32_t tmem = *tmem_slot;
+  if (S > 1) cluster_sync();  // everyone's shared memory may be written from here on
+
+  // U's sum of squares, and the momentum on the way; then X.  A task is 8 columns of one row.
+  const int tn = mi / s.groups;
+  const size_t base = (size_t)(mi % s.groups) * s.rows * s.cols;
+  const T* in = static_cast<const T*>(ptr.in[tn]) + base;
+  float* mo = a.r.step ? ptr.m_out[tn] + base : nullptr;
+  const int tasks = mine * 8 * RP;
+  auto place = [&](int task, int& r, int& l0) {
+    if (s.tr) {
+      r = task % RP;
+      l0 = (c_lo * 8 + task / RP) * 8;
+    } else {
+      r = task / (mine * 8);
+      l0 = (c_lo * 8 + task % (mine * 8)) * 8;
+    }
+  };
+  auto index = [&](int r, int l) { return s.tr ? (size_t)l * s.cols + r : (size_t)r * s.cols + l; };
+  double sum = 0.0;
+  for (int task = t; task < tasks; task += kSmallThreads) {
+    int r, l0;
+    place(task, r, l0);
+    if (r >= s.R) continue;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      if (l0 + i >= s.L) break;
+      const size_t at = index(r, l0 + i);
+      float u = to_f32(in[at]);
+      if (a.r.step) {
+        const float mv = fmaf(a.r.momentum, ptr.m[tn][base + at], u);
+        mo[at] = mv;
+        u = a.r.nesterov ? fmaf(a.r.momentum, mv, u) : mv;
+      }
+      sum += (double)u * (double)u;
+    }
+  }
+  sum = warp_sum(sum);
+  if (lane == 0) warps[warp] = sum;
+  __syncthreads();
+  if (t < S) {
+    double v = 0.0;
+    for (int k = 0; k < kSmallThreads / 32; ++k) v += warps[k];
+    if (S > 1) st_remote(at_rank(tc::smem_u32(&norms[q]), t), v);
+    else norms[0] = v;
+  }
+  if (S > 1) cluster_sync();
+  else __syncthreads();
+  double all = 0.0;
+  for (int k = 0; k < S; ++k) all += norms[k];
+  const float scale = (float)((double)kSx / (sqrt(all) + a.eps));
+  for (int task = t; task < tasks; task += kSmallThreads) {
+    int r, l0;
+    place(task, r, l0);
+    float v[8];
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      float u = 0.0f;
+      if (r < s.R && l0 + i < s.L) {
+        const size_t at = index(r, l0 + i);
+        u = to_f32(in[at]);
+        if (a.r.step) u = a.r.nesterov ? fmaf(a.r.momentum, mo[at], u) : mo[at];
+      }
+      v[i] = u * scale;
+    }
+    uint4 hi, lo;
+    split8(v, hi, lo);
+    const uint32_t off = (uint32_t)(l0 / 64 - c_lo) * kChunk + sw128(r, (l0 % 64) * 2);
+    *reinterpret_cast<uint4*>(xh + off) = hi;
+    *reinterpret_cast<uint4*>(xl + off) = lo;
+  }
+  tc::fence_proxy_async();
+  __syncthreads();
+
+  uint32_t phase = 0;
+  bool ok = true;
+  const uint32_t sxh = tc::smem_u32(xh), sxl = tc::smem_u32(xl), sah = tc::smem_u32(ah), sal = tc::smem_u32(al);
+  const uint32_t tw = tmem + ((uint32_t)quarter << 16);
+  auto finish = [&]() {  // the issued products are done and visible
+    ok = tc::mbar_wait(done, phase) && ok;
+    phase ^= 1;
+    tc::fence_after_sync();
+  };
+  constexpr int kHalf = RP / 2;       // columns of a half
+  constexpr uint32_t kSmall = 128;    // TMEM column of the small products of A and A A
+  for (int step = 0; step < a.steps; ++step) {
+    if (t == 0) {
+      constexpr uint32_t idesc = idesc_f16(128, RP, false);
+      for (int k = 0; k < mine * 4; ++k) {
+        const uint32_t off = (uint32_t)(k >> 2) * kChunk + (k & 3) * 32;
+        const uint64_t h = tc::desc_sw128(sxh + off, 16, 1024), l = tc::desc_sw128(sxl + off, 16, 1024);
+        tc::mma_bf16(tmem, h, h, idesc, k != 0);
+        tc::mma_bf16(tmem + kSmall, h, l, idesc, k != 0);
+        tc::mma_bf16(tmem + kSmall, l, h, idesc, 1);
+      }
+      tc::mma_commit(done);
+    }
+    __syncwarp();
+    finish();
+    constexpr float kToA = kSa / (kSx * kSx);
+    if (S > 1) {
+      const int blk = RP / S;
+      if (live) {
+        for (int c = side * kHalf; c < (side + 1) * kHalf; c += 16) {
+          float v[16];
+          drain16(tw + c, tw + kSmall + c, v);
+#pragma unroll
+          for (int i = 0; i < 16; ++i) {
+            const int col = c + i, dst = col / blk;
+            st_remote(at_rank(tc::smem_u32(recv + (q * blk + col % blk) * RP + row), dst), v[i]);
+          }
+        }
+      }
+      cluster_sync();
+      // rows q * blk .. of A (A is symmetric), 8 columns a task, to every CTA
+      for (int task = t; task < blk * (RP / 8); task += kSmallThreads) {
+        const int j = task / (RP / 8), i0 = (task % (RP / 8)) * 8;
+        float v[8];
+#pragma unroll
+        for (int i = 0; i < 8; ++i) v[i] = 0.0f;
+        for (int k = 0; k < S; ++k) {
+          const float4* p = reinterpret_cast<const float4*>(recv + (k * blk + j) * RP + i0);
+          const float4 x = p[0], y = p[1];
+          v[0] += x.x;
+          v[1] += x.y;
+          v[2] += x.z;
+          v[3] += x.w;
+          v[4] += y.x;
+          v[5] += y.y;
+          v[6] += y.z;
+          v[7] += y.w;
+        }
+#pragma unroll
+        for (int i = 0; i < 8; ++i) v[i] *= kToA;
+        uint4 hi, lo;
+        split8(v, hi, lo);
+        const uint32_t off = (uint32_t)(i0 / 64) * kChunk + sw128(q * blk + j, (i0 % 64) * 2);
+        for (int k = 0; k < S; ++k) {
+          st_remote(at_rank(sah + off, k), hi);
+          st_remote(at_rank(sal + off, k), lo);
+        }
+      }
+      fence_proxy_async_all();
+      tc::fence_before_sync();
+      cluster_sync();
+      tc::fence_after_sync();
+      fence_proxy_async_all();
+    } else {
+      if (live) {
+        for (int c = side * kHalf; c < (side + 1) * kHalf; c += 16) {
+          float v[16];
+          drain16(tw + c, tw + kSmall + c, v);
+#pragma unroll
+          for (int h = 0; h < 2; ++h) {
+            float w[8];
+#pragma unroll
+            for (int i = 0; i < 8; ++i) w[i] = v[8 * h + i] * kToA;
+            uint4 hi, lo;
+            split8(w, hi, lo);
+            const uint32_t off = (uint32_t)(c / 64) * kChunk + sw128(row, (c % 64 + 8 * h) * 2);
+            *reinterpret_cast<uint4*>(ah + off) = hi;
+            *reinterpret_cast<uint4*>(al + off) = lo;
+          }
+        }
+      }
+      tc::fence_proxy_async();
+      tc::fence_before_sync();
+      __syncthreads();
+      tc::fence_after_sync();
+    }
+    if (t == 0) {
+      constexpr uint32_t idesc = idesc_f16(128, RP, false);
+      for (int k = 0; k < RP / 16; ++k) {
+        const uint32_t off = (uint32_t)(k >> 2) * kChunk + (k & 3) * 32;
+        const uint64_t h = tc::desc_sw128(sah + off, 16, 1024), l = tc::desc_sw128(sal + off, 16, 1024);
+        tc::mma_bf16(tmem, h, h, idesc, k != 0);
+        tc::mma_bf16(tmem + kSmall, h, l, idesc, k != 0);
+        tc::mma_bf16(tmem + kSmall, l, h, idesc, 1);
+      }
+      tc::mma_commit(done);
+    }
+    __syncwarp();
+    finish();
+    if (live) {
+      for (int c = side * kHalf; c < (side + 1) * kHalf; c += 16) {
+        float v[16];
+        drain16(tw + c, tw + kSmall + c, v);
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+          const uint32_t off = (uint32_t)(c / 64) * kChunk + sw128(row, (c % 64 + 8 * h) * 2);
+          float w[8];
+          join8(*reinterpret_cast<const uint4*>(ah + off), *reinterpret_cast<const uint4*>(al + off), w);
+#pragma unroll
+          for (int i = 0; i < 8; ++i)
+            w[i] = kSb * fmaf(a.c, v[8 * h + i] * (1.0f / (kSa * kSa)),
+                              fmaf(a.b, w[i] * (1.0f / kSa), row == c + 8 * h + i ? a.a : 0.0f));
+          uint4 hi, lo;
+          split8(w, hi, lo);
+          *reinterpret_cast<uint4*>(ah + off) = hi;
+          *reinterpret_cast<uint4*>(al + off) = lo;
+        }
+      }
+    }
+    tc::fence_proxy_async();
+    tc::fence_before_sync();
+    __syncthreads();
+    tc::fence_after_sync();
+    const bool last = step + 1 == a.steps;
+    for (int g0 = 0; g0 < mine; g0 += 4) {  // up to 256 columns at a time
+      const int gn = min(4, mine - g0), cols = gn * 64;
+      if (t == 0) {
+        const uint32_t idesc = idesc_f16(128, cols, true);
+        for (int k = 0; k < RP / 16; ++k) {
+          const uint32_t poff = (uint32_t)(k >> 2) * kChunk + (k & 3) * 32, qoff = (uint32_t)g0 * kChunk + k * 2048;
+          const uint64_t bh = tc::desc_sw128(sah + poff, 16, 1024), bl = tc::desc_sw128(sal + poff, 16, 1024);
+          const uint64_t yh = tc::desc_sw128(sxh + qoff, kChunk, 1024), yl = tc::desc_sw128(sxl + qoff, kChunk, 1024);
+          tc::mma_bf16(tmem, bh, yh, idesc, k != 0);
+          tc::mma_bf16(tmem + 256, bh, yl, idesc, k != 0);
+          tc::mma_bf16(tmem + 256, bl, yh, idesc, 1);
+        }
+        tc::mma_commit(done);
+      }
+      __syncwarp();
+      finish();
+      if (live) {
+        for (int c = side * (cols / 2); c < (side + 1) * (cols / 2); c += 16) {
+          float v[16];
+          drain16(tw + c, tw + 256 + c, v);
+          const int l0 = (c_lo + g0) * 64 + c;
+          if (!last) {
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+              float w[8];
+#pragma unroll
+              for (int i = 0; i < 8; ++i) w[i] = v[8 * h + i] * (1.0f / kSb);
+              uint4 hi, lo;
+              split8(w, hi, lo);
+              const uint32_t off = (uint32_t)(g0 + c / 64) * kChunk + sw128(row, (c % 64 + 8 * h) * 2);
+              *reinterpret_cast<uint4*>(xh + off) = hi;
+              *reinterpret_cast<uint4*>(xl + off) = lo;
+            }
+          } else if (row < s.R && ok) {
+            T* out = static_cast<T*>(ptr.out[tn]) + base;
+            const T* w = a.r.step ? static_cast<const T*>(ptr.w[tn]) + base : nullptr;
+#pragma unroll
+            for (int i = 0; i < 16; ++i) {
+              if (l0 + i >= s.L) break;
+              const size_t at = index(row, l0 + i);
+              float o = v[i] * (1.0f / (kSb * kSx));
+              if (a.r.step) o = fmaf(a.r.keep, to_f32(w[at]), -a.r.rate * o);
+              out[at] = from_f32<T>(o);
+            }
+          }
+        }
+      }
+      tc::fence_proxy_async();
+      tc::fence_before_sync();
+      __syncthreads();
+      tc::fence_after_sync();
+    }
+  }
+  if (warp == 0) tc::tmem_dealloc(tmem, 512);
+}
+
 // ------------------------------------------------------------------ host side
 
 int up(int v, int to) { return (v + to - 1) / to * to; }
@@ -419,8 +815,61 @@ cudaError_t product(const CUtensorMap& p, const CUtensorMap& q, const Pointers& 
   return cudaGetLastError();
 }
 
+struct SmallPlan {
+  bool ok = false;
+  int S = 0, nc = 0, max_chunks = 0, rp = 0;
+  size_t smem = 0;
+};
+
+// The one-launch form serves up to 128 rows whose columns fit the shared memory of a cluster.  The
+// cluster is as large as the GPU has SMs for all matrices, and no smaller than what holds a matrix.
+SmallPlan small_plan(const Shape& s, int sms) {
+  SmallPlan p;
+  if (s.R > 128) return p;
+  p.rp = s.R <= 64 ? 64 : 128;
+  p.nc = (s.L + 63) / 64;
+  for (int S = 1; S <= kSmallMaxCluster && S <= p.nc; S *= 2) {
+    const int most = (p.nc + S - 1) / S;
+    const size_t smem = small_layout(p.rp, S, most).total + 1024;
+    if (smem > kSmallSmem) continue;
+    if (p.ok && (long long)s.nm * S > sms) break;
+    p.ok = true;
+    p.S = S;
+    p.max_chunks = most;
+    p.smem = std::max(smem, kSmallLeast);
+  }
+  return p;
+}
+
+template <typename T, int RP>
+cudaError_t run_small(const Pointers& ptr, const SmallArgs& a, size_t smem, cudaStream_t st) {
+  auto k = ns_small_kernel<T, RP>;
+  cudaError_t e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+  if (e != cudaSuccess) return e;
+  cudaLaunchConfig_t cfg{};
+  cfg.gridDim = dim3((unsigned)(a.s.nm * a.S));
+  cfg.blockDim = dim3(kSmallThreads);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = st;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeClusterDimension;
+  attr[0].val.clusterDim.x = (unsigned)a.S;
+  attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  e = cudaLaunchKernelEx(&cfg, k, ptr, a);
+  count_launch();
+  return e != cudaSuccess ? e : cudaGetLastError();
+}
+
+cudaError_t sm_count(int* sms) {
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  return e != cudaSuccess ? e : cudaDeviceGetAttribute(sms, cudaDevAttrMultiProcessorCount, dev);
+}
+
 template <typename T>
-cudaError_t run_chunk(const MuonArgs& a, int t0, int n, char* ws, cudaStream_t st) {
+cudaError_t run_chunk(const MuonArgs& a, int t0, int n, char* ws, int sms, cudaStream_t st) {
   const Shape s = shape_of(n, a.groups, a.rows, a.cols);
   const Layout l = layout_of(s);
   Pointers ptr{};
@@ -434,6 +883,11 @@ cudaError_t run_chunk(const MuonArgs& a, int t0, int n, char* ws, cudaStream_t s
     }
   }
   Rule r{a.step, a.nesterov, a.momentum, a.keep, a.rate};
+  const SmallPlan sp = small_plan(s, sms);
+  if (sp.ok) {
+    const SmallArgs g{s, r, a.a, a.b, a.c, a.eps, a.steps, sp.S, sp.nc, sp.max_chunks};
+    return sp.rp == 64 ? run_small<T, 64>(ptr, g, sp.smem, st) : run_small<T, 128>(ptr, g, sp.smem, st);
+  }
   __half* x[2] = {reinterpret_cast<__half*>(ws + l.x[0]), reinterpret_cast<__half*>(ws + l.x[1])};
   __half* am = reinterpret_cast<__half*>(ws + l.a);
   __half* bm = reinterpret_cast<__half*>(ws + l.b);
@@ -490,10 +944,13 @@ size_t muon_workspace(int n, int groups, int rows, int cols) {
 }
 
 cudaError_t launch_muon(const MuonArgs& a, void* workspace, cudaStream_t st) {
+  int sms = 0;
+  cudaError_t q = sm_count(&sms);
+  if (q != cudaSuccess) return q;
   for (int t0 = 0; t0 < a.n; t0 += kTensors) {
     const int n = std::min(kTensors, a.n - t0);
     char* ws = static_cast<char*>(workspace);
-    cudaError_t e = a.bf16 ? run_chunk<__nv_bfloat16>(a, t0, n, ws, st) : run_chunk<float>(a, t0, n, ws, st);
+    cudaError_t e = a.bf16 ? run_chunk<__nv_bfloat16>(a, t0, n, ws, sms, st) : run_chunk<float>(a, t0, n, ws, sms, st);
     if (e != cudaSuccess) return e;
   }
   return cudaSuccess;

@@ -13,7 +13,7 @@ from __future__ import annotations
 import torch
 
 from . import disco as D
-from .conv import _dtype_code, _need_cuda, _ptr, _shape, _stream
+from ._launch import DTYPES, dense, launch, like
 
 COEFFICIENTS = (3.4445, -4.7750, 2.0315)
 
@@ -53,18 +53,16 @@ def orthogonalize(update, groups: int = 1, steps: int = 5, coefficients=COEFFICI
     X = U / (|U| + eps), then `steps` times X <- a X + b (X X^T) X + c (X X^T)^2 X."""
     ts, single = _as_list(update, "update")
     for t in ts:
-        _need_cuda(t)
+        dense(t, "update")
         _matrix(t, groups)
-        _dtype_code(t)
     ns = D.newton_schulz(steps, coefficients, eps)
     outs = [torch.empty_like(t, requires_grad=False) for t in ts]
     for at in _buckets(ts):
         first = ts[at[0]]
         rows, cols = _matrix(first, groups)
         ws, nb = _workspace(len(at), groups, rows, cols, first.device)
-        with torch.cuda.device(first.device):
-            D.disco_orthogonalize(groups, rows, cols, _dtype_code(first), ns, [_ptr(ts[i]) for i in at],
-                                  [_ptr(outs[i]) for i in at], _ptr(ws), nb, _stream(first.device))
+        launch(first, D.disco_orthogonalize, groups, rows, cols, DTYPES[first.dtype], ns, [ts[i].data_ptr() for i in at],
+               [outs[i].data_ptr() for i in at], ws.data_ptr(), nb)
     return outs[0] if single else outs
 
 
@@ -81,17 +79,14 @@ def muon_update(weight, grad, momentum_buffer, lr: float, momentum: float = 0.95
     if not len(ws_) == len(gs) == len(ms):
         raise ValueError(f"{len(ws_)} weights, {len(gs)} gradients and {len(ms)} momentum buffers")
     for w, g, m in zip(ws_, gs, ms):
-        _need_cuda(w, g)
-        _need_cuda(m)
+        dense(w, "weight")
         _matrix(w, groups)
-        _dtype_code(w)
-        _shape(g, w.shape, "grad")
-        _shape(m, w.shape, "momentum_buffer")
+        like(g, w, w.shape, "grad")
         if m.dtype != torch.float32:
             raise TypeError(f"momentum_buffer is float32, not {m.dtype}")
-        if not w.device == g.device == m.device:
-            raise ValueError("weight, grad and momentum_buffer lie on different devices")
-    if inplace and len({_ptr(t) for t in ws_ + ms}) < 2 * len(ws_):
+        if not m.is_contiguous() or m.shape != w.shape or m.device != w.device:
+            raise ValueError("momentum_buffer is contiguous, of the weight's shape, on its device")
+    if inplace and len({t.data_ptr() for t in ws_ + ms}) < 2 * len(ws_):
         raise ValueError("a tensor is given twice: each is updated once")
     ns = D.newton_schulz(steps, coefficients, eps)
     w_out = ws_ if inplace else [torch.empty_like(t, requires_grad=False) for t in ws_]
@@ -100,10 +95,9 @@ def muon_update(weight, grad, momentum_buffer, lr: float, momentum: float = 0.95
         first = ws_[at[0]]
         rows, cols = _matrix(first, groups)
         ws, nb = _workspace(len(at), groups, rows, cols, first.device)
-        ptrs = [[_ptr(ts[i]) for i in at] for ts in (ws_, gs, ms, w_out, m_out)]
-        with torch.cuda.device(first.device):
-            D.disco_muon(groups, rows, cols, _dtype_code(first), ns, float(lr), float(momentum), nesterov,
-                         float(weight_decay), *ptrs, _ptr(ws), nb, _stream(first.device))
+        ptrs = [[ts[i].data_ptr() for i in at] for ts in (ws_, gs, ms, w_out, m_out)]
+        launch(first, D.disco_muon, groups, rows, cols, DTYPES[first.dtype], ns, lr, momentum, nesterov, weight_decay,
+               *ptrs, ws.data_ptr(), nb)
     return (w_out[0], m_out[0]) if single else (w_out, m_out)
 
 
@@ -122,7 +116,8 @@ class Muon(torch.optim.Optimizer):
         for group in self.param_groups:
             for p in group["params"]:
                 _matrix(p, group["groups"])
-                _dtype_code(p)
+                if p.dtype not in DTYPES:
+                    raise TypeError(f"unsupported dtype {p.dtype}; use float32 or bfloat16")
                 if not p.is_contiguous():
                     raise ValueError("Muon takes contiguous parameters")
 

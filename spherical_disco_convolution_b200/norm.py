@@ -13,40 +13,27 @@ import math
 import torch
 
 from . import disco as D
-from .conv import _dtype_code, _need_cuda, _ptr, _shape, _stream
+from ._launch import dense, launch, like
 
 
-def _one_device(*ts):
-    devs = {t.device for t in ts if t is not None}
-    if len(devs) > 1:
-        raise ValueError(f"tensors on several devices: {sorted(map(str, devs))}")
-
-
-def _field(x):
-    if x.dim() < 2 or x.numel() == 0:
-        raise ValueError(f"x has shape {tuple(x.shape)}, expected (B, C, *points) without an empty axis")
-    return x.shape[0], x.shape[1], math.prod(x.shape[2:])
-
-
-def _stats_shape(x):
-    return (2, x.shape[0]) + tuple(x.shape[2:])
+def _sizes(x):
+    shape = x.shape
+    if len(shape) < 2 or x.numel() == 0:
+        raise ValueError(f"x has shape {tuple(shape)}, expected (B, C, *points) without an empty axis")
+    return shape[0], shape[1], math.prod(shape[2:])
 
 
 def layer_norm(x: torch.Tensor, gain=None, bias=None, eps: float = 1e-5):
     """(out, stats) of x (B, C, *points): out = gain * (x - mean) * r + bias with mean and r =
     1 / sqrt(var + eps) over the channels of each point; stats (2, B, *points) holds mean and r in
     fp32, which layer_norm_backward takes.  gain and bias are (C,), in x's type, or None."""
-    _need_cuda(x, gain, bias)
-    _one_device(x, gain, bias)
-    B, C, n = _field(x)
-    _shape(gain, (C,), "gain")
-    _shape(bias, (C,), "bias")
-    dt = _dtype_code(x)
+    code = dense(x, "x")
+    B, C, n = _sizes(x)
+    gain = like(gain, x, (C,), "gain")
+    bias = like(bias, x, (C,), "bias")
     out = torch.empty_like(x)
-    stats = torch.empty(_stats_shape(x), dtype=torch.float32, device=x.device)
-    with torch.cuda.device(x.device):
-        D.disco_norm(B, C, n, dt, _ptr(x), _ptr(gain), _ptr(bias), float(eps), _ptr(out), _ptr(stats),
-                     _stream(x.device))
+    stats = torch.empty((2, B, *x.shape[2:]), dtype=torch.float32, device=x.device)
+    launch(x, D.disco_norm, B, C, n, code, x.data_ptr(), gain, bias, eps, out.data_ptr(), stats.data_ptr())
     return out, stats
 
 
@@ -54,27 +41,25 @@ def layer_norm_backward(dout: torch.Tensor, x: torch.Tensor, stats: torch.Tensor
                         need_gain: bool = True, need_bias: bool = True):
     """(dx, dgain, dbias) of layer_norm from the field it took and the stats it returned; None for
     each one not needed."""
-    _need_cuda(dout, x, gain)
-    _one_device(dout, x, stats, gain)
-    B, C, n = _field(x)
-    _shape(dout, x.shape, "dout")
-    _shape(gain, (C,), "gain")
-    _shape(stats, _stats_shape(x), "stats")
-    if stats.dtype != torch.float32 or not stats.is_contiguous():
-        raise ValueError("stats is the contiguous fp32 tensor that layer_norm returned")
+    code = dense(x, "x")
+    B, C, n = _sizes(x)
+    dout = like(dout, x, x.shape, "dout")
+    gain = like(gain, x, (C,), "gain")
+    if stats.dtype != torch.float32 or not stats.is_contiguous() or stats.device != x.device or \
+            stats.shape != (2, B, *x.shape[2:]):
+        raise ValueError("stats is the contiguous fp32 tensor (2, B, *points) that layer_norm returned")
     if not (need_input or need_gain or need_bias):
         return None, None, None
-    dt = _dtype_code(x)
     dx = torch.empty_like(x) if need_input else None
-    dgain = torch.empty((C,), dtype=x.dtype, device=x.device) if need_gain else None
-    dbias = torch.empty((C,), dtype=x.dtype, device=x.device) if need_bias else None
+    dgain = x.new_empty(C) if need_gain else None
+    dbias = x.new_empty(C) if need_bias else None
     ws, nb = None, 0
     if need_gain or need_bias:
-        nb = D.disco_norm_workspace_size(B, C, n, dt)
+        nb = D.disco_norm_workspace_size(B, C, n, code)
         ws = torch.empty(nb, dtype=torch.uint8, device=x.device)
-    with torch.cuda.device(x.device):
-        D.disco_norm_backward(B, C, n, dt, _ptr(dout), _ptr(x), _ptr(stats), _ptr(gain), _ptr(dx), _ptr(dgain),
-                              _ptr(dbias), _ptr(ws), nb, _stream(x.device))
+    launch(x, D.disco_norm_backward, B, C, n, code, dout, x.data_ptr(), stats.data_ptr(), gain,
+           None if dx is None else dx.data_ptr(), None if dgain is None else dgain.data_ptr(),
+           None if dbias is None else dbias.data_ptr(), None if ws is None else ws.data_ptr(), nb)
     return dx, dgain, dbias
 
 
