@@ -9,9 +9,10 @@
 // in its direction with it: an X rounded to 8 or 11 bits would leave the weak directions of an
 // update wrong by per cents.  So every matrix is kept as an fp16 pair hi + lo (22 bits) under a
 // power-of-two scale, and a product takes three MMAs, hi hi + hi lo + lo hi; what is left out,
-// lo lo, is below 2^-22.  The two small products go into an accumulator of their own, and no
-// accumulator runs over more than 512 values of a sum of squares (kMaxChain), because the tensor
-// core cuts what it adds instead of rounding it.  Scales: X by 2^12, A by 2^11, B by 2^9, so
+// lo lo, is below 2^-22.  The two small products go into an accumulator of their own.  The tensor
+// core cuts what it adds to an accumulator instead of rounding it (chains of 512 values left a
+// 1024 x 9216 result 3.5e-5 off, 8 times fp32's error), so the large product is taken out and
+// added in registers every 64 to 192 values.  Scales: X by 2^12, A by 2^11, B by 2^9, so
 // that |X| <= 16, |A| <= 32, |B| <= 128 stay finite in fp16; lo by 2^11 more, which puts it at hi's
 // size, so that it keeps its bits for entries far below the largest.
 #include <cuda.h>
@@ -30,7 +31,7 @@ namespace {
 constexpr float kSx = 4096.0f, kSa = 2048.0f, kSb = 512.0f, kSl = 2048.0f;
 constexpr int kTile = 128;       // output tile of a product
 constexpr int kBk = 64;          // K values per stage: one 128-byte swizzle row of fp16
-constexpr int kMaxChain = 512;   // K values of one accumulation of X X^T
+constexpr int kMaxChain = 512;   // K values of one partial product of X X^T
 constexpr int kStages = 3;
 constexpr uint32_t kOperand = kTile * 128;   // one [128][64] fp16 operand tile, bytes
 constexpr uint32_t kStageBytes = 4 * kOperand;
@@ -189,11 +190,12 @@ __device__ __forceinline__ void store16(__half* hi, __half* lo, const float (&v)
 }
 
 // One 128 x 128 tile of a product of hi + lo matrices: D = P Q^T (kGram, kSquare; both K-major)
-// or D = P Q (kUpdate, kFinal; Q is read as an MN-major operand).  Warp 4 streams the four operand
-// tiles of each K chunk by TMA, warp 5 issues the MMAs, warps 0..3 drain the accumulators (TMEM
-// lane = row of the tile).
+// or D = P Q (kUpdate, kFinal; Q is read as an MN-major operand).  Warp 8 streams the four operand
+// tiles of each K chunk by TMA, warp 9 issues the MMAs, warps 0..7 add the chunk's large product
+// to their sums (TMEM lane = row of the tile, warps 0..3 the first 64 columns) while the MMAs of
+// its small products run.
 template <typename T, Product MODE>
-__global__ void __launch_bounds__(192, 1) ns_product_kernel(const __grid_constant__ CUtensorMap map_p,
+__global__ void __launch_bounds__(320, 1) ns_product_kernel(const __grid_constant__ CUtensorMap map_p,
                                                             const __grid_constant__ CUtensorMap map_q,
                                                             const __grid_constant__ Pointers ptr,
                                                             const __grid_constant__ ProductArgs a) {
@@ -201,7 +203,9 @@ __global__ void __launch_bounds__(192, 1) ns_product_kernel(const __grid_constan
   uint8_t* smem = align1024(smem_raw);
   uint64_t* full = reinterpret_cast<uint64_t*>(smem + kStages * kStageBytes);
   uint64_t* empty = full + kStages;
-  uint64_t* done = empty + kStages;
+  uint64_t* tfull = empty + kStages;  // the chunk's large product is in TMEM
+  uint64_t* tempty = tfull + 1;       // and has been read
+  uint64_t* done = tempty + 1;
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(done + 1);
   constexpr bool kMn = MODE == kUpdate || MODE == kFinal;
   const Shape& s = a.s;
@@ -217,10 +221,12 @@ __global__ void __launch_bounds__(192, 1) ns_product_kernel(const __grid_constan
       tc::mbar_init(&full[i], 1);
       tc::mbar_init(&empty[i], 1);
     }
+    tc::mbar_init(tfull, 1);
+    tc::mbar_init(tempty, 8);
     tc::mbar_init(done, 1);
     tc::fence_barrier_init();
   }
-  if (warp == 5) {
+  if (warp == 9) {
     tc::tmem_alloc(tmem_slot, 2 * kTile);
     tc::tmem_relinquish();
   }
@@ -229,7 +235,7 @@ __global__ void __launch_bounds__(192, 1) ns_product_kernel(const __grid_constan
   tc::fence_after_sync();
   const uint32_t tmem = *tmem_slot;
 
-  if (warp == 4 && lane == 0) {
+  if (warp == 8 && lane == 0) {
     for (int k = k_lo; k < k_hi; ++k) {
       const int i = k - k_lo, st = i % kStages;
       if (i >= kStages && !tc::mbar_wait(&empty[st], ((i / kStages) & 1) ^ 1)) break;
@@ -248,56 +254,78 @@ __global__ void __launch_bounds__(192, 1) ns_product_kernel(const __grid_constan
         }
       }
     }
-  } else if (warp == 5 && lane == 0) {
+  } else if (warp == 9 && lane == 0) {
     constexpr uint32_t idesc = idesc_f16(kTile, kTile, kMn);
     for (int k = k_lo; k < k_hi; ++k) {
       const int i = k - k_lo, st = i % kStages;
       if (!tc::mbar_wait(&full[st], (i / kStages) & 1)) break;
+      if (i > 0 && !tc::mbar_wait(tempty, (i & 1) ^ 1)) break;
       tc::fence_after_sync();
       const uint32_t p0 = tc::smem_u32(smem + st * kStageBytes), q0 = p0 + 2 * kOperand;
+      auto pd = [&](int plane, int kk) { return tc::desc_sw128(p0 + plane * kOperand + kk * 32, 16, 1024); };
+      auto qd = [&](int plane, int kk) {
+        return kMn ? tc::desc_sw128(q0 + plane * kOperand + kk * 2048, kOperand / 2, 1024)
+                   : tc::desc_sw128(q0 + plane * kOperand + kk * 32, 16, 1024);
+      };
+#pragma unroll
+      for (int kk = 0; kk < kBk / 16; ++kk) tc::mma_bf16(tmem, pd(0, kk), qd(0, kk), idesc, kk != 0);
+      tc::mma_commit(tfull);
 #pragma unroll
       for (int kk = 0; kk < kBk / 16; ++kk) {
-        const uint64_t ph = tc::desc_sw128(p0 + kk * 32, 16, 1024);
-        const uint64_t pl = tc::desc_sw128(p0 + kOperand + kk * 32, 16, 1024);
-        const uint64_t qh = kMn ? tc::desc_sw128(q0 + kk * 2048, kOperand / 2, 1024)
-                                : tc::desc_sw128(q0 + kk * 32, 16, 1024);
-        const uint64_t ql = kMn ? tc::desc_sw128(q0 + kOperand + kk * 2048, kOperand / 2, 1024)
-                                : tc::desc_sw128(q0 + kOperand + kk * 32, 16, 1024);
-        const uint32_t more = (i | kk) != 0;
-        tc::mma_bf16(tmem, ph, qh, idesc, more);
-        tc::mma_bf16(tmem + kTile, ph, ql, idesc, more);
-        tc::mma_bf16(tmem + kTile, pl, qh, idesc, 1);
+        tc::mma_bf16(tmem + kTile, pd(0, kk), qd(1, kk), idesc, (i | kk) != 0);
+        tc::mma_bf16(tmem + kTile, pd(1, kk), qd(0, kk), idesc, 1);
       }
       tc::mma_commit(&empty[st]);
     }
     tc::mma_commit(done);
   }
   __syncwarp();
-  if (warp < 4) {
-    const bool ok = tc::mbar_wait(done, 0);
-    tc::fence_after_sync();
-    const int row = m0 + warp * 32 + lane;
-    const uint32_t tw = tmem + ((uint32_t)(warp * 32) << 16);
-    if (ok) {
-      for (int c = 0; c < kTile; c += 16) {
-        float v[16], e[16];
-        tc::tmem_ld16(tw + c, v);
-        tc::tmem_ld16(tw + kTile + c, e);
+  if (warp < 8) {
+    const int quarter = (warp & 3) * 32, c0 = (warp >> 2) * 64;
+    const int row = m0 + quarter + lane;
+    const uint32_t tw = tmem + ((uint32_t)quarter << 16) + c0;
+    float acc[64];
 #pragma unroll
-        for (int i = 0; i < 16; ++i) v[i] = fmaf(e[i], 1.0f / kSl, v[i]);
-        const int col = n0 + c;
+    for (int i = 0; i < 64; ++i) acc[i] = 0.0f;
+    bool ok = true;
+    for (int i = 0; i < k_hi - k_lo && ok; ++i) {
+      ok = tc::mbar_wait(tfull, i & 1);
+      tc::fence_after_sync();
+      uint32_t v[64];
+      tc::tmem_ld_chunks<4>(tw, v);
+      tc::fence_before_sync();
+      __syncwarp();
+      if (lane == 0) tc::mbar_arrive(tempty);
+#pragma unroll
+      for (int c = 0; c < 64; ++c) acc[c] += __uint_as_float(v[c]);
+    }
+    ok = ok && tc::mbar_wait(done, 0);
+    tc::fence_after_sync();
+    if (ok) {
+      {
+        uint32_t v[64];
+        tc::tmem_ld_chunks<4>(tw + kTile, v);
+#pragma unroll
+        for (int c = 0; c < 64; ++c) acc[c] = fmaf(__uint_as_float(v[c]), 1.0f / kSl, acc[c]);
+      }
+#pragma unroll
+      for (int c = 0; c < 64; c += 16) {
+        float v[16];
+#pragma unroll
+        for (int i = 0; i < 16; ++i) v[i] = acc[c + i];
+        const int col = n0 + c0 + c;
         if constexpr (MODE == kGram) {
           float4* dst = reinterpret_cast<float4*>(a.part + (((size_t)split_k * s.nm + mi) * s.Rp + row) * s.Rp + col);
 #pragma unroll
           for (int i = 0; i < 4; ++i) dst[i] = make_float4(v[4 * i], v[4 * i + 1], v[4 * i + 2], v[4 * i + 3]);
         } else if constexpr (MODE == kSquare) {
           const size_t plane = (size_t)s.nm * s.Rp * s.Rp, at = ((size_t)mi * s.Rp + row) * s.Rp + col;
-          float ah[16], al[16];
-          load16(a.am + at, ah);
-          load16(a.am + plane + at, al);
+          float xh[16], xl[16];
+          load16(a.am + at, xh);
+          load16(a.am + plane + at, xl);
 #pragma unroll
           for (int i = 0; i < 16; ++i) {
-            const float av = fmaf(al[i], 1.0f / kSl, ah[i]) * (1.0f / kSa);
+            const float av = fmaf(xl[i], 1.0f / kSl, xh[i]) * (1.0f / kSa);
             v[i] = kSb * fmaf(a.c, v[i] * (1.0f / (kSa * kSa)), fmaf(a.b, av, row == col + i ? a.a : 0.0f));
           }
           store16(a.dst + at, a.dst + plane + at, v);
@@ -325,7 +353,7 @@ __global__ void __launch_bounds__(192, 1) ns_product_kernel(const __grid_constan
     tc::fence_before_sync();
   }
   __syncthreads();
-  if (warp == 5) tc::tmem_dealloc(tmem, 2 * kTile);
+  if (warp == 9) tc::tmem_dealloc(tmem, 2 * kTile);
 }
 
 // A from the partial products of X X^T, in a fixed order.
@@ -810,7 +838,7 @@ cudaError_t product(const CUtensorMap& p, const CUtensorMap& q, const Pointers& 
   auto k = ns_product_kernel<T, MODE>;
   cudaError_t e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kProductSmem);
   if (e != cudaSuccess) return e;
-  k<<<dim3(a.s.Rp / kTile * a.tn, a.s.nm, a.S), 192, kProductSmem, st>>>(p, q, ptr, a);
+  k<<<dim3(a.s.Rp / kTile * a.tn, a.s.nm, a.S), 320, kProductSmem, st>>>(p, q, ptr, a);
   count_launch();
   return cudaGetLastError();
 }
