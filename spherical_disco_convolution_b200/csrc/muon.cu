@@ -29,12 +29,15 @@ namespace disco {
 namespace {
 
 constexpr float kSx = 4096.0f, kSa = 2048.0f, kSb = 512.0f, kSl = 2048.0f;
-constexpr int kTile = 128;       // output tile of a product
+constexpr int kTile = 128;       // a CTA's rows of a product's tile, and its share of the operands
+constexpr int kPairTile = 256;   // the tile of a pair of CTAs
 constexpr int kBk = 64;          // K values per stage: one 128-byte swizzle row of fp16
-constexpr int kMaxChain = 512;   // K values of one partial product of X X^T
+constexpr int kMaxSplits = 8;    // of the K range of a symmetric product
 constexpr int kStages = 3;
 constexpr uint32_t kOperand = kTile * 128;   // one [128][64] fp16 operand tile, bytes
 constexpr uint32_t kStageBytes = 4 * kOperand;
+constexpr int kDrainWarps = 16;
+constexpr int kProductThreads = (kDrainWarps + 2) * 32;
 constexpr int kTensors = 64;     // tensors of one set of launches (pointers travel as arguments)
 constexpr int kNormBlocks = 32;  // partial sums of squares per matrix, at most
 
@@ -48,7 +51,7 @@ struct Pointers {
 
 struct Shape {
   int groups, rows, cols;
-  int R, L, Rp, Lp;  // iterated matrix (R <= L) and its padded sides, multiples of 128
+  int R, L, Rp, Lp;  // iterated matrix (R <= L) and its padded sides, multiples of kPairTile
   bool tr;           // iterated on the transposed matrix
   int nm;            // matrices
 };
@@ -145,15 +148,13 @@ __global__ void __launch_bounds__(256) ns_load_kernel(const __grid_constant__ Po
 
 // ------------------------------------------------------------------ the products
 
-enum Product { kGram, kSquare, kUpdate, kFinal };
+enum Product { kSymmetric, kUpdate, kFinal };
 
 struct ProductArgs {
   Shape s;
-  float a, b, c;
-  int tn, S, chunks, chunk0;  // tiles along N, splits along K, K chunks in all and per split
-  float* part;                // kGram: [S][nm][Rp][Rp]
-  const __half* am;           // kSquare: A planes
-  __half* dst;                // kSquare: B planes, kUpdate: the next X
+  int tm, tn, S, chunks;  // tiles along M and N, splits along K, K chunks in all
+  float* part;            // kGram, kSquare: [S][nm][Rp][Rp]
+  __half* dst;            // kUpdate: the next X
   Rule r;
 };
 
@@ -164,17 +165,6 @@ __device__ __forceinline__ uint8_t* align1024(uint8_t* p) {
 // Instruction descriptor: fp16 x fp16 -> fp32, M x N, A K-major.
 __host__ __device__ constexpr uint32_t idesc_f16(int M, int N, bool b_mn_major) {
   return (1u << 4) | ((b_mn_major ? 1u : 0u) << 16) | ((uint32_t)(N >> 3) << 17) | ((uint32_t)(M >> 4) << 24);
-}
-
-__device__ __forceinline__ void load16(const __half* p, float (&v)[16]) {
-  alignas(16) const uint4 q[2] = {reinterpret_cast<const uint4*>(p)[0], reinterpret_cast<const uint4*>(p)[1]};
-  const __half2* h = reinterpret_cast<const __half2*>(q);
-#pragma unroll
-  for (int i = 0; i < 8; ++i) {
-    const float2 f = __half22float2(h[i]);
-    v[2 * i] = f.x;
-    v[2 * i + 1] = f.y;
-  }
 }
 
 // 16 values as hi and lo, 32 bytes of each plane.
@@ -189,29 +179,85 @@ __device__ __forceinline__ void store16(__half* hi, __half* lo, const float (&v)
   }
 }
 
-// One 128 x 128 tile of a product of hi + lo matrices: D = P Q^T (kGram, kSquare; both K-major)
-// or D = P Q (kUpdate, kFinal; Q is read as an MN-major operand).  Warp 8 streams the four operand
-// tiles of each K chunk by TMA, warp 9 issues the MMAs, warps 0..7 add the chunk's large product
-// to their sums (TMEM lane = row of the tile, warps 0..3 the first 64 columns) while the MMAs of
-// its small products run.
+// A pair of CTAs (cta_group::2) makes one 256 x 256 tile of a product of hi + lo matrices:
+// D = P P^T (kSymmetric, both operands K-major, tiles on and above the diagonal only) or D = P Q
+// (kUpdate, kFinal; Q is read as an MN-major operand).  Each CTA brings 128 rows of P and 128 columns
+// of Q and gets 128 rows of D, so that 64 KB from L2 feed 1536 cycles of MMA: one CTA with a 128 x 128
+// tile needs 64 KB for 768, more than L2 gives (measured: 2.4x slower on 1024 x 9216).
+//
+// Warp 16 streams the four operand tiles of each K chunk by TMA, all counted on the first CTA's
+// barrier; lane 0 of the first CTA's warp 17 issues the MMAs for both; warps 0..15 of both CTAs add
+// the chunk's large product to their sums (TMEM lane = row of the tile, 64 columns a warp) while the
+// MMAs of its small products run.
+__device__ __forceinline__ uint32_t cluster_rank() {
+  uint32_t r;
+  asm volatile("mov.u32 %0, %cluster_ctarank;" : "=r"(r));
+  return r;
+}
+__device__ __forceinline__ void cluster_sync() {
+  asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
+}
+__device__ __forceinline__ uint32_t at_rank(uint32_t addr, uint32_t rank) {
+  uint32_t r;
+  asm("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(r) : "r"(addr), "r"(rank));
+  return r;
+}
+// The same box load, counted on a barrier of either CTA of the pair.
+__device__ __forceinline__ void pair_load_3d(void* dst, const CUtensorMap* map, uint32_t bar, int c0, int c1, int c2) {
+  asm volatile(
+      "cp.async.bulk.tensor.3d.cta_group::2.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1, {%3, %4, "
+      "%5}], [%2];" ::"r"(tc::smem_u32(dst)),
+      "l"(map), "r"(bar), "r"(c0), "r"(c1), "r"(c2)
+      : "memory");
+}
+__device__ __forceinline__ void pair_mma(uint32_t d_tmem, uint64_t adesc, uint64_t bdesc, uint32_t idesc,
+                                         uint32_t accumulate) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "setp.ne.b32 p, %4, 0;\n\t"
+      "tcgen05.mma.cta_group::2.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d_tmem),
+      "l"(adesc), "l"(bdesc), "r"(idesc), "r"(accumulate)
+      : "memory");
+}
+// Arrives on `bar` of both CTAs once every MMA this thread has issued is done.
+__device__ __forceinline__ void pair_commit(uint64_t* bar) {
+  asm volatile(
+      "tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], %1;" ::"r"(
+          tc::smem_u32(bar)),
+      "h"((uint16_t)3)
+      : "memory");
+}
+__device__ __forceinline__ void arrive_remote(uint32_t bar) {
+  asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(bar) : "memory");
+}
+
 template <typename T, Product MODE>
-__global__ void __launch_bounds__(320, 1) ns_product_kernel(const __grid_constant__ CUtensorMap map_p,
-                                                            const __grid_constant__ CUtensorMap map_q,
-                                                            const __grid_constant__ Pointers ptr,
-                                                            const __grid_constant__ ProductArgs a) {
+__global__ void __launch_bounds__(kProductThreads, 1) __cluster_dims__(2, 1, 1)
+    ns_product_kernel(const __grid_constant__ CUtensorMap map_p, const __grid_constant__ CUtensorMap map_q,
+                      const __grid_constant__ Pointers ptr, const __grid_constant__ ProductArgs a) {
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = align1024(smem_raw);
   uint64_t* full = reinterpret_cast<uint64_t*>(smem + kStages * kStageBytes);
   uint64_t* empty = full + kStages;
   uint64_t* tfull = empty + kStages;  // the chunk's large product is in TMEM
-  uint64_t* tempty = tfull + 1;       // and has been read
+  uint64_t* tempty = tfull + 1;       // and both CTAs have read it
   uint64_t* done = tempty + 1;
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(done + 1);
-  constexpr bool kMn = MODE == kUpdate || MODE == kFinal;
+  constexpr bool kMn = MODE != kSymmetric;
   const Shape& s = a.s;
-  const int n0 = (blockIdx.x % a.tn) * kTile, m0 = (blockIdx.x / a.tn) * kTile;
-  const int mi = blockIdx.y, split_k = blockIdx.z;
-  const int k_lo = split_k * a.chunk0, k_hi = min(a.chunks, k_lo + a.chunk0);
+  const uint32_t rank = cluster_rank();
+  int tile = (int)(blockIdx.x >> 1) / a.S, bm = 0, bn = 0;
+  const int split_k = (int)(blockIdx.x >> 1) % a.S;
+  if (MODE == kSymmetric) {
+    while (tile >= a.tn - bm) tile -= a.tn - bm++;
+    bn = bm + tile;
+  } else {
+    bm = tile % a.tm;
+    bn = tile / a.tm;
+  }
+  const int m0 = bm * kPairTile + (int)rank * kTile, n0 = bn * kPairTile, qn = n0 + (int)rank * kTile;
+  const int mi = blockIdx.y;
+  const int k_lo = a.chunks * split_k / a.S, k_hi = a.chunks * (split_k + 1) / a.S;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
 
   if (threadIdx.x == 0) {
@@ -222,25 +268,28 @@ __global__ void __launch_bounds__(320, 1) ns_product_kernel(const __grid_constan
       tc::mbar_init(&empty[i], 1);
     }
     tc::mbar_init(tfull, 1);
-    tc::mbar_init(tempty, 8);
+    tc::mbar_init(tempty, 2 * kDrainWarps);
     tc::mbar_init(done, 1);
     tc::fence_barrier_init();
   }
-  if (warp == 9) {
-    tc::tmem_alloc(tmem_slot, 2 * kTile);
-    tc::tmem_relinquish();
+  if (warp == kDrainWarps + 1) {
+    asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(tc::smem_u32(tmem_slot)),
+                 "r"(512u)
+                 : "memory");
+    asm volatile("tcgen05.relinquish_alloc_permit.cta_group::2.sync.aligned;" ::: "memory");
   }
   tc::fence_before_sync();
-  __syncthreads();
+  cluster_sync();
   tc::fence_after_sync();
   const uint32_t tmem = *tmem_slot;
 
-  if (warp == 8 && lane == 0) {
+  if (warp == kDrainWarps && lane == 0) {
     for (int k = k_lo; k < k_hi; ++k) {
       const int i = k - k_lo, st = i % kStages;
       if (i >= kStages && !tc::mbar_wait(&empty[st], ((i / kStages) & 1) ^ 1)) break;
       uint8_t* base = smem + st * kStageBytes;
-      tc::mbar_arrive_expect_tx(&full[st], kStageBytes);
+      const uint32_t bar = at_rank(tc::smem_u32(&full[st]), 0);
+      if (rank == 0) tc::mbar_arrive_expect_tx(&full[st], 2 * kStageBytes);
 #pragma unroll
       for (int pl = 0; pl < 2; ++pl) {
         const int z = pl * s.nm + mi;
@@ -248,14 +297,14 @@ __global__ void __launch_bounds__(320, 1) ns_product_kernel(const __grid_constan
         uint8_t* qq = base + (2 + pl) * kOperand;
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
-          tc::tma_load_3d(pp + h * (kOperand / 2), &map_p, &full[st], k * kBk, m0 + 64 * h, z);
-          if (kMn) tc::tma_load_3d(qq + h * (kOperand / 2), &map_q, &full[st], n0 + 64 * h, k * kBk, z);
-          else tc::tma_load_3d(qq + h * (kOperand / 2), &map_q, &full[st], k * kBk, n0 + 64 * h, z);
+          pair_load_3d(pp + h * (kOperand / 2), &map_p, bar, k * kBk, m0 + 64 * h, z);
+          if (kMn) pair_load_3d(qq + h * (kOperand / 2), &map_q, bar, qn + 64 * h, k * kBk, z);
+          else pair_load_3d(qq + h * (kOperand / 2), &map_q, bar, k * kBk, qn + 64 * h, z);
         }
       }
     }
-  } else if (warp == 9 && lane == 0) {
-    constexpr uint32_t idesc = idesc_f16(kTile, kTile, kMn);
+  } else if (warp == kDrainWarps + 1 && lane == 0 && rank == 0) {
+    constexpr uint32_t idesc = idesc_f16(kPairTile, kPairTile, kMn);
     for (int k = k_lo; k < k_hi; ++k) {
       const int i = k - k_lo, st = i % kStages;
       if (!tc::mbar_wait(&full[st], (i / kStages) & 1)) break;
@@ -268,22 +317,23 @@ __global__ void __launch_bounds__(320, 1) ns_product_kernel(const __grid_constan
                    : tc::desc_sw128(q0 + plane * kOperand + kk * 32, 16, 1024);
       };
 #pragma unroll
-      for (int kk = 0; kk < kBk / 16; ++kk) tc::mma_bf16(tmem, pd(0, kk), qd(0, kk), idesc, kk != 0);
-      tc::mma_commit(tfull);
+      for (int kk = 0; kk < kBk / 16; ++kk) pair_mma(tmem, pd(0, kk), qd(0, kk), idesc, kk != 0);
+      pair_commit(tfull);
 #pragma unroll
       for (int kk = 0; kk < kBk / 16; ++kk) {
-        tc::mma_bf16(tmem + kTile, pd(0, kk), qd(1, kk), idesc, (i | kk) != 0);
-        tc::mma_bf16(tmem + kTile, pd(1, kk), qd(0, kk), idesc, 1);
+        pair_mma(tmem + kPairTile, pd(0, kk), qd(1, kk), idesc, (i | kk) != 0);
+        pair_mma(tmem + kPairTile, pd(1, kk), qd(0, kk), idesc, 1);
       }
-      tc::mma_commit(&empty[st]);
+      pair_commit(&empty[st]);
     }
-    tc::mma_commit(done);
+    pair_commit(done);
   }
   __syncwarp();
-  if (warp < 8) {
+  if (warp < kDrainWarps) {
     const int quarter = (warp & 3) * 32, c0 = (warp >> 2) * 64;
     const int row = m0 + quarter + lane;
     const uint32_t tw = tmem + ((uint32_t)quarter << 16) + c0;
+    const uint32_t release = at_rank(tc::smem_u32(tempty), 0);
     float acc[64];
 #pragma unroll
     for (int i = 0; i < 64; ++i) acc[i] = 0.0f;
@@ -291,44 +341,33 @@ __global__ void __launch_bounds__(320, 1) ns_product_kernel(const __grid_constan
     for (int i = 0; i < k_hi - k_lo && ok; ++i) {
       ok = tc::mbar_wait(tfull, i & 1);
       tc::fence_after_sync();
-      uint32_t v[64];
-      tc::tmem_ld_chunks<4>(tw, v);
-      tc::fence_before_sync();
-      __syncwarp();
-      if (lane == 0) tc::mbar_arrive(tempty);
 #pragma unroll
-      for (int c = 0; c < 64; ++c) acc[c] += __uint_as_float(v[c]);
+      for (int h = 0; h < 64; h += 32) {
+        uint32_t v[32];
+        tc::tmem_ld_chunks<2>(tw + h, v);
+        if (h == 32) {
+          tc::fence_before_sync();
+          __syncwarp();
+          if (lane == 0) arrive_remote(release);
+        }
+#pragma unroll
+        for (int c = 0; c < 32; ++c) acc[h + c] += __uint_as_float(v[c]);
+      }
     }
     ok = ok && tc::mbar_wait(done, 0);
     tc::fence_after_sync();
     if (ok) {
-      {
-        uint32_t v[64];
-        tc::tmem_ld_chunks<4>(tw + kTile, v);
-#pragma unroll
-        for (int c = 0; c < 64; ++c) acc[c] = fmaf(__uint_as_float(v[c]), 1.0f / kSl, acc[c]);
-      }
 #pragma unroll
       for (int c = 0; c < 64; c += 16) {
         float v[16];
+        tc::tmem_ld16(tw + kPairTile + c, v);
 #pragma unroll
-        for (int i = 0; i < 16; ++i) v[i] = acc[c + i];
+        for (int i = 0; i < 16; ++i) v[i] = fmaf(v[i], 1.0f / kSl, acc[c + i]);
         const int col = n0 + c0 + c;
-        if constexpr (MODE == kGram) {
+        if constexpr (MODE == kSymmetric) {
           float4* dst = reinterpret_cast<float4*>(a.part + (((size_t)split_k * s.nm + mi) * s.Rp + row) * s.Rp + col);
 #pragma unroll
           for (int i = 0; i < 4; ++i) dst[i] = make_float4(v[4 * i], v[4 * i + 1], v[4 * i + 2], v[4 * i + 3]);
-        } else if constexpr (MODE == kSquare) {
-          const size_t plane = (size_t)s.nm * s.Rp * s.Rp, at = ((size_t)mi * s.Rp + row) * s.Rp + col;
-          float xh[16], xl[16];
-          load16(a.am + at, xh);
-          load16(a.am + plane + at, xl);
-#pragma unroll
-          for (int i = 0; i < 16; ++i) {
-            const float av = fmaf(xl[i], 1.0f / kSl, xh[i]) * (1.0f / kSa);
-            v[i] = kSb * fmaf(a.c, v[i] * (1.0f / (kSa * kSa)), fmaf(a.b, av, row == col + i ? a.a : 0.0f));
-          }
-          store16(a.dst + at, a.dst + plane + at, v);
         } else if constexpr (MODE == kUpdate) {
           const size_t plane = (size_t)s.nm * s.Rp * s.Lp, at = ((size_t)mi * s.Rp + row) * s.Lp + col;
 #pragma unroll
@@ -352,29 +391,71 @@ __global__ void __launch_bounds__(320, 1) ns_product_kernel(const __grid_constan
     }
     tc::fence_before_sync();
   }
-  __syncthreads();
-  if (warp == 9) tc::tmem_dealloc(tmem, 2 * kTile);
+  // neither CTA leaves before the other's last arrival and MMA
+  cluster_sync();
+  if (warp == kDrainWarps + 1)
+    asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(512u) : "memory");
 }
 
-// A from the partial products of X X^T, in a fixed order.
-__global__ void __launch_bounds__(256) ns_reduce_kernel(const float* __restrict__ part, int S, size_t n,
-                                                        __half* __restrict__ am) {
-  const size_t i = ((size_t)blockIdx.x * 256 + threadIdx.x) * 4;
-  if (i >= n) return;
-  float4 v = *reinterpret_cast<const float4*>(part + i);
-  for (int k = 1; k < S; ++k) {
-    const float4 q = *reinterpret_cast<const float4*>(part + k * n + i);
-    v.x += q.x;
-    v.y += q.y;
-    v.z += q.z;
-    v.w += q.w;
-  }
-  const float f[4] = {v.x, v.y, v.z, v.w};
-  alignas(8) __half h[4], l[4];
+// A from the partial products of X X^T, or B = a I + b A + c A A from those of A A, in a fixed order.
+// The products hold the 256-wide tiles on and above the diagonal: a CTA adds a 64 x 64 tile there
+// and writes it and its mirror image.
+template <bool SQUARE>
+__global__ void __launch_bounds__(256) ns_reduce_kernel(const float* __restrict__ part, Shape s, int S, float a,
+                                                        float b, float c, const __half* __restrict__ am,
+                                                        __half* __restrict__ dst) {
+  __shared__ float tile[64][65];
+  const int nt = s.Rp / 64, mi = blockIdx.y;
+  int bj = blockIdx.x, bi = 0;
+  while (bj >= nt - bi) bj -= nt - bi++;
+  bj += bi;
+  const size_t plane = (size_t)s.nm * s.Rp * s.Rp, base = (size_t)mi * s.Rp * s.Rp;
+  const int x = threadIdx.x % 16 * 4, y = threadIdx.x / 16;
+  auto put = [&](size_t at, const float (&v)[4]) {
+    alignas(8) __half h[4], l[4];
 #pragma unroll
-  for (int k = 0; k < 4; ++k) split(f[k] * (kSa / (kSx * kSx)), h[k], l[k]);
-  *reinterpret_cast<uint2*>(am + i) = *reinterpret_cast<const uint2*>(h);
-  *reinterpret_cast<uint2*>(am + n + i) = *reinterpret_cast<const uint2*>(l);
+    for (int k = 0; k < 4; ++k) split(v[k], h[k], l[k]);
+    *reinterpret_cast<uint2*>(dst + at) = *reinterpret_cast<const uint2*>(h);
+    *reinterpret_cast<uint2*>(dst + plane + at) = *reinterpret_cast<const uint2*>(l);
+  };
+#pragma unroll
+  for (int r = y; r < 64; r += 16) {
+    const int i = bi * 64 + r, j = bj * 64 + x;
+    const size_t at = base + (size_t)i * s.Rp + j;
+    float4 q = *reinterpret_cast<const float4*>(part + at);
+    for (int k = 1; k < S; ++k) {
+      const float4 p = *reinterpret_cast<const float4*>(part + k * plane + at);
+      q.x += p.x;
+      q.y += p.y;
+      q.z += p.z;
+      q.w += p.w;
+    }
+    float v[4] = {q.x, q.y, q.z, q.w};
+    if (SQUARE) {
+      const uint2 hq = *reinterpret_cast<const uint2*>(am + at), lq = *reinterpret_cast<const uint2*>(am + plane + at);
+      const __half2 *h = reinterpret_cast<const __half2*>(&hq), *l = reinterpret_cast<const __half2*>(&lq);
+      const float2 h0 = __half22float2(h[0]), h1 = __half22float2(h[1]), l0 = __half22float2(l[0]),
+                   l1 = __half22float2(l[1]);
+      const float av[4] = {fmaf(l0.x, 1.0f / kSl, h0.x), fmaf(l0.y, 1.0f / kSl, h0.y), fmaf(l1.x, 1.0f / kSl, h1.x),
+                           fmaf(l1.y, 1.0f / kSl, h1.y)};
+#pragma unroll
+      for (int k = 0; k < 4; ++k)
+        v[k] = kSb * fmaf(c, v[k] * (1.0f / (kSa * kSa)), fmaf(b, av[k] * (1.0f / kSa), i == j + k ? a : 0.0f));
+    } else {
+#pragma unroll
+      for (int k = 0; k < 4; ++k) v[k] *= kSa / (kSx * kSx);
+    }
+    put(at, v);
+#pragma unroll
+    for (int k = 0; k < 4; ++k) tile[r][x + k] = v[k];
+  }
+  if (bi == bj) return;
+  __syncthreads();
+#pragma unroll
+  for (int r = y; r < 64; r += 16) {
+    const float v[4] = {tile[x][r], tile[x + 1][r], tile[x + 2][r], tile[x + 3][r]};
+    put(base + (size_t)(bj * 64 + r) * s.Rp + bi * 64 + x, v);
+  }
 }
 
 // ------------------------------------------------------------------ small matrices: one launch
@@ -422,19 +503,6 @@ __host__ __device__ constexpr SmallLayout small_layout(int rp, int S, int max_ch
 
 __device__ __forceinline__ uint32_t sw128(int row, int col_byte) {
   return (uint32_t)row * 128u + ((uint32_t)col_byte ^ (((uint32_t)row & 7u) << 4));
-}
-__device__ __forceinline__ uint32_t cluster_rank() {
-  uint32_t r;
-  asm volatile("mov.u32 %0, %cluster_ctarank;" : "=r"(r));
-  return r;
-}
-__device__ __forceinline__ void cluster_sync() {
-  asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
-}
-__device__ __forceinline__ uint32_t at_rank(uint32_t addr, uint32_t rank) {
-  uint32_t r;
-  asm("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(r) : "r"(addr), "r"(rank));
-  return r;
 }
 __device__ __forceinline__ void st_remote(uint32_t addr, float v) {
   asm volatile("st.shared::cluster.f32 [%0], %1;" ::"r"(addr), "f"(v) : "memory");
@@ -785,15 +853,24 @@ Shape shape_of(int n, int groups, int rows, int cols) {
   s.tr = rows > cols;
   s.R = std::min(rows, cols);
   s.L = std::max(rows, cols);
-  s.Rp = up(s.R, kTile);
-  s.Lp = up(s.L, kTile);
+  s.Rp = up(s.R, kPairTile);
+  s.Lp = up(s.L, kPairTile);
   s.nm = n * groups;
   return s;
 }
 
-int splits_of(const Shape& s) { return (s.Lp + kMaxChain - 1) / kMaxChain; }
+// Splits of the K range (in chunks) of a symmetric product: enough for a pair of CTAs on every
+// two SMs, each of 256 values at least.
+int splits_of(const Shape& s, int k, int sms) {
+  const int nt = s.Rp / kPairTile;
+  const long long tiles = (long long)nt * (nt + 1) / 2 * s.nm;
+  const int room = (int)std::max<long long>(1, sms / 2 / tiles);
+  return std::max(1, std::min({room, k / 256, kMaxSplits}));
+}
 
 size_t align256(size_t v) { return (v + 255) & ~size_t(255); }
+
+constexpr int kMostSms = 160;  // what the workspace provides for
 
 struct Layout {
   size_t x[2], a, b, part, norm, total;
@@ -812,7 +889,7 @@ Layout layout_of(const Shape& s) {
   l.x[1] = take(4 * nx);
   l.a = take(4 * na);
   l.b = take(4 * na);
-  l.part = take(4 * na * splits_of(s));
+  l.part = take(4 * na * std::max(splits_of(s, s.Lp, kMostSms), splits_of(s, s.Rp, kMostSms)));
   l.norm = take(sizeof(double) * s.nm * kNormBlocks);
   l.total = at;
   return l;
@@ -838,7 +915,8 @@ cudaError_t product(const CUtensorMap& p, const CUtensorMap& q, const Pointers& 
   auto k = ns_product_kernel<T, MODE>;
   cudaError_t e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kProductSmem);
   if (e != cudaSuccess) return e;
-  k<<<dim3(a.s.Rp / kTile * a.tn, a.s.nm, a.S), 320, kProductSmem, st>>>(p, q, ptr, a);
+  const int tiles = MODE == kSymmetric ? a.tn * (a.tn + 1) / 2 : a.tm * a.tn;
+  k<<<dim3(2 * tiles * a.S, a.s.nm), kProductThreads, kProductSmem, st>>>(p, q, ptr, a);
   count_launch();
   return cudaGetLastError();
 }
@@ -933,31 +1011,29 @@ cudaError_t run_chunk(const MuonArgs& a, int t0, int n, char* ws, int sms, cudaS
   ns_load_kernel<T><<<dim3(s.Lp / 32, s.Rp / 32, s.nm), 256, 0, st>>>(ptr, s, r, a.eps, norm, blocks, x[0]);
   count_launch();
   if ((e = cudaGetLastError()) != cudaSuccess) return e;
-  const int S = splits_of(s);
-  const size_t na = (size_t)s.nm * s.Rp * s.Rp;
   ProductArgs g{};
   g.s = s;
-  g.a = a.a;
-  g.b = a.b;
-  g.c = a.c;
   g.r = r;
+  g.part = part;
+  const int nt = s.Rp / 64;
+  const dim3 red(nt * (nt + 1) / 2, s.nm);
   for (int k = 0; k < a.steps; ++k) {
     const int now = k & 1;
-    g.part = part;
-    g.tn = s.Rp / kTile;
+    g.tm = g.tn = s.Rp / kPairTile;
     g.chunks = s.Lp / kBk;
-    g.chunk0 = kMaxChain / kBk;
-    g.S = S;
-    if ((e = product<T, kGram>(mx[now], mx[now], ptr, g, st)) != cudaSuccess) return e;
-    ns_reduce_kernel<<<(unsigned)((na / 4 + 255) / 256), 256, 0, st>>>(part, S, na, am);
+    g.S = splits_of(s, s.Lp, sms);
+    if ((e = product<T, kSymmetric>(mx[now], mx[now], ptr, g, st)) != cudaSuccess) return e;
+    ns_reduce_kernel<false><<<red, 256, 0, st>>>(part, s, g.S, a.a, a.b, a.c, nullptr, am);
+    count_launch();
+    if ((e = cudaGetLastError()) != cudaSuccess) return e;
+    g.chunks = s.Rp / kBk;
+    g.S = splits_of(s, s.Rp, sms);
+    if ((e = product<T, kSymmetric>(ma, ma, ptr, g, st)) != cudaSuccess) return e;
+    ns_reduce_kernel<true><<<red, 256, 0, st>>>(part, s, g.S, a.a, a.b, a.c, am, bm);
     count_launch();
     if ((e = cudaGetLastError()) != cudaSuccess) return e;
     g.S = 1;
-    g.chunks = g.chunk0 = s.Rp / kBk;
-    g.am = am;
-    g.dst = bm;
-    if ((e = product<T, kSquare>(ma, ma, ptr, g, st)) != cudaSuccess) return e;
-    g.tn = s.Lp / kTile;
+    g.tn = s.Lp / kPairTile;
     g.dst = x[now ^ 1];
     e = k + 1 < a.steps ? product<T, kUpdate>(mb, mx[now], ptr, g, st) : product<T, kFinal>(mb, mx[now], ptr, g, st);
     if (e != cudaSuccess) return e;
@@ -968,13 +1044,15 @@ cudaError_t run_chunk(const MuonArgs& a, int t0, int n, char* ws, int sms, cudaS
 }  // namespace
 
 size_t muon_workspace(int n, int groups, int rows, int cols) {
-  return layout_of(shape_of(std::min(n, kTensors), groups, rows, cols)).total;
+  const Shape s = shape_of(std::min(n, kTensors), groups, rows, cols);
+  return small_plan(s, kMostSms).ok ? 256 : layout_of(s).total;
 }
 
 cudaError_t launch_muon(const MuonArgs& a, void* workspace, cudaStream_t st) {
   int sms = 0;
   cudaError_t q = sm_count(&sms);
   if (q != cudaSuccess) return q;
+  sms = std::min(sms, kMostSms);
   for (int t0 = 0; t0 < a.n; t0 += kTensors) {
     const int n = std::min(kTensors, a.n - t0);
     char* ws = static_cast<char*>(workspace);
