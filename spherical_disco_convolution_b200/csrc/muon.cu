@@ -39,7 +39,7 @@ constexpr uint32_t kStageBytes = 4 * kOperand;
 constexpr int kDrainWarps = 16;
 constexpr int kProductThreads = (kDrainWarps + 2) * 32;
 constexpr int kTensors = 64;     // tensors of one set of launches (pointers travel as arguments)
-constexpr int kNormBlocks = 32;  // partial sums of squares per matrix, at most
+constexpr int kNormBlocks = 256;  // partial sums of squares per matrix, at most
 
 struct Pointers {
   const void* in[kTensors];
@@ -73,6 +73,44 @@ __device__ __forceinline__ double warp_sum(double v) {
   return v;
 }
 
+// kWide values from an address on their own alignment, by one load where it is wide enough.
+constexpr int kWide = 8;
+template <typename T>
+__device__ __forceinline__ void load_wide(const T* p, int n, float (&v)[kWide]) {
+  if (n == kWide && reinterpret_cast<uintptr_t>(p) % 16 == 0) {
+    alignas(16) T q[kWide];
+#pragma unroll
+    for (int i = 0; i < kWide * (int)sizeof(T) / 16; ++i)
+      reinterpret_cast<uint4*>(q)[i] = reinterpret_cast<const uint4*>(p)[i];
+#pragma unroll
+    for (int i = 0; i < kWide; ++i) v[i] = to_f32(q[i]);
+  } else {
+#pragma unroll
+    for (int i = 0; i < kWide; ++i) v[i] = i < n ? to_f32(p[i]) : 0.0f;
+  }
+}
+template <typename T>
+__device__ __forceinline__ void store_wide(T* p, int n, const float (&v)[kWide]) {
+  if (n == kWide && reinterpret_cast<uintptr_t>(p) % 16 == 0) {
+    alignas(16) T q[kWide];
+#pragma unroll
+    for (int i = 0; i < kWide; ++i) q[i] = from_f32<T>(v[i]);
+#pragma unroll
+    for (int i = 0; i < kWide * (int)sizeof(T) / 16; ++i)
+      reinterpret_cast<uint4*>(p)[i] = reinterpret_cast<const uint4*>(q)[i];
+  } else {
+#pragma unroll
+    for (int i = 0; i < kWide; ++i)
+      if (i < n) p[i] = from_f32<T>(v[i]);
+  }
+}
+
+// The update itself from the gradient u and the momentum m before it (after it: m_new).
+__device__ __forceinline__ float new_momentum(const Rule& r, float u, float m) { return fmaf(r.momentum, m, u); }
+__device__ __forceinline__ float update_of(const Rule& r, float u, float m_new) {
+  return r.nesterov ? fmaf(r.momentum, m_new, u) : m_new;
+}
+
 // Sums of squares of a slice of each matrix; for a whole step the momentum is updated on the way.
 // fp64: no update is too large or too small for its square.
 template <typename T>
@@ -84,18 +122,27 @@ __global__ void __launch_bounds__(256) ns_norm_kernel(const __grid_constant__ Po
   const T* in = static_cast<const T*>(p.in[t]) + base;
   const float* m = r.step ? p.m[t] + base : nullptr;
   float* mo = r.step ? p.m_out[t] + base : nullptr;
-  double sum = 0.0;
-  for (size_t i = (size_t)blockIdx.x * 256 + threadIdx.x; i < n; i += (size_t)gridDim.x * 256) {
-    float u = to_f32(in[i]);
+  double sum[2] = {0.0, 0.0};
+  const size_t stride = (size_t)gridDim.x * 256 * kWide;
+#pragma unroll 2
+  for (size_t i = ((size_t)blockIdx.x * 256 + threadIdx.x) * kWide; i < n; i += stride) {
+    const int here = (int)(n - i < kWide ? n - i : kWide);
+    float u[kWide];
+    load_wide(in + i, here, u);
     if (r.step) {
-      const float mv = fmaf(r.momentum, m[i], u);
-      mo[i] = mv;
-      u = r.nesterov ? fmaf(r.momentum, mv, u) : mv;
+      float v[kWide];
+      load_wide(m + i, here, v);
+#pragma unroll
+      for (int k = 0; k < kWide; ++k) v[k] = new_momentum(r, u[k], v[k]);
+      store_wide(mo + i, here, v);
+#pragma unroll
+      for (int k = 0; k < kWide; ++k) u[k] = update_of(r, u[k], v[k]);
     }
-    sum += (double)u * (double)u;
+#pragma unroll
+    for (int k = 0; k < kWide; ++k) sum[k & 1] = fma((double)u[k], (double)u[k], sum[k & 1]);
   }
-  sum = warp_sum(sum);
-  if ((threadIdx.x & 31) == 0) warps[threadIdx.x >> 5] = sum;
+  const double all = warp_sum(sum[0] + sum[1]);
+  if ((threadIdx.x & 31) == 0) warps[threadIdx.x >> 5] = all;
   __syncthreads();
   if (threadIdx.x == 0) {
     double v = 0.0;
@@ -104,45 +151,54 @@ __global__ void __launch_bounds__(256) ns_norm_kernel(const __grid_constant__ Po
   }
 }
 
-// X = U / (|U|_F + eps) as hi and lo planes [2][nm][Rp][Lp], zero in the padding.
+// X = U / (|U|_F + eps) as hi and lo planes [2][nm][Rp][Lp], zero in the padding: a 64 x 64 tile a CTA.
 template <typename T>
 __global__ void __launch_bounds__(256) ns_load_kernel(const __grid_constant__ Pointers p, Shape s, Rule r, double eps,
                                                       const double* __restrict__ part, int parts,
                                                       __half* __restrict__ x) {
-  __shared__ float tile[32][33];
+  __shared__ float tile[64][65];
   __shared__ float scale;
   const int mi = blockIdx.z, t = mi / s.groups, g = mi % s.groups;
-  const int tx = threadIdx.x & 31, ty = threadIdx.x >> 5;
-  if (ty == 0) {
+  if (threadIdx.x < 32) {
     double v = 0.0;
-    for (int k = tx; k < parts; k += 32) v += part[(size_t)mi * parts + k];
+    for (int k = threadIdx.x; k < parts; k += 32) v += part[(size_t)mi * parts + k];
     v = warp_sum(v);
-    if (tx == 0) scale = (float)((double)kSx / (sqrt(v) + eps));
+    if (threadIdx.x == 0) scale = (float)((double)kSx / (sqrt(v) + eps));
   }
-  const size_t n = (size_t)s.rows * s.cols, base = g * n;
+  const size_t base = (size_t)g * s.rows * s.cols;
   const T* in = static_cast<const T*>(p.in[t]) + base;
   const float* mo = r.step ? p.m_out[t] + base : nullptr;
-  const int l0 = blockIdx.x * 32, r0 = blockIdx.y * 32;
+  const int l0 = blockIdx.x * 64, r0 = blockIdx.y * 64;
+  const int x8 = threadIdx.x % 8 * kWide, y = threadIdx.x / 8;
   // a row of the tile is read along the tensor's columns
-  for (int k = ty; k < 32; k += 8) {
-    const int row = s.tr ? l0 + k : r0 + k, col = s.tr ? r0 + tx : l0 + tx;
-    float u = 0.0f;
-    if (row < s.rows && col < s.cols) {
+#pragma unroll
+  for (int k = y; k < 64; k += 32) {
+    const int row = (s.tr ? l0 : r0) + k, col = (s.tr ? r0 : l0) + x8;
+    const int here = row < s.rows ? max(0, min(kWide, s.cols - col)) : 0;
+    float u[kWide] = {};
+    if (here > 0) {
       const size_t i = (size_t)row * s.cols + col;
-      u = to_f32(in[i]);
-      if (r.step) u = r.nesterov ? fmaf(r.momentum, mo[i], u) : mo[i];
+      load_wide(in + i, here, u);
+      if (r.step) {
+        float m[kWide];
+        load_wide(mo + i, here, m);
+#pragma unroll
+        for (int e = 0; e < kWide; ++e) u[e] = update_of(r, u[e], m[e]);
+      }
     }
-    tile[k][tx] = u;
+#pragma unroll
+    for (int e = 0; e < kWide; ++e) tile[k][x8 + e] = u[e];
   }
   __syncthreads();
   const size_t plane = (size_t)s.nm * s.Rp * s.Lp;
-  for (int k = ty; k < 32; k += 8) {
-    const float v = (s.tr ? tile[tx][k] : tile[k][tx]) * scale;
-    __half hi, lo;
-    split(v, hi, lo);
-    const size_t at = ((size_t)mi * s.Rp + r0 + k) * s.Lp + l0 + tx;
-    x[at] = hi;
-    x[plane + at] = lo;
+#pragma unroll
+  for (int k = y; k < 64; k += 32) {
+    alignas(16) __half h[kWide], l[kWide];
+#pragma unroll
+    for (int e = 0; e < kWide; ++e) split((s.tr ? tile[x8 + e][k] : tile[k][x8 + e]) * scale, h[e], l[e]);
+    const size_t at = ((size_t)mi * s.Rp + r0 + k) * s.Lp + l0 + x8;
+    *reinterpret_cast<uint4*>(x + at) = *reinterpret_cast<const uint4*>(h);
+    *reinterpret_cast<uint4*>(x + plane + at) = *reinterpret_cast<const uint4*>(l);
   }
 }
 
@@ -227,8 +283,10 @@ __device__ __forceinline__ void pair_commit(uint64_t* bar) {
       "h"((uint16_t)3)
       : "memory");
 }
+// Arrives on a barrier of either CTA.  What it orders is this warp's reads of TMEM, which are
+// complete (wait::ld), and no memory: a release over the cluster would cost a fence a chunk.
 __device__ __forceinline__ void arrive_remote(uint32_t bar) {
-  asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(bar) : "memory");
+  asm volatile("mbarrier.arrive.shared::cluster.b64 _, [%0];" ::"r"(bar) : "memory");
 }
 
 template <typename T, Product MODE>
@@ -1004,11 +1062,11 @@ cudaError_t run_chunk(const MuonArgs& a, int t0, int n, char* ws, int sms, cudaS
       !plane_map(&ma, am, s.Rp, s.Rp, 2 * s.nm) || !plane_map(&mb, bm, s.Rp, s.Rp, 2 * s.nm))
     return cudaErrorInvalidValue;
   cudaError_t e;
-  const int blocks = (int)std::min<size_t>(kNormBlocks, ((size_t)a.rows * a.cols + 1023) / 1024);
+  const int blocks = (int)std::min<size_t>(kNormBlocks, ((size_t)a.rows * a.cols + 256 * kWide - 1) / (256 * kWide));
   ns_norm_kernel<T><<<dim3(blocks, s.nm), 256, 0, st>>>(ptr, s, r, norm);
   count_launch();
   if ((e = cudaGetLastError()) != cudaSuccess) return e;
-  ns_load_kernel<T><<<dim3(s.Lp / 32, s.Rp / 32, s.nm), 256, 0, st>>>(ptr, s, r, a.eps, norm, blocks, x[0]);
+  ns_load_kernel<T><<<dim3(s.Lp / 64, s.Rp / 64, s.nm), 256, 0, st>>>(ptr, s, r, a.eps, norm, blocks, x[0]);
   count_launch();
   if ((e = cudaGetLastError()) != cudaSuccess) return e;
   ProductArgs g{};
