@@ -61,6 +61,11 @@ struct Rule {
   float momentum, keep, rate;
 };
 
+// Programmatic dependent launch: the next kernel of a chain may be brought up while this one runs,
+// and waits here for the results of the one before it.
+__device__ __forceinline__ void wait_previous() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
+__device__ __forceinline__ void let_next_start() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
+
 // hi + lo / kSl = v to 22 bits (v within fp16's range).
 __device__ __forceinline__ void split(float v, __half& hi, __half& lo) {
   hi = __float2half_rn(v);
@@ -111,12 +116,18 @@ __device__ __forceinline__ float update_of(const Rule& r, float u, float m_new) 
   return r.nesterov ? fmaf(r.momentum, m_new, u) : m_new;
 }
 
+// What is stored of a result: the new weight from the old one, or the result itself.
+__device__ __forceinline__ float result_of(const Rule& r, float w, float x) {
+  return r.step ? fmaf(r.keep, w, -r.rate * x) : x;
+}
+
 // Sums of squares of a slice of each matrix; for a whole step the momentum is updated on the way.
 // fp64: no update is too large or too small for its square.
 template <typename T>
 __global__ void __launch_bounds__(256) ns_norm_kernel(const __grid_constant__ Pointers p, Shape s, Rule r,
                                                       double* __restrict__ part) {
   __shared__ double warps[8];
+  let_next_start();
   const int mi = blockIdx.y, t = mi / s.groups, g = mi % s.groups;
   const size_t n = (size_t)s.rows * s.cols, base = g * n;
   const T* in = static_cast<const T*>(p.in[t]) + base;
@@ -159,6 +170,8 @@ __global__ void __launch_bounds__(256) ns_load_kernel(const __grid_constant__ Po
   __shared__ float tile[64][65];
   __shared__ float scale;
   const int mi = blockIdx.z, t = mi / s.groups, g = mi % s.groups;
+  let_next_start();
+  wait_previous();
   if (threadIdx.x < 32) {
     double v = 0.0;
     for (int k = threadIdx.x; k < parts; k += 32) v += part[(size_t)mi * parts + k];
@@ -206,10 +219,18 @@ __global__ void __launch_bounds__(256) ns_load_kernel(const __grid_constant__ Po
 
 enum Product { kSymmetric, kUpdate, kFinal };
 
+// What becomes of the entries of a symmetric product: A from those of X X^T (am null), or
+// B = a I + b A + c A A from those of A A.
+struct Becomes {
+  float a, b, c;
+  const __half* am;
+};
+
 struct ProductArgs {
   Shape s;
   int tm, tn, S, chunks;  // tiles along M and N, splits along K, K chunks in all
-  float* part;            // kGram, kSquare: [S][nm][Rp][Rp]
+  float* part;            // kSymmetric, S > 1: [S][nm][Rp][Rp]
+  Becomes f;              // kSymmetric, S = 1: what the product becomes, into dst
   __half* dst;            // kUpdate: the next X
   Rule r;
 };
@@ -223,16 +244,47 @@ __host__ __device__ constexpr uint32_t idesc_f16(int M, int N, bool b_mn_major) 
   return (1u << 4) | ((b_mn_major ? 1u : 0u) << 16) | ((uint32_t)(N >> 3) << 17) | ((uint32_t)(M >> 4) << 24);
 }
 
-// 16 values as hi and lo, 32 bytes of each plane.
-__device__ __forceinline__ void store16(__half* hi, __half* lo, const float (&v)[16]) {
-  alignas(16) __half h[16], l[16];
+// 8 values as 16 bytes of hi and of lo.
+__device__ __forceinline__ void split8(const float (&v)[8], uint4& hi, uint4& lo) {
+  alignas(16) __half2 h[4], l[4];
 #pragma unroll
-  for (int i = 0; i < 16; ++i) split(v[i], h[i], l[i]);
-#pragma unroll
-  for (int i = 0; i < 2; ++i) {
-    reinterpret_cast<uint4*>(hi)[i] = reinterpret_cast<const uint4*>(h)[i];
-    reinterpret_cast<uint4*>(lo)[i] = reinterpret_cast<const uint4*>(l)[i];
+  for (int i = 0; i < 4; ++i) {
+    h[i] = __floats2half2_rn(v[2 * i], v[2 * i + 1]);
+    const float2 f = __half22float2(h[i]);
+    l[i] = __floats2half2_rn((v[2 * i] - f.x) * kSl, (v[2 * i + 1] - f.y) * kSl);
   }
+  hi = *reinterpret_cast<const uint4*>(h);
+  lo = *reinterpret_cast<const uint4*>(l);
+}
+__device__ __forceinline__ void widen8(uint4 hi, float (&v)[8]) {
+  const __half2* h = reinterpret_cast<const __half2*>(&hi);
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const float2 x = __half22float2(h[i]);
+    v[2 * i] = x.x;
+    v[2 * i + 1] = x.y;
+  }
+}
+__device__ __forceinline__ void join8(uint4 hi, uint4 lo, float (&v)[8]) {
+  float w[8];
+  widen8(hi, v);
+  widen8(lo, w);
+#pragma unroll
+  for (int i = 0; i < 8; ++i) v[i] = fmaf(w[i], 1.0f / kSl, v[i]);
+}
+// 8 entries of a row of a symmetric product, scaled as the next operand; `diag`: which of them lies
+// on the diagonal, if any.
+__device__ __forceinline__ void become(const Becomes& f, size_t plane, size_t at, int diag, float (&v)[8]) {
+  if (!f.am) {
+#pragma unroll
+    for (int i = 0; i < 8; ++i) v[i] *= kSa / (kSx * kSx);
+    return;
+  }
+  float x[8];
+  join8(*reinterpret_cast<const uint4*>(f.am + at), *reinterpret_cast<const uint4*>(f.am + plane + at), x);
+#pragma unroll
+  for (int i = 0; i < 8; ++i)
+    v[i] = fmaf(f.c * (kSb / (kSa * kSa)), v[i], fmaf(f.b * (kSb / kSa), x[i], i == diag ? f.a * kSb : 0.0f));
 }
 
 // A pair of CTAs (cta_group::2) makes one 256 x 256 tile of a product of hi + lo matrices:
@@ -336,10 +388,12 @@ __global__ void __launch_bounds__(kProductThreads, 1) __cluster_dims__(2, 1, 1)
                  : "memory");
     asm volatile("tcgen05.relinquish_alloc_permit.cta_group::2.sync.aligned;" ::: "memory");
   }
+  let_next_start();
   tc::fence_before_sync();
   cluster_sync();
   tc::fence_after_sync();
   const uint32_t tmem = *tmem_slot;
+  wait_previous();
 
   if (warp == kDrainWarps && lane == 0) {
     for (int k = k_lo; k < k_hi; ++k) {
@@ -414,36 +468,90 @@ __global__ void __launch_bounds__(kProductThreads, 1) __cluster_dims__(2, 1, 1)
     }
     ok = ok && tc::mbar_wait(done, 0);
     tc::fence_after_sync();
-    if (ok) {
+    // The tile goes through the operand buffers, which are free: 128 rows of 256 fp32 values, the
+    // 16-byte blocks of a row exchanged by the row's last bits.  What is made of it then runs in
+    // short loops: unrolled over a thread's 64 registers the code came cold from L2 and cost 8 us.
+    {
+      uint8_t* to = smem + (row - m0) * 1024;
+      const uint32_t turn = ((uint32_t)row & 7u) << 4;
 #pragma unroll
       for (int c = 0; c < 64; c += 16) {
         float v[16];
         tc::tmem_ld16(tw + kPairTile + c, v);
 #pragma unroll
-        for (int i = 0; i < 16; ++i) v[i] = fmaf(v[i], 1.0f / kSl, acc[c + i]);
-        const int col = n0 + c0 + c;
+        for (int i = 0; i < 16; i += 4)
+          *reinterpret_cast<float4*>(to + (((uint32_t)(c0 + c + i) * 4) ^ turn)) =
+              make_float4(fmaf(v[i], 1.0f / kSl, acc[c + i]), fmaf(v[i + 1], 1.0f / kSl, acc[c + i + 1]),
+                          fmaf(v[i + 2], 1.0f / kSl, acc[c + i + 2]), fmaf(v[i + 3], 1.0f / kSl, acc[c + i + 3]));
+      }
+    }
+    tc::named_bar_sync(1, kDrainWarps * 32);
+    const size_t pa = (size_t)s.nm * s.Rp * s.Rp, px = (size_t)s.nm * s.Rp * s.Lp;
+    const size_t tensor = (size_t)(mi % s.groups) * s.rows * s.cols;
+    if (ok && !(MODE == kFinal && s.tr)) {
+#pragma unroll 1
+      for (int r = warp; r < kTile; r += kDrainWarps) {  // a warp takes a row, a lane 8 columns
+        const uint8_t* from = smem + r * 1024;
+        const uint32_t turn = (uint32_t)r & 7u;
+        const float4 x = *reinterpret_cast<const float4*>(from + (((2u * lane) ^ turn) << 4));
+        const float4 y = *reinterpret_cast<const float4*>(from + (((2u * lane + 1u) ^ turn) << 4));
+        float v[8] = {x.x, x.y, x.z, x.w, y.x, y.y, y.z, y.w};
+        const int grow = m0 + r, col = n0 + lane * 8;
         if constexpr (MODE == kSymmetric) {
-          float4* dst = reinterpret_cast<float4*>(a.part + (((size_t)split_k * s.nm + mi) * s.Rp + row) * s.Rp + col);
-#pragma unroll
-          for (int i = 0; i < 4; ++i) dst[i] = make_float4(v[4 * i], v[4 * i + 1], v[4 * i + 2], v[4 * i + 3]);
-        } else if constexpr (MODE == kUpdate) {
-          const size_t plane = (size_t)s.nm * s.Rp * s.Lp, at = ((size_t)mi * s.Rp + row) * s.Lp + col;
-#pragma unroll
-          for (int i = 0; i < 16; ++i) v[i] *= 1.0f / kSb;
-          store16(a.dst + at, a.dst + plane + at, v);
-        } else {
-          const int t = mi / s.groups;
-          const size_t base = (size_t)(mi % s.groups) * s.rows * s.cols;
-          T* out = static_cast<T*>(ptr.out[t]) + base;
-          const T* w = a.r.step ? static_cast<const T*>(ptr.w[t]) + base : nullptr;
-#pragma unroll
-          for (int i = 0; i < 16; ++i) {
-            if (row >= s.R || col + i >= s.L) continue;
-            const size_t at = s.tr ? (size_t)(col + i) * s.cols + row : (size_t)row * s.cols + col + i;
-            float o = v[i] * (1.0f / (kSb * kSx));
-            if (a.r.step) o = fmaf(a.r.keep, to_f32(w[at]), -a.r.rate * o);
-            out[at] = from_f32<T>(o);
+          const size_t at = ((size_t)mi * s.Rp + grow) * s.Rp + col;
+          if (a.S > 1) {
+            float4* dst = reinterpret_cast<float4*>(a.part + (size_t)split_k * pa + at);
+            dst[0] = x;
+            dst[1] = y;
+          } else {
+            become(a.f, pa, at, grow - col, v);
+            uint4 hi, lo;
+            split8(v, hi, lo);
+            *reinterpret_cast<uint4*>(a.dst + at) = hi;
+            *reinterpret_cast<uint4*>(a.dst + pa + at) = lo;
+            if (bm != bn) {  // for the mirror image
+              *reinterpret_cast<float4*>(smem + r * 1024 + (((2u * lane) ^ turn) << 4)) = make_float4(v[0], v[1], v[2], v[3]);
+              *reinterpret_cast<float4*>(smem + r * 1024 + (((2u * lane + 1u) ^ turn) << 4)) = make_float4(v[4], v[5], v[6], v[7]);
+            }
           }
+        } else if constexpr (MODE == kUpdate) {
+          const size_t at = ((size_t)mi * s.Rp + grow) * s.Lp + col;
+#pragma unroll
+          for (int i = 0; i < 8; ++i) v[i] *= 1.0f / kSb;
+          uint4 hi, lo;
+          split8(v, hi, lo);
+          *reinterpret_cast<uint4*>(a.dst + at) = hi;
+          *reinterpret_cast<uint4*>(a.dst + px + at) = lo;
+        } else {
+          const int here = grow < s.R ? max(0, min(8, s.L - col)) : 0;
+          if (here > 0) {
+            const size_t at = tensor + (size_t)grow * s.cols + col;
+            float w[8] = {};
+            if (a.r.step) load_wide(static_cast<const T*>(ptr.w[mi / s.groups]) + at, here, w);
+#pragma unroll
+            for (int i = 0; i < 8; ++i) v[i] = result_of(a.r, w[i], v[i] * (1.0f / (kSb * kSx)));
+            store_wide(static_cast<T*>(ptr.out[mi / s.groups]) + at, here, v);
+          }
+        }
+      }
+    }
+    if ((MODE == kSymmetric && a.S == 1 && bm != bn) || (MODE == kFinal && s.tr)) {
+      tc::named_bar_sync(1, kDrainWarps * 32);
+#pragma unroll 1
+      for (int k = warp; k < kPairTile * 4 && ok; k += kDrainWarps) {  // a warp takes 32 rows of a column
+        const int c = k / 4, r = k % 4 * 32 + lane;
+        float v = *reinterpret_cast<const float*>(smem + r * 1024 + (((uint32_t)c * 4) ^ (((uint32_t)r & 7u) << 4)));
+        const int grow = m0 + r, col = n0 + c;
+        if constexpr (MODE == kSymmetric) {
+          const size_t at = ((size_t)mi * s.Rp + col) * s.Rp + grow;
+          __half h, l;
+          split(v, h, l);
+          a.dst[at] = h;
+          a.dst[pa + at] = l;
+        } else if (grow < s.R && col < s.L) {
+          const size_t at = tensor + (size_t)col * s.cols + grow;
+          const float w = a.r.step ? to_f32(static_cast<const T*>(ptr.w[mi / s.groups])[at]) : 0.0f;
+          static_cast<T*>(ptr.out[mi / s.groups])[at] = from_f32<T>(result_of(a.r, w, v * (1.0f / (kSb * kSx))));
         }
       }
     }
@@ -455,64 +563,56 @@ __global__ void __launch_bounds__(kProductThreads, 1) __cluster_dims__(2, 1, 1)
     asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(512u) : "memory");
 }
 
-// A from the partial products of X X^T, or B = a I + b A + c A A from those of A A, in a fixed order.
-// The products hold the 256-wide tiles on and above the diagonal: a CTA adds a 64 x 64 tile there
-// and writes it and its mirror image.
-template <bool SQUARE>
-__global__ void __launch_bounds__(256) ns_reduce_kernel(const float* __restrict__ part, Shape s, int S, float a,
-                                                        float b, float c, const __half* __restrict__ am,
+// The next operand from the partial products of a symmetric product split along K, added in a fixed
+// order.  They hold the 256-wide tiles on and above the diagonal: a CTA adds a 64 x 64 tile there and
+// writes it and its mirror image.
+__global__ void __launch_bounds__(256) ns_reduce_kernel(const float* __restrict__ part, Shape s, int S, Becomes f,
                                                         __half* __restrict__ dst) {
   __shared__ float tile[64][65];
+  let_next_start();
+  wait_previous();
   const int nt = s.Rp / 64, mi = blockIdx.y;
   int bj = blockIdx.x, bi = 0;
   while (bj >= nt - bi) bj -= nt - bi++;
   bj += bi;
   const size_t plane = (size_t)s.nm * s.Rp * s.Rp, base = (size_t)mi * s.Rp * s.Rp;
-  const int x = threadIdx.x % 16 * 4, y = threadIdx.x / 16;
-  auto put = [&](size_t at, const float (&v)[4]) {
-    alignas(8) __half h[4], l[4];
+  const int x = threadIdx.x % 8 * 8, y = threadIdx.x / 8;
 #pragma unroll
-    for (int k = 0; k < 4; ++k) split(v[k], h[k], l[k]);
-    *reinterpret_cast<uint2*>(dst + at) = *reinterpret_cast<const uint2*>(h);
-    *reinterpret_cast<uint2*>(dst + plane + at) = *reinterpret_cast<const uint2*>(l);
-  };
-#pragma unroll
-  for (int r = y; r < 64; r += 16) {
+  for (int r = y; r < 64; r += 32) {
     const int i = bi * 64 + r, j = bj * 64 + x;
     const size_t at = base + (size_t)i * s.Rp + j;
-    float4 q = *reinterpret_cast<const float4*>(part + at);
-    for (int k = 1; k < S; ++k) {
-      const float4 p = *reinterpret_cast<const float4*>(part + k * plane + at);
-      q.x += p.x;
-      q.y += p.y;
-      q.z += p.z;
-      q.w += p.w;
+    float v[8] = {};
+#pragma unroll 4
+    for (int k = 0; k < S; ++k) {
+#pragma unroll
+      for (int e = 0; e < 8; e += 4) {
+        const float4 p = *reinterpret_cast<const float4*>(part + k * plane + at + e);
+        v[e] += p.x;
+        v[e + 1] += p.y;
+        v[e + 2] += p.z;
+        v[e + 3] += p.w;
+      }
     }
-    float v[4] = {q.x, q.y, q.z, q.w};
-    if (SQUARE) {
-      const uint2 hq = *reinterpret_cast<const uint2*>(am + at), lq = *reinterpret_cast<const uint2*>(am + plane + at);
-      const __half2 *h = reinterpret_cast<const __half2*>(&hq), *l = reinterpret_cast<const __half2*>(&lq);
-      const float2 h0 = __half22float2(h[0]), h1 = __half22float2(h[1]), l0 = __half22float2(l[0]),
-                   l1 = __half22float2(l[1]);
-      const float av[4] = {fmaf(l0.x, 1.0f / kSl, h0.x), fmaf(l0.y, 1.0f / kSl, h0.y), fmaf(l1.x, 1.0f / kSl, h1.x),
-                           fmaf(l1.y, 1.0f / kSl, h1.y)};
+    become(f, plane, at, i - j, v);
+    uint4 hi, lo;
+    split8(v, hi, lo);
+    *reinterpret_cast<uint4*>(dst + at) = hi;
+    *reinterpret_cast<uint4*>(dst + plane + at) = lo;
 #pragma unroll
-      for (int k = 0; k < 4; ++k)
-        v[k] = kSb * fmaf(c, v[k] * (1.0f / (kSa * kSa)), fmaf(b, av[k] * (1.0f / kSa), i == j + k ? a : 0.0f));
-    } else {
-#pragma unroll
-      for (int k = 0; k < 4; ++k) v[k] *= kSa / (kSx * kSx);
-    }
-    put(at, v);
-#pragma unroll
-    for (int k = 0; k < 4; ++k) tile[r][x + k] = v[k];
+    for (int e = 0; e < 8; ++e) tile[r][x + e] = v[e];
   }
   if (bi == bj) return;
   __syncthreads();
 #pragma unroll
-  for (int r = y; r < 64; r += 16) {
-    const float v[4] = {tile[x][r], tile[x + 1][r], tile[x + 2][r], tile[x + 3][r]};
-    put(base + (size_t)(bj * 64 + r) * s.Rp + bi * 64 + x, v);
+  for (int r = y; r < 64; r += 32) {
+    float v[8];
+#pragma unroll
+    for (int e = 0; e < 8; ++e) v[e] = tile[x + e][r];
+    const size_t mirror = base + (size_t)(bj * 64 + r) * s.Rp + bi * 64 + x;
+    uint4 hi, lo;
+    split8(v, hi, lo);
+    *reinterpret_cast<uint4*>(dst + mirror) = hi;
+    *reinterpret_cast<uint4*>(dst + plane + mirror) = lo;
   }
 }
 
@@ -530,7 +630,8 @@ __global__ void __launch_bounds__(256) ns_reduce_kernel(const float* __restrict_
 // M = 128; with RP = 64 rows 64..127 of an operand are whatever follows the tile, and the rows of the
 // result they make are not read.
 
-constexpr int kSmallThreads = 256;
+constexpr int kSmallThreads = 512;
+constexpr int kSides = kSmallThreads / 128;    // warps that share 32 lanes of TMEM, each a run of columns
 constexpr int kSmallMaxCluster = 8;
 constexpr size_t kSmallSmem = 226 * 1024;      // of 227 KB
 constexpr size_t kSmallLeast = 120 * 1024;     // more than half of an SM: one CTA (and its TMEM) per SM
@@ -575,32 +676,34 @@ __device__ __forceinline__ void st_remote(uint32_t addr, uint4 v) {
 // Generic-proxy writes to shared memory of the whole cluster before later async-proxy reads.
 __device__ __forceinline__ void fence_proxy_async_all() { asm volatile("fence.proxy.async;" ::: "memory"); }
 
-// 8 values as 16 bytes of hi and of lo.
-__device__ __forceinline__ void split8(const float (&v)[8], uint4& hi, uint4& lo) {
-  alignas(16) __half h[8], l[8];
-#pragma unroll
-  for (int i = 0; i < 8; ++i) split(v[i], h[i], l[i]);
-  hi = *reinterpret_cast<const uint4*>(h);
-  lo = *reinterpret_cast<const uint4*>(l);
-}
-__device__ __forceinline__ void join8(uint4 hi, uint4 lo, float (&v)[8]) {
-  const __half2* h = reinterpret_cast<const __half2*>(&hi);
-  const __half2* l = reinterpret_cast<const __half2*>(&lo);
+// 8 fp32 values kept in the places of 8 hi and 8 lo halves, bit for bit.
+__device__ __forceinline__ void bits8(const float (&v)[8], uint4& hi, uint4& lo) {
+  uint32_t h[4], l[4];
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
-    const float2 x = __half22float2(h[i]), y = __half22float2(l[i]);
-    v[2 * i] = fmaf(y.x, 1.0f / kSl, x.x);
-    v[2 * i + 1] = fmaf(y.y, 1.0f / kSl, x.y);
+    const uint32_t a = __float_as_uint(v[2 * i]), b = __float_as_uint(v[2 * i + 1]);
+    h[i] = __byte_perm(a, b, 0x7632);
+    l[i] = __byte_perm(a, b, 0x5410);
+  }
+  hi = make_uint4(h[0], h[1], h[2], h[3]);
+  lo = make_uint4(l[0], l[1], l[2], l[3]);
+}
+__device__ __forceinline__ void unbits8(uint4 hi, uint4 lo, float (&v)[8]) {
+  const uint32_t h[4] = {hi.x, hi.y, hi.z, hi.w}, l[4] = {lo.x, lo.y, lo.z, lo.w};
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    v[2 * i] = __uint_as_float(__byte_perm(l[i], h[i], 0x5410));
+    v[2 * i + 1] = __uint_as_float(__byte_perm(l[i], h[i], 0x7632));
   }
 }
 
-// Sum of main and small products, 16 columns of a lane's row.
+// 16 columns of a lane's row: the large product plus the small ones.
 __device__ __forceinline__ void drain16(uint32_t main, uint32_t small, float (&v)[16]) {
-  float e[16];
-  tc::tmem_ld16(main, v);
-  tc::tmem_ld16(small, e);
+  uint32_t r[16], e[16];
+  tc::tmem_ld_chunks<1>(main, r);
+  tc::tmem_ld_chunks<1>(small, e);
 #pragma unroll
-  for (int i = 0; i < 16; ++i) v[i] = fmaf(e[i], 1.0f / kSl, v[i]);
+  for (int i = 0; i < 16; ++i) v[i] = fmaf(__uint_as_float(e[i]), 1.0f / kSl, __uint_as_float(r[i]));
 }
 
 template <typename T, int RP>
@@ -613,14 +716,14 @@ __global__ void __launch_bounds__(kSmallThreads, 1)
   uint8_t *xh = smem, *xl = smem + lay.xl, *ah = smem + lay.ah, *al = smem + lay.al;
   float* recv = reinterpret_cast<float*>(smem + lay.recv);
   double* norms = reinterpret_cast<double*>(smem + lay.misc);  // [cluster]
-  double* warps = norms + kSmallMaxCluster;                    // [8]
-  uint64_t* done = reinterpret_cast<uint64_t*>(warps + 8);
+  double* warps = norms + kSmallMaxCluster;                    // [16]
+  uint64_t* done = reinterpret_cast<uint64_t*>(warps + kSmallThreads / 32);
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(done + 1);
   const Shape& s = a.s;
   const int t = threadIdx.x, warp = t >> 5, lane = t & 31;
   const int S = a.S, q = S > 1 ? (int)cluster_rank() : 0, mi = blockIdx.x / S;
   const int c_lo = a.nc * q / S, mine = a.nc * (q + 1) / S - c_lo;
-  const int quarter = (warp & 3) * 32, side = warp >> 2;  // TMEM lanes and half of the columns
+  const int quarter = (warp & 3) * 32, side = warp >> 2;  // TMEM lanes and run of the columns
   const int row = quarter + lane;
   const bool live = quarter < RP;
 
@@ -632,49 +735,99 @@ __global__ void __launch_bounds__(kSmallThreads, 1)
     tc::tmem_alloc(tmem_slot, 512);
     tc::tmem_relinquish();
   }
-  tc::fence_before_sync();
-  __syncthreads();
-  tc::fence_after_sync();
-  const uint32_t tmem = *tmem_slot;
-  if (S > 1) cluster_sync();  // everyone's shared memory may be written from here on
 
-  // U's sum of squares, and the momentum on the way; then X.  A task is 8 columns of one row.
+  // U into the places of X (bit for bit), its sum of squares, and the momentum on the way.  A task is
+  // 8 neighbours in memory: 8 columns of a row of X, or 8 rows of a column of the transposed one.
   const int tn = mi / s.groups;
   const size_t base = (size_t)(mi % s.groups) * s.rows * s.cols;
-  const T* in = static_cast<const T*>(ptr.in[tn]) + base;
-  float* mo = a.r.step ? ptr.m_out[tn] + base : nullptr;
   const int tasks = mine * 8 * RP;
-  auto place = [&](int task, int& r, int& l0) {
+  struct Task {
+    int r, l, here;   // first element, how many of the 8 are the matrix's
+    size_t at;        // in the tensor's matrix
+    uint32_t off;     // of the first element in a plane of X
+  };
+  auto task_of = [&](int k) {
+    Task x;
     if (s.tr) {
-      r = task % RP;
-      l0 = (c_lo * 8 + task / RP) * 8;
+      x.r = k % (RP / 8) * 8;
+      x.l = c_lo * 64 + k / (RP / 8);
+      x.here = x.l < s.L ? max(0, min(8, s.R - x.r)) : 0;
+      x.at = (size_t)x.l * s.cols + x.r;
     } else {
-      r = task / (mine * 8);
-      l0 = (c_lo * 8 + task % (mine * 8)) * 8;
+      x.r = k / (mine * 8);
+      x.l = c_lo * 64 + k % (mine * 8) * 8;
+      x.here = x.r < s.R ? max(0, min(8, s.L - x.l)) : 0;
+      x.at = (size_t)x.r * s.cols + x.l;
+    }
+    x.off = (uint32_t)(x.l / 64 - c_lo) * kChunk + sw128(x.r, x.l % 64 * 2);
+    return x;
+  };
+  // rows r .. r + 7 of a column start on a swizzle period: row r + i is at i * 128 with the 16-byte
+  // block i of the row exchanged
+  auto down = [&](const Task& x, int i) { return (x.off + 128u * i) ^ ((uint32_t)i << 4); };
+  auto put8 = [&](const Task& x, uint4 hi, uint4 lo) {
+    if (!s.tr) {
+      *reinterpret_cast<uint4*>(xh + x.off) = hi;
+      *reinterpret_cast<uint4*>(xl + x.off) = lo;
+    } else {
+      const uint16_t *h = reinterpret_cast<const uint16_t*>(&hi), *l = reinterpret_cast<const uint16_t*>(&lo);
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        *reinterpret_cast<uint16_t*>(xh + down(x, i)) = h[i];
+        *reinterpret_cast<uint16_t*>(xl + down(x, i)) = l[i];
+      }
     }
   };
-  auto index = [&](int r, int l) { return s.tr ? (size_t)l * s.cols + r : (size_t)r * s.cols + l; };
-  double sum = 0.0;
-  for (int task = t; task < tasks; task += kSmallThreads) {
-    int r, l0;
-    place(task, r, l0);
-    if (r >= s.R) continue;
+  auto get8 = [&](const Task& x, uint4& hi, uint4& lo) {
+    if (!s.tr) {
+      hi = *reinterpret_cast<const uint4*>(xh + x.off);
+      lo = *reinterpret_cast<const uint4*>(xl + x.off);
+    } else {
+      alignas(16) uint16_t h[8], l[8];
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      if (l0 + i >= s.L) break;
-      const size_t at = index(r, l0 + i);
-      float u = to_f32(in[at]);
-      if (a.r.step) {
-        const float mv = fmaf(a.r.momentum, ptr.m[tn][base + at], u);
-        mo[at] = mv;
-        u = a.r.nesterov ? fmaf(a.r.momentum, mv, u) : mv;
+      for (int i = 0; i < 8; ++i) {
+        h[i] = *reinterpret_cast<const uint16_t*>(xh + down(x, i));
+        l[i] = *reinterpret_cast<const uint16_t*>(xl + down(x, i));
       }
-      sum += (double)u * (double)u;
+      hi = *reinterpret_cast<const uint4*>(h);
+      lo = *reinterpret_cast<const uint4*>(l);
     }
+  };
+  {
+    const T* in = static_cast<const T*>(ptr.in[tn]) + base;
+    const float* m = a.r.step ? ptr.m[tn] + base : nullptr;
+    float* mo = a.r.step ? ptr.m_out[tn] + base : nullptr;
+    double sum = 0.0;
+#pragma unroll 2
+    for (int k = t; k < tasks; k += kSmallThreads) {
+      const Task x = task_of(k);
+      float u[8] = {};
+      if (x.here > 0) {
+        load_wide(in + x.at, x.here, u);
+        if (a.r.step) {
+          float v[8];
+          load_wide(m + x.at, x.here, v);
+#pragma unroll
+          for (int i = 0; i < 8; ++i) v[i] = new_momentum(a.r, u[i], v[i]);
+          store_wide(mo + x.at, x.here, v);
+#pragma unroll
+          for (int i = 0; i < 8; ++i) u[i] = i < x.here ? update_of(a.r, u[i], v[i]) : 0.0f;
+        }
+#pragma unroll
+        for (int i = 0; i < 8; ++i) sum = fma((double)u[i], (double)u[i], sum);
+      }
+      uint4 hi, lo;
+      bits8(u, hi, lo);
+      put8(x, hi, lo);
+    }
+    sum = warp_sum(sum);
+    if (lane == 0) warps[warp] = sum;
   }
-  sum = warp_sum(sum);
-  if (lane == 0) warps[warp] = sum;
-  __syncthreads();
+  tc::fence_before_sync();
+  if (S > 1) cluster_sync();  // everyone's shared memory may be written from here on
+  else __syncthreads();
+  tc::fence_after_sync();
+  const uint32_t tmem = *tmem_slot;
   if (t < S) {
     double v = 0.0;
     for (int k = 0; k < kSmallThreads / 32; ++k) v += warps[k];
@@ -686,25 +839,16 @@ __global__ void __launch_bounds__(kSmallThreads, 1)
   double all = 0.0;
   for (int k = 0; k < S; ++k) all += norms[k];
   const float scale = (float)((double)kSx / (sqrt(all) + a.eps));
-  for (int task = t; task < tasks; task += kSmallThreads) {
-    int r, l0;
-    place(task, r, l0);
-    float v[8];
-#pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      float u = 0.0f;
-      if (r < s.R && l0 + i < s.L) {
-        const size_t at = index(r, l0 + i);
-        u = to_f32(in[at]);
-        if (a.r.step) u = a.r.nesterov ? fmaf(a.r.momentum, mo[at], u) : mo[at];
-      }
-      v[i] = u * scale;
-    }
+  for (int k = t; k < tasks; k += kSmallThreads) {
+    const Task x = task_of(k);
     uint4 hi, lo;
+    float v[8];
+    get8(x, hi, lo);
+    unbits8(hi, lo, v);
+#pragma unroll
+    for (int i = 0; i < 8; ++i) v[i] *= scale;
     split8(v, hi, lo);
-    const uint32_t off = (uint32_t)(l0 / 64 - c_lo) * kChunk + sw128(r, (l0 % 64) * 2);
-    *reinterpret_cast<uint4*>(xh + off) = hi;
-    *reinterpret_cast<uint4*>(xl + off) = lo;
+    put8(x, hi, lo);
   }
   tc::fence_proxy_async();
   __syncthreads();
@@ -718,45 +862,56 @@ __global__ void __launch_bounds__(kSmallThreads, 1)
     phase ^= 1;
     tc::fence_after_sync();
   };
-  constexpr int kHalf = RP / 2;       // columns of a half
-  constexpr uint32_t kSmall = 128;    // TMEM column of the small products of A and A A
-  for (int step = 0; step < a.steps; ++step) {
-    if (t == 0) {
-      constexpr uint32_t idesc = idesc_f16(128, RP, false);
-      for (int k = 0; k < mine * 4; ++k) {
-        const uint32_t off = (uint32_t)(k >> 2) * kChunk + (k & 3) * 32;
-        const uint64_t h = tc::desc_sw128(sxh + off, 16, 1024), l = tc::desc_sw128(sxl + off, 16, 1024);
-        tc::mma_bf16(tmem, h, h, idesc, k != 0);
-        tc::mma_bf16(tmem + kSmall, h, l, idesc, k != 0);
-        tc::mma_bf16(tmem + kSmall, l, h, idesc, 1);
-      }
-      tc::mma_commit(done);
+  auto settle = [&]() {  // shared memory as written by all, TMEM as read by all, before the next products
+    tc::fence_proxy_async();
+    tc::fence_before_sync();
+    __syncthreads();
+    tc::fence_after_sync();
+  };
+  // P P^T of hi and lo planes with K-major chunks, K = 16 * steps
+  auto square = [&](uint32_t ph, uint32_t pl, int steps) {
+    constexpr uint32_t idesc = idesc_f16(128, RP, false);
+    for (int k = 0; k < steps; ++k) {
+      const uint32_t off = (uint32_t)(k >> 2) * kChunk + (k & 3) * 32;
+      const uint64_t h = tc::desc_sw128(ph + off, 16, 1024);
+      tc::mma_bf16(tmem, h, h, idesc, k != 0);
+      const uint64_t l = tc::desc_sw128(pl + off, 16, 1024);
+      tc::mma_bf16(tmem + 128, h, l, idesc, k != 0);
+      tc::mma_bf16(tmem + 128, l, h, idesc, 1);
     }
+    tc::mma_commit(done);
+  };
+  constexpr int kRun = RP / kSides;  // columns of A a warp drains
+  constexpr float kToA = kSa / (kSx * kSx);
+  const int shift = 31 - __clz(RP / S);  // log2 of a block of A's columns
+  for (int step = 0; step < a.steps; ++step) {
+    if (t == 0) square(sxh, sxl, mine * 4);
     __syncwarp();
     finish();
-    constexpr float kToA = kSa / (kSx * kSx);
     if (S > 1) {
-      const int blk = RP / S;
       if (live) {
-        for (int c = side * kHalf; c < (side + 1) * kHalf; c += 16) {
-          float v[16];
-          drain16(tw + c, tw + kSmall + c, v);
 #pragma unroll
-          for (int i = 0; i < 16; ++i) {
-            const int col = c + i, dst = col / blk;
-            st_remote(at_rank(tc::smem_u32(recv + (q * blk + col % blk) * RP + row), dst), v[i]);
+        for (int c = side * kRun; c < (side + 1) * kRun; c += 16) {
+          float v[16];
+          drain16(tw + c, tw + 128 + c, v);
+#pragma unroll
+          for (int h = 0; h < 16; h += 8) {  // a block has 8 columns at least; a warp's row is 128 bytes
+            const int col = c + h, dst = col >> shift, at = (q << shift) + (col & ((1 << shift) - 1));
+            const uint32_t to = at_rank(tc::smem_u32(recv + at * RP + row), dst);
+#pragma unroll
+            for (int i = 0; i < 8; ++i) st_remote(to + i * RP * 4, v[h + i]);
           }
         }
       }
+      tc::fence_before_sync();
       cluster_sync();
-      // rows q * blk .. of A (A is symmetric), 8 columns a task, to every CTA
-      for (int task = t; task < blk * (RP / 8); task += kSmallThreads) {
-        const int j = task / (RP / 8), i0 = (task % (RP / 8)) * 8;
-        float v[8];
-#pragma unroll
-        for (int i = 0; i < 8; ++i) v[i] = 0.0f;
+      // rows of block q of A (A is symmetric), 8 columns a task, to every CTA
+      for (int task = t; task < (RP / 8) << shift; task += kSmallThreads) {
+        const int j = task / (RP / 8), i0 = task % (RP / 8) * 8;
+        float v[8] = {};
+#pragma unroll 4
         for (int k = 0; k < S; ++k) {
-          const float4* p = reinterpret_cast<const float4*>(recv + (k * blk + j) * RP + i0);
+          const float4* p = reinterpret_cast<const float4*>(recv + ((k << shift) + j) * RP + i0);
           const float4 x = p[0], y = p[1];
           v[0] += x.x;
           v[1] += x.y;
@@ -771,66 +926,54 @@ __global__ void __launch_bounds__(kSmallThreads, 1)
         for (int i = 0; i < 8; ++i) v[i] *= kToA;
         uint4 hi, lo;
         split8(v, hi, lo);
-        const uint32_t off = (uint32_t)(i0 / 64) * kChunk + sw128(q * blk + j, (i0 % 64) * 2);
+        const uint32_t off = (uint32_t)(i0 / 64) * kChunk + sw128((q << shift) + j, i0 % 64 * 2);
         for (int k = 0; k < S; ++k) {
           st_remote(at_rank(sah + off, k), hi);
           st_remote(at_rank(sal + off, k), lo);
         }
       }
       fence_proxy_async_all();
-      tc::fence_before_sync();
       cluster_sync();
       tc::fence_after_sync();
       fence_proxy_async_all();
     } else {
       if (live) {
-        for (int c = side * kHalf; c < (side + 1) * kHalf; c += 16) {
-          float v[16];
-          drain16(tw + c, tw + kSmall + c, v);
 #pragma unroll
-          for (int h = 0; h < 2; ++h) {
+        for (int c = side * kRun; c < (side + 1) * kRun; c += 16) {
+          float v[16];
+          drain16(tw + c, tw + 128 + c, v);
+#pragma unroll
+          for (int h = 0; h < 16; h += 8) {
             float w[8];
 #pragma unroll
-            for (int i = 0; i < 8; ++i) w[i] = v[8 * h + i] * kToA;
+            for (int i = 0; i < 8; ++i) w[i] = v[h + i] * kToA;
+            const uint32_t off = (uint32_t)((c + h) / 64) * kChunk + sw128(row, (c + h) % 64 * 2);
             uint4 hi, lo;
             split8(w, hi, lo);
-            const uint32_t off = (uint32_t)(c / 64) * kChunk + sw128(row, (c % 64 + 8 * h) * 2);
             *reinterpret_cast<uint4*>(ah + off) = hi;
             *reinterpret_cast<uint4*>(al + off) = lo;
           }
         }
       }
-      tc::fence_proxy_async();
-      tc::fence_before_sync();
-      __syncthreads();
-      tc::fence_after_sync();
+      settle();
     }
-    if (t == 0) {
-      constexpr uint32_t idesc = idesc_f16(128, RP, false);
-      for (int k = 0; k < RP / 16; ++k) {
-        const uint32_t off = (uint32_t)(k >> 2) * kChunk + (k & 3) * 32;
-        const uint64_t h = tc::desc_sw128(sah + off, 16, 1024), l = tc::desc_sw128(sal + off, 16, 1024);
-        tc::mma_bf16(tmem, h, h, idesc, k != 0);
-        tc::mma_bf16(tmem + kSmall, h, l, idesc, k != 0);
-        tc::mma_bf16(tmem + kSmall, l, h, idesc, 1);
-      }
-      tc::mma_commit(done);
-    }
+    if (t == 0) square(sah, sal, RP / 16);
     __syncwarp();
     finish();
     if (live) {
-      for (int c = side * kHalf; c < (side + 1) * kHalf; c += 16) {
-        float v[16];
-        drain16(tw + c, tw + kSmall + c, v);
 #pragma unroll
-        for (int h = 0; h < 2; ++h) {
-          const uint32_t off = (uint32_t)(c / 64) * kChunk + sw128(row, (c % 64 + 8 * h) * 2);
+      for (int c = side * kRun; c < (side + 1) * kRun; c += 16) {
+        float v[16];
+        drain16(tw + c, tw + 128 + c, v);
+#pragma unroll
+        for (int h = 0; h < 16; h += 8) {
+          const uint32_t off = (uint32_t)((c + h) / 64) * kChunk + sw128(row, (c + h) % 64 * 2);
           float w[8];
           join8(*reinterpret_cast<const uint4*>(ah + off), *reinterpret_cast<const uint4*>(al + off), w);
 #pragma unroll
           for (int i = 0; i < 8; ++i)
-            w[i] = kSb * fmaf(a.c, v[8 * h + i] * (1.0f / (kSa * kSa)),
-                              fmaf(a.b, w[i] * (1.0f / kSa), row == c + 8 * h + i ? a.a : 0.0f));
+            w[i] = fmaf(a.c * (kSb / (kSa * kSa)), v[h + i],
+                        fmaf(a.b * (kSb / kSa), w[i], row == c + h + i ? a.a * kSb : 0.0f));
           uint4 hi, lo;
           split8(w, hi, lo);
           *reinterpret_cast<uint4*>(ah + off) = hi;
@@ -838,62 +981,61 @@ __global__ void __launch_bounds__(kSmallThreads, 1)
         }
       }
     }
-    tc::fence_proxy_async();
-    tc::fence_before_sync();
-    __syncthreads();
-    tc::fence_after_sync();
+    settle();
     const bool last = step + 1 == a.steps;
     for (int g0 = 0; g0 < mine; g0 += 4) {  // up to 256 columns at a time
-      const int gn = min(4, mine - g0), cols = gn * 64;
+      const int cols = min(4, mine - g0) * 64;
       if (t == 0) {
         const uint32_t idesc = idesc_f16(128, cols, true);
         for (int k = 0; k < RP / 16; ++k) {
           const uint32_t poff = (uint32_t)(k >> 2) * kChunk + (k & 3) * 32, qoff = (uint32_t)g0 * kChunk + k * 2048;
-          const uint64_t bh = tc::desc_sw128(sah + poff, 16, 1024), bl = tc::desc_sw128(sal + poff, 16, 1024);
+          const uint64_t bh = tc::desc_sw128(sah + poff, 16, 1024);
           const uint64_t yh = tc::desc_sw128(sxh + qoff, kChunk, 1024), yl = tc::desc_sw128(sxl + qoff, kChunk, 1024);
           tc::mma_bf16(tmem, bh, yh, idesc, k != 0);
           tc::mma_bf16(tmem + 256, bh, yl, idesc, k != 0);
-          tc::mma_bf16(tmem + 256, bl, yh, idesc, 1);
+          tc::mma_bf16(tmem + 256, tc::desc_sw128(sal + poff, 16, 1024), yh, idesc, 1);
         }
         tc::mma_commit(done);
       }
       __syncwarp();
       finish();
       if (live) {
-        for (int c = side * (cols / 2); c < (side + 1) * (cols / 2); c += 16) {
+        for (int c = side * (cols / kSides); c < (side + 1) * (cols / kSides); c += 16) {
           float v[16];
           drain16(tw + c, tw + 256 + c, v);
-          const int l0 = (c_lo + g0) * 64 + c;
-          if (!last) {
 #pragma unroll
-            for (int h = 0; h < 2; ++h) {
-              float w[8];
+          for (int h = 0; h < 16; h += 8) {
+            float w[8];
 #pragma unroll
-              for (int i = 0; i < 8; ++i) w[i] = v[8 * h + i] * (1.0f / kSb);
-              uint4 hi, lo;
-              split8(w, hi, lo);
-              const uint32_t off = (uint32_t)(g0 + c / 64) * kChunk + sw128(row, (c % 64 + 8 * h) * 2);
-              *reinterpret_cast<uint4*>(xh + off) = hi;
-              *reinterpret_cast<uint4*>(xl + off) = lo;
-            }
-          } else if (row < s.R && ok) {
-            T* out = static_cast<T*>(ptr.out[tn]) + base;
-            const T* w = a.r.step ? static_cast<const T*>(ptr.w[tn]) + base : nullptr;
-#pragma unroll
-            for (int i = 0; i < 16; ++i) {
-              if (l0 + i >= s.L) break;
-              const size_t at = index(row, l0 + i);
-              float o = v[i] * (1.0f / (kSb * kSx));
-              if (a.r.step) o = fmaf(a.r.keep, to_f32(w[at]), -a.r.rate * o);
-              out[at] = from_f32<T>(o);
-            }
+            for (int i = 0; i < 8; ++i) w[i] = v[h + i] * (last ? 1.0f / (kSb * kSx) : 1.0f / kSb);
+            uint4 hi, lo;
+            if (last) bits8(w, hi, lo);
+            else split8(w, hi, lo);
+            const uint32_t off = (uint32_t)(g0 + (c + h) / 64) * kChunk + sw128(row, (c + h) % 64 * 2);
+            *reinterpret_cast<uint4*>(xh + off) = hi;
+            *reinterpret_cast<uint4*>(xl + off) = lo;
           }
         }
       }
-      tc::fence_proxy_async();
-      tc::fence_before_sync();
-      __syncthreads();
-      tc::fence_after_sync();
+      settle();
+    }
+  }
+  if (ok) {
+    T* out = static_cast<T*>(ptr.out[tn]) + base;
+    const T* w = a.r.step ? static_cast<const T*>(ptr.w[tn]) + base : nullptr;
+#pragma unroll 2
+    for (int k = t; k < tasks; k += kSmallThreads) {
+      const Task x = task_of(k);
+      if (x.here <= 0) continue;
+      uint4 hi, lo;
+      float v[8];
+      get8(x, hi, lo);
+      unbits8(hi, lo, v);
+      float o[8] = {};
+      if (a.r.step) load_wide(w + x.at, x.here, o);
+#pragma unroll
+      for (int i = 0; i < 8; ++i) v[i] = result_of(a.r, o[i], v[i]);
+      store_wide(out + x.at, x.here, v);
     }
   }
   if (warp == 0) tc::tmem_dealloc(tmem, 512);
@@ -917,13 +1059,31 @@ Shape shape_of(int n, int groups, int rows, int cols) {
   return s;
 }
 
-// Splits of the K range (in chunks) of a symmetric product: enough for a pair of CTAs on every
-// two SMs, each of 256 values at least.
+// Splits of the K range of a symmetric product: as many as give every two SMs a pair of CTAs, each
+// of 768 values at least (with one split the product needs no second kernel).
 int splits_of(const Shape& s, int k, int sms) {
   const int nt = s.Rp / kPairTile;
   const long long tiles = (long long)nt * (nt + 1) / 2 * s.nm;
   const int room = (int)std::max<long long>(1, sms / 2 / tiles);
-  return std::max(1, std::min({room, k / 256, kMaxSplits}));
+  return std::max(1, std::min({room, k / 768, kMaxSplits}));
+}
+
+// The next kernel of a chain, brought up while the one before it runs.
+template <typename K, typename... A>
+cudaError_t chain(K k, dim3 grid, int threads, size_t smem, cudaStream_t st, A... args) {
+  cudaLaunchConfig_t cfg{};
+  cfg.gridDim = grid;
+  cfg.blockDim = dim3(threads);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = st;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  cudaError_t e = cudaLaunchKernelEx(&cfg, k, args...);
+  count_launch();
+  return e != cudaSuccess ? e : cudaGetLastError();
 }
 
 size_t align256(size_t v) { return (v + 255) & ~size_t(255); }
@@ -974,9 +1134,7 @@ cudaError_t product(const CUtensorMap& p, const CUtensorMap& q, const Pointers& 
   cudaError_t e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kProductSmem);
   if (e != cudaSuccess) return e;
   const int tiles = MODE == kSymmetric ? a.tn * (a.tn + 1) / 2 : a.tm * a.tn;
-  k<<<dim3(2 * tiles * a.S, a.s.nm), kProductThreads, kProductSmem, st>>>(p, q, ptr, a);
-  count_launch();
-  return cudaGetLastError();
+  return chain(k, dim3(2 * tiles * a.S, a.s.nm), kProductThreads, kProductSmem, st, p, q, ptr, a);
 }
 
 struct SmallPlan {
@@ -985,18 +1143,22 @@ struct SmallPlan {
   size_t smem = 0;
 };
 
-// The one-launch form serves up to 128 rows whose columns fit the shared memory of a cluster.  The
-// cluster is as large as the GPU has SMs for all matrices, and no smaller than what holds a matrix.
+// The one-launch form serves up to 128 rows whose columns fit the shared memory of a cluster.  A
+// step costs as much as three chunks besides its CTA's own, and the exchange between CTAs one more
+// (measured: 48 matrices of 64 x 576 in 74, 55 and 81 us on clusters of 1, 2 and 4).
 SmallPlan small_plan(const Shape& s, int sms) {
   SmallPlan p;
   if (s.R > 128) return p;
   p.rp = s.R <= 64 ? 64 : 128;
   p.nc = (s.L + 63) / 64;
+  long long best = 0;
   for (int S = 1; S <= kSmallMaxCluster && S <= p.nc; S *= 2) {
     const int most = (p.nc + S - 1) / S;
     const size_t smem = small_layout(p.rp, S, most).total + 1024;
     if (smem > kSmallSmem) continue;
-    if (p.ok && (long long)s.nm * S > sms) break;
+    const long long waves = ((long long)s.nm * S + sms - 1) / sms, cost = waves * (most + 3 + (S > 1 ? 1 : 0));
+    if (p.ok && cost >= best) continue;
+    best = cost;
     p.ok = true;
     p.S = S;
     p.max_chunks = most;
@@ -1066,31 +1228,32 @@ cudaError_t run_chunk(const MuonArgs& a, int t0, int n, char* ws, int sms, cudaS
   ns_norm_kernel<T><<<dim3(blocks, s.nm), 256, 0, st>>>(ptr, s, r, norm);
   count_launch();
   if ((e = cudaGetLastError()) != cudaSuccess) return e;
-  ns_load_kernel<T><<<dim3(s.Lp / 64, s.Rp / 64, s.nm), 256, 0, st>>>(ptr, s, r, a.eps, norm, blocks, x[0]);
-  count_launch();
-  if ((e = cudaGetLastError()) != cudaSuccess) return e;
+  if ((e = chain(ns_load_kernel<T>, dim3(s.Lp / 64, s.Rp / 64, s.nm), 256, 0, st, ptr, s, r, a.eps,
+                 (const double*)norm, blocks, x[0])) != cudaSuccess)
+    return e;
   ProductArgs g{};
   g.s = s;
   g.r = r;
   g.part = part;
   const int nt = s.Rp / 64;
   const dim3 red(nt * (nt + 1) / 2, s.nm);
+  // P P^T into dst, as `f` says
+  auto square = [&](const CUtensorMap& p, int k, const Becomes& f, __half* dst) {
+    g.tm = g.tn = s.Rp / kPairTile;
+    g.chunks = k / kBk;
+    g.S = splits_of(s, k, sms);
+    g.f = f;
+    g.dst = dst;
+    cudaError_t err = product<T, kSymmetric>(p, p, ptr, g, st);
+    if (err == cudaSuccess && g.S > 1) err = chain(ns_reduce_kernel, red, 256, 0, st, (const float*)part, s, g.S, f, dst);
+    return err;
+  };
   for (int k = 0; k < a.steps; ++k) {
     const int now = k & 1;
-    g.tm = g.tn = s.Rp / kPairTile;
-    g.chunks = s.Lp / kBk;
-    g.S = splits_of(s, s.Lp, sms);
-    if ((e = product<T, kSymmetric>(mx[now], mx[now], ptr, g, st)) != cudaSuccess) return e;
-    ns_reduce_kernel<false><<<red, 256, 0, st>>>(part, s, g.S, a.a, a.b, a.c, nullptr, am);
-    count_launch();
-    if ((e = cudaGetLastError()) != cudaSuccess) return e;
-    g.chunks = s.Rp / kBk;
-    g.S = splits_of(s, s.Rp, sms);
-    if ((e = product<T, kSymmetric>(ma, ma, ptr, g, st)) != cudaSuccess) return e;
-    ns_reduce_kernel<true><<<red, 256, 0, st>>>(part, s, g.S, a.a, a.b, a.c, am, bm);
-    count_launch();
-    if ((e = cudaGetLastError()) != cudaSuccess) return e;
+    if ((e = square(mx[now], s.Lp, Becomes{a.a, a.b, a.c, nullptr}, am)) != cudaSuccess) return e;
+    if ((e = square(ma, s.Rp, Becomes{a.a, a.b, a.c, am}, bm)) != cudaSuccess) return e;
     g.S = 1;
+    g.chunks = s.Rp / kBk;
     g.tn = s.Lp / kPairTile;
     g.dst = x[now ^ 1];
     e = k + 1 < a.steps ? product<T, kUpdate>(mb, mx[now], ptr, g, st) : product<T, kFinal>(mb, mx[now], ptr, g, st);
