@@ -12,7 +12,7 @@
 // lo lo, is below 2^-22.  The two small products go into an accumulator of their own.  The tensor
 // core cuts what it adds to an accumulator instead of rounding it (chains of 512 values left a
 // 1024 x 9216 result 3.5e-5 off, 8 times fp32's error), so the large product is taken out and
-// added in registers every 64 to 192 values.  Scales: X by 2^12, A by 2^11, B by 2^9, so
+// added in registers every 64 values (192 in the one-launch form).  Scales: X by 2^12, A by 2^11, B by 2^9, so
 // that |X| <= 16, |A| <= 32, |B| <= 128 stay finite in fp16; lo by 2^11 more, which puts it at hi's
 // size, so that it keeps its bits for entries far below the largest.
 #include <cuda.h>
@@ -1060,12 +1060,14 @@ Shape shape_of(int n, int groups, int rows, int cols) {
 }
 
 // Splits of the K range of a symmetric product: as many as give every two SMs a pair of CTAs, each
-// of 768 values at least (with one split the product needs no second kernel).
+// of 256 values at least, unless the second kernel that they need (7 us) costs more than the
+// chunks (1.3 us) that they save.
 int splits_of(const Shape& s, int k, int sms) {
-  const int nt = s.Rp / kPairTile;
+  const int nt = s.Rp / kPairTile, chunks = k / kBk;
   const long long tiles = (long long)nt * (nt + 1) / 2 * s.nm;
   const int room = (int)std::max<long long>(1, sms / 2 / tiles);
-  return std::max(1, std::min({room, k / 768, kMaxSplits}));
+  const int S = std::max(1, std::min({room, chunks / 4, kMaxSplits}));
+  return (chunks - chunks / S) * 13 < 70 ? 1 : S;
 }
 
 // The next kernel of a chain, brought up while the one before it runs.

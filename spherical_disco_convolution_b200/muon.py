@@ -10,6 +10,8 @@ all tensors of one shape together.  fp32 or bf16; momentum is always fp32.
 
 from __future__ import annotations
 
+import functools
+
 import torch
 
 from . import disco as D
@@ -43,9 +45,12 @@ def _buckets(ts):
     return by.values()
 
 
-def _workspace(n, groups, rows, cols, device):
-    nb = D.disco_orthogonalize_workspace_size(n, groups, rows, cols)
-    return torch.empty(nb, dtype=torch.uint8, device=device), nb
+_workspace_size = functools.lru_cache(maxsize=1024)(D.disco_orthogonalize_workspace_size)
+
+
+def _workspace(x, n, groups, rows, cols):
+    nb = _workspace_size(n, groups, rows, cols)
+    return x.new_empty(nb, dtype=torch.uint8), nb
 
 
 def orthogonalize(update, groups: int = 1, steps: int = 5, coefficients=COEFFICIENTS, eps: float = 1e-7):
@@ -60,7 +65,7 @@ def orthogonalize(update, groups: int = 1, steps: int = 5, coefficients=COEFFICI
     for at in _buckets(ts):
         first = ts[at[0]]
         rows, cols = _matrix(first, groups)
-        ws, nb = _workspace(len(at), groups, rows, cols, first.device)
+        ws, nb = _workspace(first, len(at), groups, rows, cols)
         launch(first, D.disco_orthogonalize, groups, rows, cols, DTYPES[first.dtype], ns, [ts[i].data_ptr() for i in at],
                [outs[i].data_ptr() for i in at], ws.data_ptr(), nb)
     return outs[0] if single else outs
@@ -94,7 +99,7 @@ def muon_update(weight, grad, momentum_buffer, lr: float, momentum: float = 0.95
     for at in _buckets(ws_):
         first = ws_[at[0]]
         rows, cols = _matrix(first, groups)
-        ws, nb = _workspace(len(at), groups, rows, cols, first.device)
+        ws, nb = _workspace(first, len(at), groups, rows, cols)
         ptrs = [[ts[i].data_ptr() for i in at] for ts in (ws_, gs, ms, w_out, m_out)]
         launch(first, D.disco_muon, groups, rows, cols, DTYPES[first.dtype], ns, lr, momentum, nesterov, weight_decay,
                *ptrs, ws.data_ptr(), nb)

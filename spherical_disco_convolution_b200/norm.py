@@ -8,12 +8,15 @@ fp32 or bf16, all tensors of a call in one type; statistics and sums are fp32.
 
 from __future__ import annotations
 
+import functools
 import math
 
 import torch
 
 from . import disco as D
 from ._launch import dense, launch, like
+
+_workspace_size = functools.lru_cache(maxsize=1024)(D.disco_norm_workspace_size)
 
 
 def _sizes(x):
@@ -32,7 +35,7 @@ def layer_norm(x: torch.Tensor, gain=None, bias=None, eps: float = 1e-5):
     gain = like(gain, x, (C,), "gain")
     bias = like(bias, x, (C,), "bias")
     out = torch.empty_like(x)
-    stats = torch.empty((2, B, *x.shape[2:]), dtype=torch.float32, device=x.device)
+    stats = x.new_empty((2, B, *x.shape[2:]), dtype=torch.float32)
     launch(x, D.disco_norm, B, C, n, code, x.data_ptr(), gain, bias, eps, out.data_ptr(), stats.data_ptr())
     return out, stats
 
@@ -55,8 +58,8 @@ def layer_norm_backward(dout: torch.Tensor, x: torch.Tensor, stats: torch.Tensor
     dbias = x.new_empty(C) if need_bias else None
     ws, nb = None, 0
     if need_gain or need_bias:
-        nb = D.disco_norm_workspace_size(B, C, n, code)
-        ws = torch.empty(nb, dtype=torch.uint8, device=x.device)
+        nb = _workspace_size(B, C, n, code)
+        ws = x.new_empty(nb, dtype=torch.uint8)
     launch(x, D.disco_norm_backward, B, C, n, code, dout, x.data_ptr(), stats.data_ptr(), gain,
            None if dx is None else dx.data_ptr(), None if dgain is None else dgain.data_ptr(),
            None if dbias is None else dbias.data_ptr(), None if ws is None else ws.data_ptr(), nb)
