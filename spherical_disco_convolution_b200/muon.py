@@ -15,7 +15,7 @@ import functools
 import torch
 
 from . import disco as D
-from ._launch import DTYPES, dense, launch, like
+from ._launch import DTYPES, dense, launch
 
 COEFFICIENTS = (3.4445, -4.7750, 2.0315)
 
@@ -39,9 +39,13 @@ def _as_list(ts, what):
 
 def _buckets(ts):
     """Indices of the tensors that one call can take together."""
+    x = ts[0]
+    shape, dtype, device = x.shape, x.dtype, x.device
+    if all(t.shape == shape and t.dtype == dtype and t.device == device for t in ts):
+        return [range(len(ts))]
     by = {}
     for i, t in enumerate(ts):
-        by.setdefault((tuple(t.shape), t.dtype, t.device), []).append(i)
+        by.setdefault((t.shape, t.dtype, t.device), []).append(i)
     return by.values()
 
 
@@ -53,21 +57,33 @@ def _workspace(x, n, groups, rows, cols):
     return x.new_empty(nb, dtype=torch.uint8), nb
 
 
+def _pointers(ts, x, what, dtype=None):
+    """Pointers of dense tensors of x's shape and device, and of its type or the one given."""
+    shape, device, dtype = x.shape, x.device, dtype or x.dtype
+    for t in ts:
+        if t.dtype != dtype:
+            raise TypeError(f"{what} is {dtype} here, not {t.dtype}")
+        if t.shape != shape or t.device != device or not t.is_contiguous():
+            raise ValueError(f"{what} is contiguous, of shape {tuple(shape)}, on {device}")
+    return [t.data_ptr() for t in ts]
+
+
 def orthogonalize(update, groups: int = 1, steps: int = 5, coefficients=COEFFICIENTS, eps: float = 1e-7):
     """The nearly orthogonal factor of each group's matrix of `update` (one tensor, or a list):
     X = U / (|U| + eps), then `steps` times X <- a X + b (X X^T) X + c (X X^T)^2 X."""
     ts, single = _as_list(update, "update")
-    for t in ts:
-        dense(t, "update")
-        _matrix(t, groups)
     ns = D.newton_schulz(steps, coefficients, eps)
-    outs = [torch.empty_like(t, requires_grad=False) for t in ts]
+    outs = [None] * len(ts)
     for at in _buckets(ts):
-        first = ts[at[0]]
-        rows, cols = _matrix(first, groups)
-        ws, nb = _workspace(first, len(at), groups, rows, cols)
-        launch(first, D.disco_orthogonalize, groups, rows, cols, DTYPES[first.dtype], ns, [ts[i].data_ptr() for i in at],
-               [outs[i].data_ptr() for i in at], ws.data_ptr(), nb)
+        x = ts[at[0]]
+        code = dense(x, "update")
+        rows, cols = _matrix(x, groups)
+        u = _pointers([ts[i] for i in at], x, "update")
+        out = [torch.empty_like(x, requires_grad=False) for _ in at]
+        ws, nb = _workspace(x, len(at), groups, rows, cols)
+        launch(x, D.disco_orthogonalize, groups, rows, cols, code, ns, u, [o.data_ptr() for o in out], ws.data_ptr(), nb)
+        for i, o in zip(at, out):
+            outs[i] = o
     return outs[0] if single else outs
 
 
@@ -78,31 +94,30 @@ def muon_update(weight, grad, momentum_buffer, lr: float, momentum: float = 0.95
     m' = momentum * m + grad, U = grad + momentum * m' (nesterov) or m', and
     w' = (1 - lr * weight_decay) * w - lr * sqrt(max(1, rows / cols)) * orthogonalize(U).
     momentum_buffer is fp32.  inplace writes both results into the tensors given."""
-    ws_, single = _as_list(weight, "weight")
+    ws, single = _as_list(weight, "weight")
     gs, _ = _as_list(grad, "grad")
     ms, _ = _as_list(momentum_buffer, "momentum_buffer")
-    if not len(ws_) == len(gs) == len(ms):
-        raise ValueError(f"{len(ws_)} weights, {len(gs)} gradients and {len(ms)} momentum buffers")
-    for w, g, m in zip(ws_, gs, ms):
-        dense(w, "weight")
-        _matrix(w, groups)
-        like(g, w, w.shape, "grad")
-        if m.dtype != torch.float32:
-            raise TypeError(f"momentum_buffer is float32, not {m.dtype}")
-        if not m.is_contiguous() or m.shape != w.shape or m.device != w.device:
-            raise ValueError("momentum_buffer is contiguous, of the weight's shape, on its device")
-    if inplace and len({t.data_ptr() for t in ws_ + ms}) < 2 * len(ws_):
-        raise ValueError("a tensor is given twice: each is updated once")
+    if not len(ws) == len(gs) == len(ms):
+        raise ValueError(f"{len(ws)} weights, {len(gs)} gradients and {len(ms)} momentum buffers")
     ns = D.newton_schulz(steps, coefficients, eps)
-    w_out = ws_ if inplace else [torch.empty_like(t, requires_grad=False) for t in ws_]
+    calls = []
+    for at in _buckets(ws):  # everything is checked before anything is written
+        x = ws[at[0]]
+        code = dense(x, "weight")
+        rows, cols = _matrix(x, groups)
+        w = _pointers([ws[i] for i in at], x, "weight")
+        g = _pointers([gs[i] for i in at], x, "grad")
+        m = _pointers([ms[i] for i in at], x, "momentum_buffer", torch.float32)
+        calls.append((at, x, code, rows, cols, w, g, m))
+    if inplace and len({p for c in calls for p in c[5] + c[7]}) < 2 * len(ws):
+        raise ValueError("a tensor is given twice: each is updated once")
+    w_out = ws if inplace else [torch.empty_like(t, requires_grad=False) for t in ws]
     m_out = ms if inplace else [torch.empty_like(t, requires_grad=False) for t in ms]
-    for at in _buckets(ws_):
-        first = ws_[at[0]]
-        rows, cols = _matrix(first, groups)
-        ws, nb = _workspace(first, len(at), groups, rows, cols)
-        ptrs = [[ts[i].data_ptr() for i in at] for ts in (ws_, gs, ms, w_out, m_out)]
-        launch(first, D.disco_muon, groups, rows, cols, DTYPES[first.dtype], ns, lr, momentum, nesterov, weight_decay,
-               *ptrs, ws.data_ptr(), nb)
+    for at, x, code, rows, cols, w, g, m in calls:
+        work, nb = _workspace(x, len(at), groups, rows, cols)
+        launch(x, D.disco_muon, groups, rows, cols, code, ns, lr, momentum, nesterov, weight_decay, w, g, m,
+               w if inplace else [w_out[i].data_ptr() for i in at], m if inplace else [m_out[i].data_ptr() for i in at],
+               work.data_ptr(), nb)
     return (w_out[0], m_out[0]) if single else (w_out, m_out)
 
 
