@@ -489,48 +489,54 @@ __global__ void __launch_bounds__(kProductThreads, 1) __cluster_dims__(2, 1, 1)
     const size_t pa = (size_t)s.nm * s.Rp * s.Rp, px = (size_t)s.nm * s.Rp * s.Lp;
     const size_t tensor = (size_t)(mi % s.groups) * s.rows * s.cols;
     if (ok && !(MODE == kFinal && s.tr)) {
-#pragma unroll 1
-      for (int r = warp; r < kTile; r += kDrainWarps) {  // a warp takes a row, a lane 8 columns
-        const uint8_t* from = smem + r * 1024;
-        const uint32_t turn = (uint32_t)r & 7u;
-        const float4 x = *reinterpret_cast<const float4*>(from + (((2u * lane) ^ turn) << 4));
-        const float4 y = *reinterpret_cast<const float4*>(from + (((2u * lane + 1u) ^ turn) << 4));
-        float v[8] = {x.x, x.y, x.z, x.w, y.x, y.y, y.z, y.w};
-        const int grow = m0 + r, col = n0 + lane * 8;
-        if constexpr (MODE == kSymmetric) {
-          const size_t at = ((size_t)mi * s.Rp + grow) * s.Rp + col;
-          if (a.S > 1) {
-            float4* dst = reinterpret_cast<float4*>(a.part + (size_t)split_k * pa + at);
-            dst[0] = x;
-            dst[1] = y;
-          } else {
+      if (MODE == kSymmetric && a.S > 1) {
+#pragma unroll 2
+        for (int r = warp; r < kTile; r += kDrainWarps) {  // a warp takes a row, a lane 4 columns and 4 more
+          const uint8_t* from = smem + r * 1024;
+          float* dst = a.part + (size_t)split_k * pa + ((size_t)mi * s.Rp + m0 + r) * s.Rp + n0 + lane * 4;
+#pragma unroll
+          for (int h = 0; h < 2; ++h)
+            *reinterpret_cast<float4*>(dst + 128 * h) =
+                *reinterpret_cast<const float4*>(from + ((uint32_t)((lane + 32 * h) ^ (r & 7)) << 4));
+        }
+      } else {
+#pragma unroll 2
+        for (int r = warp; r < kTile; r += kDrainWarps) {  // a warp takes a row, a lane 8 columns
+          uint8_t* from = smem + r * 1024;
+          const uint32_t turn = (uint32_t)r & 7u;
+          float4* px0 = reinterpret_cast<float4*>(from + (((2u * lane) ^ turn) << 4));
+          float4* px1 = reinterpret_cast<float4*>(from + (((2u * lane + 1u) ^ turn) << 4));
+          float v[8] = {px0->x, px0->y, px0->z, px0->w, px1->x, px1->y, px1->z, px1->w};
+          const int grow = m0 + r, col = n0 + lane * 8;
+          if constexpr (MODE == kSymmetric) {
+            const size_t at = ((size_t)mi * s.Rp + grow) * s.Rp + col;
             become(a.f, pa, at, grow - col, v);
             uint4 hi, lo;
             split8(v, hi, lo);
             *reinterpret_cast<uint4*>(a.dst + at) = hi;
             *reinterpret_cast<uint4*>(a.dst + pa + at) = lo;
             if (bm != bn) {  // for the mirror image
-              *reinterpret_cast<float4*>(smem + r * 1024 + (((2u * lane) ^ turn) << 4)) = make_float4(v[0], v[1], v[2], v[3]);
-              *reinterpret_cast<float4*>(smem + r * 1024 + (((2u * lane + 1u) ^ turn) << 4)) = make_float4(v[4], v[5], v[6], v[7]);
+              *px0 = make_float4(v[0], v[1], v[2], v[3]);
+              *px1 = make_float4(v[4], v[5], v[6], v[7]);
             }
-          }
-        } else if constexpr (MODE == kUpdate) {
-          const size_t at = ((size_t)mi * s.Rp + grow) * s.Lp + col;
+          } else if constexpr (MODE == kUpdate) {
+            const size_t at = ((size_t)mi * s.Rp + grow) * s.Lp + col;
 #pragma unroll
-          for (int i = 0; i < 8; ++i) v[i] *= 1.0f / kSb;
-          uint4 hi, lo;
-          split8(v, hi, lo);
-          *reinterpret_cast<uint4*>(a.dst + at) = hi;
-          *reinterpret_cast<uint4*>(a.dst + px + at) = lo;
-        } else {
-          const int here = grow < s.R ? max(0, min(8, s.L - col)) : 0;
-          if (here > 0) {
-            const size_t at = tensor + (size_t)grow * s.cols + col;
-            float w[8] = {};
-            if (a.r.step) load_wide(static_cast<const T*>(ptr.w[mi / s.groups]) + at, here, w);
+            for (int i = 0; i < 8; ++i) v[i] *= 1.0f / kSb;
+            uint4 hi, lo;
+            split8(v, hi, lo);
+            *reinterpret_cast<uint4*>(a.dst + at) = hi;
+            *reinterpret_cast<uint4*>(a.dst + px + at) = lo;
+          } else {
+            const int here = grow < s.R ? max(0, min(8, s.L - col)) : 0;
+            if (here > 0) {
+              const size_t at = tensor + (size_t)grow * s.cols + col;
+              float w[8] = {};
+              if (a.r.step) load_wide(static_cast<const T*>(ptr.w[mi / s.groups]) + at, here, w);
 #pragma unroll
-            for (int i = 0; i < 8; ++i) v[i] = result_of(a.r, w[i], v[i] * (1.0f / (kSb * kSx)));
-            store_wide(static_cast<T*>(ptr.out[mi / s.groups]) + at, here, v);
+              for (int i = 0; i < 8; ++i) v[i] = result_of(a.r, w[i], v[i] * (1.0f / (kSb * kSx)));
+              store_wide(static_cast<T*>(ptr.out[mi / s.groups]) + at, here, v);
+            }
           }
         }
       }
