@@ -319,7 +319,7 @@ disco_status disco_norm_backward(int B, int C, long long npts, disco_dtype dtype
  * aligned.  Both calls are asynchronous on `stream`, allocate nothing and give the same bits every
  * time.  Errors: DISCO_ERR_INVALID_ARG for a non-positive size, a NULL pointer or one off its
  * element's alignment, an unknown dtype, steps outside 1..32, a coefficient that is not finite or
- * above 32 in magnitude, eps not positive, a scalar that is not finite, momentum outside [0, 1),
+ * above 32 in magnitude, eps below 1e-30 or not finite, a scalar that is not finite, momentum outside [0, 1),
  * or a missing or short workspace; DISCO_ERR_UNSUPPORTED for n * groups above 65535 or a matrix
  * side above 32768; DISCO_ERR_CUDA for a failed launch. */
 typedef struct {

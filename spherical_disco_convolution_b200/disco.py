@@ -411,6 +411,6 @@ def disco_orthogonalize(groups, rows, cols, dtype, ns, update, out, workspace, w
 def disco_muon(groups, rows, cols, dtype, ns, lr, momentum, nesterov, weight_decay, w, grad, m, w_out, m_out,
                workspace, ws_bytes, stream) -> None:
     """w, grad, m, w_out and m_out: lists of n device pointers."""
-    _check(_lib.disco_muon(len(w), groups, rows, cols, dtype, ctypes.byref(ns), lr, momentum, int(nesterov),
-                           weight_decay, _pointers(w), _pointers(grad), _pointers(m), _pointers(w_out),
+    _check(_lib.disco_muon(len(w), groups, rows, cols, dtype, ctypes.byref(ns), float(lr), float(momentum),
+                           int(nesterov), float(weight_decay), _pointers(w), _pointers(grad), _pointers(m), _pointers(w_out),
                            _pointers(m_out), workspace, ws_bytes, stream))

@@ -133,13 +133,20 @@ class Muon(torch.optim.Optimizer):
                  eps: float = 1e-7):
         super().__init__(params, dict(lr=lr, momentum=momentum, nesterov=nesterov, weight_decay=weight_decay,
                                       groups=groups, steps=steps, coefficients=tuple(coefficients), eps=eps))
-        for group in self.param_groups:
+
+    def add_param_group(self, param_group):
+        super().add_param_group(param_group)
+        group = self.param_groups[-1]
+        try:
             for p in group["params"]:
                 _matrix(p, group["groups"])
                 if p.dtype not in DTYPES:
                     raise TypeError(f"unsupported dtype {p.dtype}; use float32 or bfloat16")
                 if not p.is_contiguous():
                     raise ValueError("Muon takes contiguous parameters")
+        except (TypeError, ValueError):
+            self.param_groups.pop()
+            raise
 
     @torch.no_grad()
     def step(self, closure=None):

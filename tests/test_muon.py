@@ -43,7 +43,7 @@ def _muon(lr=0.1, momentum=0.9, wd=0.0, w=(P,), g=(P,), m=(P,), wo=(P,), mo=(P,)
 @pytest.mark.parametrize("kw,want", [
     (dict(groups=0), 1), (dict(rows=0), 1), (dict(cols=-3), 1), (dict(dtype=2), 1), (dict(steps=0), 1),
     (dict(steps=33), 1), (dict(coef=(math.nan, 0, 0)), 1), (dict(coef=(1, 33, 0)), 1), (dict(coef=(1, 0, -math.inf)), 1),
-    (dict(eps=0.0), 1), (dict(eps=-1.0), 1), (dict(eps=math.nan), 1), (dict(ps=(None,)), 1), (dict(outs=(None,)), 1),
+    (dict(eps=0.0), 1), (dict(eps=-1.0), 1), (dict(eps=9e-31), 1), (dict(eps=math.inf), 1), (dict(eps=math.nan), 1), (dict(ps=(None,)), 1), (dict(outs=(None,)), 1),
     (dict(ps=(P + 2,)), 1), (dict(outs=(P + 1,), dtype=1), 1), (dict(ws=None), 1), (dict(ws=P + 128), 1),
     (dict(nb=64), 1), (dict(ps=(), outs=()), 1), (dict(groups=65536), 2), (dict(rows=32769), 2), (dict(cols=40000), 2),
 ])
@@ -78,6 +78,10 @@ def test_python_refuses():
             call()
     with pytest.raises(TypeError):
         muon.Muon([torch.nn.Parameter(w.half())])
+    opt = muon.Muon([torch.nn.Parameter(w)])
+    with pytest.raises(ValueError):
+        opt.add_param_group({"params": [torch.nn.Parameter(torch.zeros(4))]})
+    assert len(opt.param_groups) == 1
 
 
 def test_momentum_stays_fp32_through_a_checkpoint():
@@ -318,6 +322,28 @@ def test_bases_off_sixteen_bytes_and_neighbours_untouched(shape, dtype, cuda):
                           ws.data_ptr(), nb, torch.cuda.current_stream().cuda_stream)
     assert torch.equal(buf[31:31 + n].view(shape), want)
     assert (buf[:31] == 3).all() and (buf[31 + n:] == 3).all()
+
+
+@gpu
+@pytest.mark.parametrize("shape", [(20, 50), (60, 12), (140, 260), (90, 1000)])
+def test_the_result_may_replace_the_update(shape, cuda):
+    u = update(shape, F32, 17, cuda)
+    want = muon.orthogonalize(u)
+    nb = D.disco_orthogonalize_workspace_size(1, 1, *shape)
+    ws = torch.empty(nb, dtype=torch.uint8, device=cuda)
+    D.disco_orthogonalize(1, *shape, D.DISCO_F32, D.newton_schulz(5, NS, 1e-7), [u.data_ptr()], [u.data_ptr()],
+                          ws.data_ptr(), nb, torch.cuda.current_stream().cuda_stream)
+    assert torch.equal(u, want)
+
+
+@gpu
+def test_least_eps_and_scalars_as_tensors(cuda):
+    assert (muon.orthogonalize(torch.zeros(20, 50, device=cuda), eps=1e-30) == 0).all()
+    assert (muon.orthogonalize(torch.zeros(200, 300, device=cuda), eps=1e-30) == 0).all()
+    w, g, m = (torch.randn(12, 30, device=cuda) for _ in range(3))
+    a = muon.muon_update(w, g, m, torch.tensor(0.1), momentum=torch.tensor(0.5), weight_decay=torch.tensor(0.25))
+    b = muon.muon_update(w, g, m, 0.1, momentum=0.5, weight_decay=0.25)
+    assert torch.allclose(a[0], b[0], rtol=1e-6) and torch.equal(a[1], b[1])
 
 
 @gpu
