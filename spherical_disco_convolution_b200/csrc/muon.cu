@@ -30,7 +30,6 @@ namespace {
 
 constexpr float kSx = 4096.0f, kSa = 2048.0f, kSb = 512.0f, kSl = 2048.0f;
 constexpr int kTile = 128;       // a CTA's rows of a product's tile, and its share of the operands
-constexpr int kPairTile = 256;   // the tile of a pair of CTAs
 constexpr int kBk = 64;          // K values per stage: one 128-byte swizzle row of fp16
 constexpr int kMaxSplits = 8;    // of the K range of a symmetric product
 constexpr int kStages = 3;
@@ -51,7 +50,8 @@ struct Pointers {
 
 struct Shape {
   int groups, rows, cols;
-  int R, L, Rp, Lp;  // iterated matrix (R <= L) and its padded sides, multiples of kPairTile
+  int R, L, Rp, Lp;  // iterated matrix (R <= L) and its padded sides, multiples of `tile`
+  int tile;          // side of a product's tile: 256 (a pair of CTAs) or 128 (one CTA)
   bool tr;           // iterated on the transposed matrix
   int nm;            // matrices
 };
@@ -287,16 +287,18 @@ __device__ __forceinline__ void become(const Becomes& f, size_t plane, size_t at
     v[i] = fmaf(f.c * (kSb / (kSa * kSa)), v[i], fmaf(f.b * (kSb / kSa), x[i], i == diag ? f.a * kSb : 0.0f));
 }
 
-// A pair of CTAs (cta_group::2) makes one 256 x 256 tile of a product of hi + lo matrices:
-// D = P P^T (kSymmetric, both operands K-major, tiles on and above the diagonal only) or D = P Q
-// (kUpdate, kFinal; Q is read as an MN-major operand).  Each CTA brings 128 rows of P and 128 columns
-// of Q and gets 128 rows of D, so that 64 KB from L2 feed 1536 cycles of MMA: one CTA with a 128 x 128
-// tile needs 64 KB for 768, more than L2 gives (measured: 2.4x slower on 1024 x 9216).
+// One tile of a product of hi + lo matrices: D = P P^T (kSymmetric, both operands K-major, tiles on
+// and above the diagonal only) or D = P Q (kUpdate, kFinal; Q is read as an MN-major operand).
+//
+// PAIR: two CTAs (cta_group::2) make a 256 x 256 tile.  Each brings 128 rows of P and 128 columns of Q
+// and gets 128 rows of D, so that 64 KB from L2 feed 1536 cycles of MMA; one CTA with a 128 x 128 tile
+// needs 64 KB for 768, more than L2 gives when all SMs ask (1024 x 9216: 2.4x slower).  Below one
+// tile for every pair latency counts instead, and one CTA makes a 128 x 128 tile.
 //
 // Warp 16 streams the four operand tiles of each K chunk by TMA, all counted on the first CTA's
 // barrier; lane 0 of the first CTA's warp 17 issues the MMAs for both; warps 0..15 of both CTAs add
-// the chunk's large product to their sums (TMEM lane = row of the tile, 64 columns a warp) while the
-// MMAs of its small products run.
+// the chunk's large product to their sums (TMEM lane = row of the tile, a quarter of the columns a
+// warp) while the MMAs of its small products run.
 __device__ __forceinline__ uint32_t cluster_rank() {
   uint32_t r;
   asm volatile("mov.u32 %0, %cluster_ctarank;" : "=r"(r));
@@ -341,8 +343,8 @@ __device__ __forceinline__ void arrive_remote(uint32_t bar) {
   asm volatile("mbarrier.arrive.shared::cluster.b64 _, [%0];" ::"r"(bar) : "memory");
 }
 
-template <typename T, Product MODE>
-__global__ void __launch_bounds__(kProductThreads, 1) __cluster_dims__(2, 1, 1)
+template <typename T, Product MODE, bool PAIR>
+__global__ void __launch_bounds__(kProductThreads, 1)
     ns_product_kernel(const __grid_constant__ CUtensorMap map_p, const __grid_constant__ CUtensorMap map_q,
                       const __grid_constant__ Pointers ptr, const __grid_constant__ ProductArgs a) {
   extern __shared__ uint8_t smem_raw[];
@@ -350,14 +352,16 @@ __global__ void __launch_bounds__(kProductThreads, 1) __cluster_dims__(2, 1, 1)
   uint64_t* full = reinterpret_cast<uint64_t*>(smem + kStages * kStageBytes);
   uint64_t* empty = full + kStages;
   uint64_t* tfull = empty + kStages;  // the chunk's large product is in TMEM
-  uint64_t* tempty = tfull + 1;       // and both CTAs have read it
+  uint64_t* tempty = tfull + 1;       // and every CTA has read it
   uint64_t* done = tempty + 1;
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(done + 1);
   constexpr bool kMn = MODE != kSymmetric;
+  constexpr int kCtas = PAIR ? 2 : 1, kSide = kCtas * kTile, kCols = kSide / 4;  // columns of a warp
   const Shape& s = a.s;
-  const uint32_t rank = cluster_rank();
-  int tile = (int)(blockIdx.x >> 1) / a.S, bm = 0, bn = 0;
-  const int split_k = (int)(blockIdx.x >> 1) % a.S;
+  const uint32_t rank = PAIR ? cluster_rank() : 0;
+  const int job = (int)blockIdx.x / kCtas;
+  int tile = job / a.S, bm = 0, bn = 0;
+  const int split_k = job % a.S;
   if (MODE == kSymmetric) {
     while (tile >= a.tn - bm) tile -= a.tn - bm++;
     bn = bm + tile;
@@ -365,10 +369,14 @@ __global__ void __launch_bounds__(kProductThreads, 1) __cluster_dims__(2, 1, 1)
     bm = tile % a.tm;
     bn = tile / a.tm;
   }
-  const int m0 = bm * kPairTile + (int)rank * kTile, n0 = bn * kPairTile, qn = n0 + (int)rank * kTile;
+  const int m0 = bm * kSide + (int)rank * kTile, n0 = bn * kSide, qn = n0 + (int)rank * kTile;
   const int mi = blockIdx.y;
   const int k_lo = a.chunks * split_k / a.S, k_hi = a.chunks * (split_k + 1) / a.S;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  auto all_sync = [] {
+    if constexpr (PAIR) cluster_sync();
+    else __syncthreads();
+  };
 
   if (threadIdx.x == 0) {
     tc::prefetch_map(&map_p);
@@ -378,19 +386,24 @@ __global__ void __launch_bounds__(kProductThreads, 1) __cluster_dims__(2, 1, 1)
       tc::mbar_init(&empty[i], 1);
     }
     tc::mbar_init(tfull, 1);
-    tc::mbar_init(tempty, 2 * kDrainWarps);
+    tc::mbar_init(tempty, kCtas * kDrainWarps);
     tc::mbar_init(done, 1);
     tc::fence_barrier_init();
   }
   if (warp == kDrainWarps + 1) {
-    asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(tc::smem_u32(tmem_slot)),
-                 "r"(512u)
-                 : "memory");
-    asm volatile("tcgen05.relinquish_alloc_permit.cta_group::2.sync.aligned;" ::: "memory");
+    if constexpr (PAIR) {
+      asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(tc::smem_u32(tmem_slot)),
+                   "r"(2u * kSide)
+                   : "memory");
+      asm volatile("tcgen05.relinquish_alloc_permit.cta_group::2.sync.aligned;" ::: "memory");
+    } else {
+      tc::tmem_alloc(tmem_slot, 2 * kSide);
+      tc::tmem_relinquish();
+    }
   }
   let_next_start();
   tc::fence_before_sync();
-  cluster_sync();
+  all_sync();
   tc::fence_after_sync();
   const uint32_t tmem = *tmem_slot;
   wait_previous();
@@ -400,8 +413,12 @@ __global__ void __launch_bounds__(kProductThreads, 1) __cluster_dims__(2, 1, 1)
       const int i = k - k_lo, st = i % kStages;
       if (i >= kStages && !tc::mbar_wait(&empty[st], ((i / kStages) & 1) ^ 1)) break;
       uint8_t* base = smem + st * kStageBytes;
-      const uint32_t bar = at_rank(tc::smem_u32(&full[st]), 0);
-      if (rank == 0) tc::mbar_arrive_expect_tx(&full[st], 2 * kStageBytes);
+      const uint32_t bar = PAIR ? at_rank(tc::smem_u32(&full[st]), 0) : 0;
+      if (rank == 0) tc::mbar_arrive_expect_tx(&full[st], kCtas * kStageBytes);
+      auto load = [&](uint8_t* dst, const CUtensorMap* map, int c0, int c1, int z) {
+        if constexpr (PAIR) pair_load_3d(dst, map, bar, c0, c1, z);
+        else tc::tma_load_3d(dst, map, &full[st], c0, c1, z);
+      };
 #pragma unroll
       for (int pl = 0; pl < 2; ++pl) {
         const int z = pl * s.nm + mi;
@@ -409,14 +426,22 @@ __global__ void __launch_bounds__(kProductThreads, 1) __cluster_dims__(2, 1, 1)
         uint8_t* qq = base + (2 + pl) * kOperand;
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
-          pair_load_3d(pp + h * (kOperand / 2), &map_p, bar, k * kBk, m0 + 64 * h, z);
-          if (kMn) pair_load_3d(qq + h * (kOperand / 2), &map_q, bar, qn + 64 * h, k * kBk, z);
-          else pair_load_3d(qq + h * (kOperand / 2), &map_q, bar, k * kBk, qn + 64 * h, z);
+          load(pp + h * (kOperand / 2), &map_p, k * kBk, m0 + 64 * h, z);
+          if (kMn) load(qq + h * (kOperand / 2), &map_q, qn + 64 * h, k * kBk, z);
+          else load(qq + h * (kOperand / 2), &map_q, k * kBk, qn + 64 * h, z);
         }
       }
     }
   } else if (warp == kDrainWarps + 1 && lane == 0 && rank == 0) {
-    constexpr uint32_t idesc = idesc_f16(kPairTile, kPairTile, kMn);
+    constexpr uint32_t idesc = idesc_f16(kSide, kSide, kMn);
+    auto mma = [&](uint32_t d, uint64_t x, uint64_t y, uint32_t more) {
+      if constexpr (PAIR) pair_mma(d, x, y, idesc, more);
+      else tc::mma_bf16(d, x, y, idesc, more);
+    };
+    auto commit = [](uint64_t* bar) {
+      if constexpr (PAIR) pair_commit(bar);
+      else tc::mma_commit(bar);
+    };
     for (int k = k_lo; k < k_hi; ++k) {
       const int i = k - k_lo, st = i % kStages;
       if (!tc::mbar_wait(&full[st], (i / kStages) & 1)) break;
@@ -429,38 +454,40 @@ __global__ void __launch_bounds__(kProductThreads, 1) __cluster_dims__(2, 1, 1)
                    : tc::desc_sw128(q0 + plane * kOperand + kk * 32, 16, 1024);
       };
 #pragma unroll
-      for (int kk = 0; kk < kBk / 16; ++kk) pair_mma(tmem, pd(0, kk), qd(0, kk), idesc, kk != 0);
-      pair_commit(tfull);
+      for (int kk = 0; kk < kBk / 16; ++kk) mma(tmem, pd(0, kk), qd(0, kk), kk != 0);
+      commit(tfull);
 #pragma unroll
       for (int kk = 0; kk < kBk / 16; ++kk) {
-        pair_mma(tmem + kPairTile, pd(0, kk), qd(1, kk), idesc, (i | kk) != 0);
-        pair_mma(tmem + kPairTile, pd(1, kk), qd(0, kk), idesc, 1);
+        mma(tmem + kSide, pd(0, kk), qd(1, kk), (i | kk) != 0);
+        mma(tmem + kSide, pd(1, kk), qd(0, kk), 1);
       }
-      pair_commit(&empty[st]);
+      commit(&empty[st]);
     }
-    pair_commit(done);
+    commit(done);
   }
   __syncwarp();
   if (warp < kDrainWarps) {
-    const int quarter = (warp & 3) * 32, c0 = (warp >> 2) * 64;
-    const int row = m0 + quarter + lane;
+    const int quarter = (warp & 3) * 32, c0 = (warp >> 2) * kCols;
     const uint32_t tw = tmem + ((uint32_t)quarter << 16) + c0;
-    const uint32_t release = at_rank(tc::smem_u32(tempty), 0);
-    float acc[64];
+    const uint32_t release = PAIR ? at_rank(tc::smem_u32(tempty), 0) : 0;
+    float acc[kCols];
 #pragma unroll
-    for (int i = 0; i < 64; ++i) acc[i] = 0.0f;
+    for (int i = 0; i < kCols; ++i) acc[i] = 0.0f;
     bool ok = true;
     for (int i = 0; i < k_hi - k_lo && ok; ++i) {
       ok = tc::mbar_wait(tfull, i & 1);
       tc::fence_after_sync();
 #pragma unroll
-      for (int h = 0; h < 64; h += 32) {
+      for (int h = 0; h < kCols; h += 32) {
         uint32_t v[32];
         tc::tmem_ld_chunks<2>(tw + h, v);
-        if (h == 32) {
+        if (h + 32 == kCols) {
           tc::fence_before_sync();
           __syncwarp();
-          if (lane == 0) arrive_remote(release);
+          if (lane == 0) {
+            if constexpr (PAIR) arrive_remote(release);
+            else tc::mbar_arrive(tempty);
+          }
         }
 #pragma unroll
         for (int c = 0; c < 32; ++c) acc[h + c] += __uint_as_float(v[c]);
@@ -468,75 +495,69 @@ __global__ void __launch_bounds__(kProductThreads, 1) __cluster_dims__(2, 1, 1)
     }
     ok = ok && tc::mbar_wait(done, 0);
     tc::fence_after_sync();
-    // The tile goes through the operand buffers, which are free: 128 rows of 256 fp32 values, the
+    // The tile goes through the operand buffers, which are free: 128 rows of kSide fp32 values, the
     // 16-byte blocks of a row exchanged by the row's last bits.  What is made of it then runs in
-    // short loops: unrolled over a thread's 64 registers the code came cold from L2 and cost 8 us.
-    {
-      uint8_t* to = smem + (row - m0) * 1024;
-      const uint32_t turn = ((uint32_t)row & 7u) << 4;
+    // short loops: unrolled over a thread's registers the code came cold from L2 and cost 8 us.
+    constexpr uint32_t kRowBytes = kSide * 4;
+    auto block_of = [&](int r, int block) {
+      return reinterpret_cast<float4*>(smem + r * kRowBytes + (((uint32_t)block ^ ((uint32_t)r & 7u)) << 4));
+    };
 #pragma unroll
-      for (int c = 0; c < 64; c += 16) {
-        float v[16];
-        tc::tmem_ld16(tw + kPairTile + c, v);
+    for (int c = 0; c < kCols; c += 16) {
+      float v[16];
+      tc::tmem_ld16(tw + kSide + c, v);
 #pragma unroll
-        for (int i = 0; i < 16; i += 4)
-          *reinterpret_cast<float4*>(to + (((uint32_t)(c0 + c + i) * 4) ^ turn)) =
-              make_float4(fmaf(v[i], 1.0f / kSl, acc[c + i]), fmaf(v[i + 1], 1.0f / kSl, acc[c + i + 1]),
-                          fmaf(v[i + 2], 1.0f / kSl, acc[c + i + 2]), fmaf(v[i + 3], 1.0f / kSl, acc[c + i + 3]));
-      }
+      for (int i = 0; i < 16; i += 4)
+        *block_of(quarter + lane, (c0 + c + i) / 4) =
+            make_float4(fmaf(v[i], 1.0f / kSl, acc[c + i]), fmaf(v[i + 1], 1.0f / kSl, acc[c + i + 1]),
+                        fmaf(v[i + 2], 1.0f / kSl, acc[c + i + 2]), fmaf(v[i + 3], 1.0f / kSl, acc[c + i + 3]));
     }
     tc::named_bar_sync(1, kDrainWarps * 32);
     const size_t pa = (size_t)s.nm * s.Rp * s.Rp, px = (size_t)s.nm * s.Rp * s.Lp;
     const size_t tensor = (size_t)(mi % s.groups) * s.rows * s.cols;
-    if (ok && !(MODE == kFinal && s.tr)) {
-      if (MODE == kSymmetric && a.S > 1) {
+    if (ok && MODE == kSymmetric && a.S > 1) {
 #pragma unroll 2
-        for (int r = warp; r < kTile; r += kDrainWarps) {  // a warp takes a row, a lane 4 columns and 4 more
-          const uint8_t* from = smem + r * 1024;
-          float* dst = a.part + (size_t)split_k * pa + ((size_t)mi * s.Rp + m0 + r) * s.Rp + n0 + lane * 4;
+      for (int r = warp; r < kTile; r += kDrainWarps) {  // a warp takes a row, a lane 4 columns of each 128
+        float* dst = a.part + (size_t)split_k * pa + ((size_t)mi * s.Rp + m0 + r) * s.Rp + n0 + lane * 4;
 #pragma unroll
-          for (int h = 0; h < 2; ++h)
-            *reinterpret_cast<float4*>(dst + 128 * h) =
-                *reinterpret_cast<const float4*>(from + ((uint32_t)((lane + 32 * h) ^ (r & 7)) << 4));
-        }
-      } else {
+        for (int h = 0; h < kCtas; ++h) *reinterpret_cast<float4*>(dst + 128 * h) = *block_of(r, lane + 32 * h);
+      }
+    } else if (ok && !(MODE == kFinal && s.tr)) {
+      constexpr int kLanes = kSide / 8;  // lanes of a row, 8 columns each
+      const int lr = lane % kLanes;
 #pragma unroll 2
-        for (int r = warp; r < kTile; r += kDrainWarps) {  // a warp takes a row, a lane 8 columns
-          uint8_t* from = smem + r * 1024;
-          const uint32_t turn = (uint32_t)r & 7u;
-          float4* px0 = reinterpret_cast<float4*>(from + (((2u * lane) ^ turn) << 4));
-          float4* px1 = reinterpret_cast<float4*>(from + (((2u * lane + 1u) ^ turn) << 4));
-          float v[8] = {px0->x, px0->y, px0->z, px0->w, px1->x, px1->y, px1->z, px1->w};
-          const int grow = m0 + r, col = n0 + lane * 8;
-          if constexpr (MODE == kSymmetric) {
-            const size_t at = ((size_t)mi * s.Rp + grow) * s.Rp + col;
-            become(a.f, pa, at, grow - col, v);
-            uint4 hi, lo;
-            split8(v, hi, lo);
-            *reinterpret_cast<uint4*>(a.dst + at) = hi;
-            *reinterpret_cast<uint4*>(a.dst + pa + at) = lo;
-            if (bm != bn) {  // for the mirror image
-              *px0 = make_float4(v[0], v[1], v[2], v[3]);
-              *px1 = make_float4(v[4], v[5], v[6], v[7]);
-            }
-          } else if constexpr (MODE == kUpdate) {
-            const size_t at = ((size_t)mi * s.Rp + grow) * s.Lp + col;
+      for (int r = warp * (32 / kLanes) + lane / kLanes; r < kTile; r += kDrainWarps * (32 / kLanes)) {
+        float4 *b0 = block_of(r, 2 * lr), *b1 = block_of(r, 2 * lr + 1);
+        float v[8] = {b0->x, b0->y, b0->z, b0->w, b1->x, b1->y, b1->z, b1->w};
+        const int row = m0 + r, col = n0 + lr * 8;
+        if constexpr (MODE == kSymmetric) {
+          const size_t at = ((size_t)mi * s.Rp + row) * s.Rp + col;
+          become(a.f, pa, at, row - col, v);
+          uint4 hi, lo;
+          split8(v, hi, lo);
+          *reinterpret_cast<uint4*>(a.dst + at) = hi;
+          *reinterpret_cast<uint4*>(a.dst + pa + at) = lo;
+          if (bm != bn) {  // for the mirror image
+            *b0 = make_float4(v[0], v[1], v[2], v[3]);
+            *b1 = make_float4(v[4], v[5], v[6], v[7]);
+          }
+        } else if constexpr (MODE == kUpdate) {
+          const size_t at = ((size_t)mi * s.Rp + row) * s.Lp + col;
 #pragma unroll
-            for (int i = 0; i < 8; ++i) v[i] *= 1.0f / kSb;
-            uint4 hi, lo;
-            split8(v, hi, lo);
-            *reinterpret_cast<uint4*>(a.dst + at) = hi;
-            *reinterpret_cast<uint4*>(a.dst + px + at) = lo;
-          } else {
-            const int here = grow < s.R ? max(0, min(8, s.L - col)) : 0;
-            if (here > 0) {
-              const size_t at = tensor + (size_t)grow * s.cols + col;
-              float w[8] = {};
-              if (a.r.step) load_wide(static_cast<const T*>(ptr.w[mi / s.groups]) + at, here, w);
+          for (int i = 0; i < 8; ++i) v[i] *= 1.0f / kSb;
+          uint4 hi, lo;
+          split8(v, hi, lo);
+          *reinterpret_cast<uint4*>(a.dst + at) = hi;
+          *reinterpret_cast<uint4*>(a.dst + px + at) = lo;
+        } else {
+          const int here = row < s.R ? max(0, min(8, s.L - col)) : 0;
+          if (here > 0) {
+            const size_t at = tensor + (size_t)row * s.cols + col;
+            float w[8] = {};
+            if (a.r.step) load_wide(static_cast<const T*>(ptr.w[mi / s.groups]) + at, here, w);
 #pragma unroll
-              for (int i = 0; i < 8; ++i) v[i] = result_of(a.r, w[i], v[i] * (1.0f / (kSb * kSx)));
-              store_wide(static_cast<T*>(ptr.out[mi / s.groups]) + at, here, v);
-            }
+            for (int i = 0; i < 8; ++i) v[i] = result_of(a.r, w[i], v[i] * (1.0f / (kSb * kSx)));
+            store_wide(static_cast<T*>(ptr.out[mi / s.groups]) + at, here, v);
           }
         }
       }
@@ -544,18 +565,18 @@ __global__ void __launch_bounds__(kProductThreads, 1) __cluster_dims__(2, 1, 1)
     if ((MODE == kSymmetric && a.S == 1 && bm != bn) || (MODE == kFinal && s.tr)) {
       tc::named_bar_sync(1, kDrainWarps * 32);
 #pragma unroll 1
-      for (int k = warp; k < kPairTile * 4 && ok; k += kDrainWarps) {  // a warp takes 32 rows of a column
+      for (int k = warp; k < kSide * 4 && ok; k += kDrainWarps) {  // a warp takes 32 rows of a column
         const int c = k / 4, r = k % 4 * 32 + lane;
-        float v = *reinterpret_cast<const float*>(smem + r * 1024 + (((uint32_t)c * 4) ^ (((uint32_t)r & 7u) << 4)));
-        const int grow = m0 + r, col = n0 + c;
+        const float v = reinterpret_cast<const float*>(block_of(r, c / 4))[c % 4];
+        const int row = m0 + r, col = n0 + c;
         if constexpr (MODE == kSymmetric) {
-          const size_t at = ((size_t)mi * s.Rp + col) * s.Rp + grow;
+          const size_t at = ((size_t)mi * s.Rp + col) * s.Rp + row;
           __half h, l;
           split(v, h, l);
           a.dst[at] = h;
           a.dst[pa + at] = l;
-        } else if (grow < s.R && col < s.L) {
-          const size_t at = tensor + (size_t)col * s.cols + grow;
+        } else if (row < s.R && col < s.L) {
+          const size_t at = tensor + (size_t)col * s.cols + row;
           const float w = a.r.step ? to_f32(static_cast<const T*>(ptr.w[mi / s.groups])[at]) : 0.0f;
           static_cast<T*>(ptr.out[mi / s.groups])[at] = from_f32<T>(result_of(a.r, w, v * (1.0f / (kSb * kSx))));
         }
@@ -564,13 +585,16 @@ __global__ void __launch_bounds__(kProductThreads, 1) __cluster_dims__(2, 1, 1)
     tc::fence_before_sync();
   }
   // neither CTA leaves before the other's last arrival and MMA
-  cluster_sync();
-  if (warp == kDrainWarps + 1)
-    asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(512u) : "memory");
+  all_sync();
+  if (warp == kDrainWarps + 1) {
+    if constexpr (PAIR)
+      asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(2u * kSide) : "memory");
+    else tc::tmem_dealloc(tmem, 2 * kSide);
+  }
 }
 
 // The next operand from the partial products of a symmetric product split along K, added in a fixed
-// order.  They hold the 256-wide tiles on and above the diagonal: a CTA adds a 64 x 64 tile there and
+// order.  They hold the tiles on and above the diagonal: a CTA adds a 64 x 64 tile there and
 // writes it and its mirror image.
 __global__ void __launch_bounds__(256) ns_reduce_kernel(const float* __restrict__ part, Shape s, int S, Becomes f,
                                                         __half* __restrict__ dst) {
@@ -1059,36 +1083,41 @@ Shape shape_of(int n, int groups, int rows, int cols) {
   s.tr = rows > cols;
   s.R = std::min(rows, cols);
   s.L = std::max(rows, cols);
-  s.Rp = up(s.R, kPairTile);
-  s.Lp = up(s.L, kPairTile);
   s.nm = n * groups;
+  // pairs of CTAs where there is a tile for nearly every one of them
+  s.tile = (long long)s.nm * up(s.R, 256) * up(s.L, 256) / (256 * 256) >= 64 ? 256 : 128;
+  s.Rp = up(s.R, s.tile);
+  s.Lp = up(s.L, s.tile);
   return s;
 }
 
-// Splits of the K range of a symmetric product: as many as give every two SMs a pair of CTAs, each
-// of 256 values at least, unless the second kernel that they need (7 us) costs more than the
-// chunks (1.3 us) that they save.
+// Splits of the K range of a symmetric product: as many as give every SM work, each of 256 values at
+// least, unless the second kernel that they need (7 us) costs more than the chunks (1.0 us on a
+// pair, 0.5 us on one CTA) that they save.
 int splits_of(const Shape& s, int k, int sms) {
-  const int nt = s.Rp / kPairTile, chunks = k / kBk;
+  const int nt = s.Rp / s.tile, chunks = k / kBk, ctas = s.tile / kTile;
   const long long tiles = (long long)nt * (nt + 1) / 2 * s.nm;
-  const int room = (int)std::max<long long>(1, sms / 2 / tiles);
+  const int room = (int)std::max<long long>(1, sms / ctas / tiles);
   const int S = std::max(1, std::min({room, chunks / 4, kMaxSplits}));
-  return (chunks - chunks / S) * 13 < 70 ? 1 : S;
+  return (chunks - chunks / S) * ctas < 14 ? 1 : S;
 }
 
 // The next kernel of a chain, brought up while the one before it runs.
 template <typename K, typename... A>
-cudaError_t chain(K k, dim3 grid, int threads, size_t smem, cudaStream_t st, A... args) {
+cudaError_t chain(K k, dim3 grid, int cluster, int threads, size_t smem, cudaStream_t st, A... args) {
   cudaLaunchConfig_t cfg{};
   cfg.gridDim = grid;
   cfg.blockDim = dim3(threads);
   cfg.dynamicSmemBytes = smem;
   cfg.stream = st;
-  cudaLaunchAttribute attr[1];
+  cudaLaunchAttribute attr[2];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr[0].val.programmaticStreamSerializationAllowed = 1;
+  attr[1].id = cudaLaunchAttributeClusterDimension;
+  attr[1].val.clusterDim.x = (unsigned)cluster;
+  attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
   cfg.attrs = attr;
-  cfg.numAttrs = 1;
+  cfg.numAttrs = cluster > 1 ? 2 : 1;
   cudaError_t e = cudaLaunchKernelEx(&cfg, k, args...);
   count_launch();
   return e != cudaSuccess ? e : cudaGetLastError();
@@ -1135,14 +1164,20 @@ bool plane_map(CUtensorMap* m, const void* base, int cols, int rows, int z) {
 
 constexpr size_t kProductSmem = kStages * kStageBytes + 1024 + 128;
 
+template <typename T, Product MODE, bool PAIR>
+cudaError_t product_on(const CUtensorMap& p, const CUtensorMap& q, const Pointers& ptr, const ProductArgs& a,
+                       cudaStream_t st) {
+  auto k = ns_product_kernel<T, MODE, PAIR>;
+  cudaError_t e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kProductSmem);
+  if (e != cudaSuccess) return e;
+  const int tiles = MODE == kSymmetric ? a.tn * (a.tn + 1) / 2 : a.tm * a.tn, ctas = PAIR ? 2 : 1;
+  return chain(k, dim3(ctas * tiles * a.S, a.s.nm), ctas, kProductThreads, kProductSmem, st, p, q, ptr, a);
+}
+
 template <typename T, Product MODE>
 cudaError_t product(const CUtensorMap& p, const CUtensorMap& q, const Pointers& ptr, const ProductArgs& a,
                     cudaStream_t st) {
-  auto k = ns_product_kernel<T, MODE>;
-  cudaError_t e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kProductSmem);
-  if (e != cudaSuccess) return e;
-  const int tiles = MODE == kSymmetric ? a.tn * (a.tn + 1) / 2 : a.tm * a.tn;
-  return chain(k, dim3(2 * tiles * a.S, a.s.nm), kProductThreads, kProductSmem, st, p, q, ptr, a);
+  return a.s.tile == 256 ? product_on<T, MODE, true>(p, q, ptr, a, st) : product_on<T, MODE, false>(p, q, ptr, a, st);
 }
 
 struct SmallPlan {
@@ -1236,7 +1271,7 @@ cudaError_t run_chunk(const MuonArgs& a, int t0, int n, char* ws, int sms, cudaS
   ns_norm_kernel<T><<<dim3(blocks, s.nm), 256, 0, st>>>(ptr, s, r, norm);
   count_launch();
   if ((e = cudaGetLastError()) != cudaSuccess) return e;
-  if ((e = chain(ns_load_kernel<T>, dim3(s.Lp / 64, s.Rp / 64, s.nm), 256, 0, st, ptr, s, r, a.eps,
+  if ((e = chain(ns_load_kernel<T>, dim3(s.Lp / 64, s.Rp / 64, s.nm), 1, 256, 0, st, ptr, s, r, a.eps,
                  (const double*)norm, blocks, x[0])) != cudaSuccess)
     return e;
   ProductArgs g{};
@@ -1247,13 +1282,13 @@ cudaError_t run_chunk(const MuonArgs& a, int t0, int n, char* ws, int sms, cudaS
   const dim3 red(nt * (nt + 1) / 2, s.nm);
   // P P^T into dst, as `f` says
   auto square = [&](const CUtensorMap& p, int k, const Becomes& f, __half* dst) {
-    g.tm = g.tn = s.Rp / kPairTile;
+    g.tm = g.tn = s.Rp / s.tile;
     g.chunks = k / kBk;
     g.S = splits_of(s, k, sms);
     g.f = f;
     g.dst = dst;
     cudaError_t err = product<T, kSymmetric>(p, p, ptr, g, st);
-    if (err == cudaSuccess && g.S > 1) err = chain(ns_reduce_kernel, red, 256, 0, st, (const float*)part, s, g.S, f, dst);
+    if (err == cudaSuccess && g.S > 1) err = chain(ns_reduce_kernel, red, 1, 256, 0, st, (const float*)part, s, g.S, f, dst);
     return err;
   };
   for (int k = 0; k < a.steps; ++k) {
@@ -1262,7 +1297,7 @@ cudaError_t run_chunk(const MuonArgs& a, int t0, int n, char* ws, int sms, cudaS
     if ((e = square(ma, s.Rp, Becomes{a.a, a.b, a.c, am}, bm)) != cudaSuccess) return e;
     g.S = 1;
     g.chunks = s.Rp / kBk;
-    g.tn = s.Lp / kPairTile;
+    g.tn = s.Lp / s.tile;
     g.dst = x[now ^ 1];
     e = k + 1 < a.steps ? product<T, kUpdate>(mb, mx[now], ptr, g, st) : product<T, kFinal>(mb, mx[now], ptr, g, st);
     if (e != cudaSuccess) return e;
