@@ -229,6 +229,7 @@ struct Becomes {
 struct ProductArgs {
   Shape s;
   int tm, tn, S, chunks;  // tiles along M and N, splits along K, K chunks in all
+  bool upper;             // P is kept on and above the diagonal only
   float* part;            // kSymmetric, S > 1: [S][nm][Rp][Rp]
   Becomes f;              // kSymmetric, S = 1: what the product becomes, into dst
   __half* dst;            // kUpdate: the next X
@@ -239,9 +240,10 @@ __device__ __forceinline__ uint8_t* align1024(uint8_t* p) {
   return reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(p) + 1023) & ~uintptr_t(1023));
 }
 
-// Instruction descriptor: fp16 x fp16 -> fp32, M x N, A K-major.
-__host__ __device__ constexpr uint32_t idesc_f16(int M, int N, bool b_mn_major) {
-  return (1u << 4) | ((b_mn_major ? 1u : 0u) << 16) | ((uint32_t)(N >> 3) << 17) | ((uint32_t)(M >> 4) << 24);
+// Instruction descriptor: fp16 x fp16 -> fp32, M x N, A and B major modes.
+__host__ __device__ constexpr uint32_t idesc_f16(int M, int N, bool a_mn_major, bool b_mn_major) {
+  return (1u << 4) | ((a_mn_major ? 1u : 0u) << 15) | ((b_mn_major ? 1u : 0u) << 16) | ((uint32_t)(N >> 3) << 17) |
+         ((uint32_t)(M >> 4) << 24);
 }
 
 // 8 values as 16 bytes of hi and of lo.
@@ -287,8 +289,11 @@ __device__ __forceinline__ void become(const Becomes& f, size_t plane, size_t at
     v[i] = fmaf(f.c * (kSb / (kSa * kSa)), v[i], fmaf(f.b * (kSb / kSa), x[i], i == diag ? f.a * kSb : 0.0f));
 }
 
-// One tile of a product of hi + lo matrices: D = P P^T (kSymmetric, both operands K-major, tiles on
-// and above the diagonal only) or D = P Q (kUpdate, kFinal; Q is read as an MN-major operand).
+// One tile of a product of hi + lo matrices: D = P P^T (kSymmetric, tiles on and above the diagonal
+// only) or D = P Q (kUpdate, kFinal; Q is read as an MN-major operand).  P is X, or one of the
+// symmetric matrices A and B, of which only the tiles on and above the diagonal are kept (`upper`): a
+// chunk below it is loaded from its mirror image and read as an MN-major operand (writing the mirror
+// images instead cost 3 to 5 us a product).
 //
 // PAIR: two CTAs (cta_group::2) make a 256 x 256 tile.  Each brings 128 rows of P and 128 columns of Q
 // and gets 128 rows of D, so that 64 KB from L2 feed 1536 cycles of MMA; one CTA with a 128 x 128 tile
@@ -373,6 +378,9 @@ __global__ void __launch_bounds__(kProductThreads, 1)
   const int mi = blockIdx.y;
   const int k_lo = a.chunks * split_k / a.S, k_hi = a.chunks * (split_k + 1) / a.S;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  // whether a chunk of P (of Q) comes as the mirror image, and is then MN-major like Q of an update
+  auto p_mn = [&](int k) { return a.upper && k * kBk / kSide < bm; };
+  auto q_mn = [&](int k) { return kMn || (a.upper && k * kBk / kSide < bn); };
   auto all_sync = [] {
     if constexpr (PAIR) cluster_sync();
     else __syncthreads();
@@ -426,18 +434,14 @@ __global__ void __launch_bounds__(kProductThreads, 1)
         uint8_t* qq = base + (2 + pl) * kOperand;
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
-          load(pp + h * (kOperand / 2), &map_p, k * kBk, m0 + 64 * h, z);
-          if (kMn) load(qq + h * (kOperand / 2), &map_q, qn + 64 * h, k * kBk, z);
+          if (p_mn(k)) load(pp + h * (kOperand / 2), &map_p, m0 + 64 * h, k * kBk, z);
+          else load(pp + h * (kOperand / 2), &map_p, k * kBk, m0 + 64 * h, z);
+          if (q_mn(k)) load(qq + h * (kOperand / 2), &map_q, qn + 64 * h, k * kBk, z);
           else load(qq + h * (kOperand / 2), &map_q, k * kBk, qn + 64 * h, z);
         }
       }
     }
   } else if (warp == kDrainWarps + 1 && lane == 0 && rank == 0) {
-    constexpr uint32_t idesc = idesc_f16(kSide, kSide, kMn);
-    auto mma = [&](uint32_t d, uint64_t x, uint64_t y, uint32_t more) {
-      if constexpr (PAIR) pair_mma(d, x, y, idesc, more);
-      else tc::mma_bf16(d, x, y, idesc, more);
-    };
     auto commit = [](uint64_t* bar) {
       if constexpr (PAIR) pair_commit(bar);
       else tc::mma_commit(bar);
@@ -448,18 +452,23 @@ __global__ void __launch_bounds__(kProductThreads, 1)
       if (i > 0 && !tc::mbar_wait(tempty, (i & 1) ^ 1)) break;
       tc::fence_after_sync();
       const uint32_t p0 = tc::smem_u32(smem + st * kStageBytes), q0 = p0 + 2 * kOperand;
-      auto pd = [&](int plane, int kk) { return tc::desc_sw128(p0 + plane * kOperand + kk * 32, 16, 1024); };
-      auto qd = [&](int plane, int kk) {
-        return kMn ? tc::desc_sw128(q0 + plane * kOperand + kk * 2048, kOperand / 2, 1024)
-                   : tc::desc_sw128(q0 + plane * kOperand + kk * 32, 16, 1024);
+      const bool pm = p_mn(k), qm = q_mn(k);
+      const uint32_t idesc = idesc_f16(kSide, kSide, pm, qm);
+      auto operand = [](uint32_t base, bool mn, int kk) {
+        return mn ? tc::desc_sw128(base + kk * 2048, kOperand / 2, 1024) : tc::desc_sw128(base + kk * 32, 16, 1024);
+      };
+      auto mma = [&](uint32_t d, int p_plane, int q_plane, int kk, uint32_t more) {
+        const uint64_t x = operand(p0 + p_plane * kOperand, pm, kk), y = operand(q0 + q_plane * kOperand, qm, kk);
+        if constexpr (PAIR) pair_mma(d, x, y, idesc, more);
+        else tc::mma_bf16(d, x, y, idesc, more);
       };
 #pragma unroll
-      for (int kk = 0; kk < kBk / 16; ++kk) mma(tmem, pd(0, kk), qd(0, kk), kk != 0);
+      for (int kk = 0; kk < kBk / 16; ++kk) mma(tmem, 0, 0, kk, kk != 0);
       commit(tfull);
 #pragma unroll
       for (int kk = 0; kk < kBk / 16; ++kk) {
-        mma(tmem + kSide, pd(0, kk), qd(1, kk), (i | kk) != 0);
-        mma(tmem + kSide, pd(1, kk), qd(0, kk), 1);
+        mma(tmem + kSide, 0, 1, kk, (i | kk) != 0);
+        mma(tmem + kSide, 1, 0, kk, 1);
       }
       commit(&empty[st]);
     }
@@ -527,7 +536,7 @@ __global__ void __launch_bounds__(kProductThreads, 1)
       const int lr = lane % kLanes;
 #pragma unroll 2
       for (int r = warp * (32 / kLanes) + lane / kLanes; r < kTile; r += kDrainWarps * (32 / kLanes)) {
-        float4 *b0 = block_of(r, 2 * lr), *b1 = block_of(r, 2 * lr + 1);
+        const float4 *b0 = block_of(r, 2 * lr), *b1 = block_of(r, 2 * lr + 1);
         float v[8] = {b0->x, b0->y, b0->z, b0->w, b1->x, b1->y, b1->z, b1->w};
         const int row = m0 + r, col = n0 + lr * 8;
         if constexpr (MODE == kSymmetric) {
@@ -537,10 +546,6 @@ __global__ void __launch_bounds__(kProductThreads, 1)
           split8(v, hi, lo);
           *reinterpret_cast<uint4*>(a.dst + at) = hi;
           *reinterpret_cast<uint4*>(a.dst + pa + at) = lo;
-          if (bm != bn) {  // for the mirror image
-            *b0 = make_float4(v[0], v[1], v[2], v[3]);
-            *b1 = make_float4(v[4], v[5], v[6], v[7]);
-          }
         } else if constexpr (MODE == kUpdate) {
           const size_t at = ((size_t)mi * s.Rp + row) * s.Lp + col;
 #pragma unroll
@@ -562,20 +567,13 @@ __global__ void __launch_bounds__(kProductThreads, 1)
         }
       }
     }
-    if ((MODE == kSymmetric && a.S == 1 && bm != bn) || (MODE == kFinal && s.tr)) {
-      tc::named_bar_sync(1, kDrainWarps * 32);
-#pragma unroll 1
+    if (MODE == kFinal && s.tr) {
+#pragma unroll 2
       for (int k = warp; k < kSide * 4 && ok; k += kDrainWarps) {  // a warp takes 32 rows of a column
         const int c = k / 4, r = k % 4 * 32 + lane;
         const float v = reinterpret_cast<const float*>(block_of(r, c / 4))[c % 4];
         const int row = m0 + r, col = n0 + c;
-        if constexpr (MODE == kSymmetric) {
-          const size_t at = ((size_t)mi * s.Rp + col) * s.Rp + row;
-          __half h, l;
-          split(v, h, l);
-          a.dst[at] = h;
-          a.dst[pa + at] = l;
-        } else if (row < s.R && col < s.L) {
+        if (row < s.R && col < s.L) {
           const size_t at = tensor + (size_t)col * s.cols + row;
           const float w = a.r.step ? to_f32(static_cast<const T*>(ptr.w[mi / s.groups])[at]) : 0.0f;
           static_cast<T*>(ptr.out[mi / s.groups])[at] = from_f32<T>(result_of(a.r, w, v * (1.0f / (kSb * kSx))));
@@ -594,17 +592,13 @@ __global__ void __launch_bounds__(kProductThreads, 1)
 }
 
 // The next operand from the partial products of a symmetric product split along K, added in a fixed
-// order.  They hold the tiles on and above the diagonal: a CTA adds a 64 x 64 tile there and
-// writes it and its mirror image.
+// order: 64 x 64 entries a CTA, those of the tiles on and above the diagonal.
 __global__ void __launch_bounds__(256) ns_reduce_kernel(const float* __restrict__ part, Shape s, int S, Becomes f,
                                                         __half* __restrict__ dst) {
-  __shared__ float tile[64][65];
   let_next_start();
   wait_previous();
-  const int nt = s.Rp / 64, mi = blockIdx.y;
-  int bj = blockIdx.x, bi = 0;
-  while (bj >= nt - bi) bj -= nt - bi++;
-  bj += bi;
+  const int mi = blockIdx.z, bi = blockIdx.y, bj = blockIdx.x;
+  if (bi * 64 / s.tile > bj * 64 / s.tile) return;
   const size_t plane = (size_t)s.nm * s.Rp * s.Rp, base = (size_t)mi * s.Rp * s.Rp;
   const int x = threadIdx.x % 8 * 8, y = threadIdx.x / 8;
 #pragma unroll
@@ -628,21 +622,6 @@ __global__ void __launch_bounds__(256) ns_reduce_kernel(const float* __restrict_
     split8(v, hi, lo);
     *reinterpret_cast<uint4*>(dst + at) = hi;
     *reinterpret_cast<uint4*>(dst + plane + at) = lo;
-#pragma unroll
-    for (int e = 0; e < 8; ++e) tile[r][x + e] = v[e];
-  }
-  if (bi == bj) return;
-  __syncthreads();
-#pragma unroll
-  for (int r = y; r < 64; r += 32) {
-    float v[8];
-#pragma unroll
-    for (int e = 0; e < 8; ++e) v[e] = tile[x + e][r];
-    const size_t mirror = base + (size_t)(bj * 64 + r) * s.Rp + bi * 64 + x;
-    uint4 hi, lo;
-    split8(v, hi, lo);
-    *reinterpret_cast<uint4*>(dst + mirror) = hi;
-    *reinterpret_cast<uint4*>(dst + plane + mirror) = lo;
   }
 }
 
@@ -900,7 +879,7 @@ __global__ void __launch_bounds__(kSmallThreads, 1)
   };
   // P P^T of hi and lo planes with K-major chunks, K = 16 * steps
   auto square = [&](uint32_t ph, uint32_t pl, int steps) {
-    constexpr uint32_t idesc = idesc_f16(128, RP, false);
+    constexpr uint32_t idesc = idesc_f16(128, RP, false, false);
     for (int k = 0; k < steps; ++k) {
       const uint32_t off = (uint32_t)(k >> 2) * kChunk + (k & 3) * 32;
       const uint64_t h = tc::desc_sw128(ph + off, 16, 1024);
@@ -1016,7 +995,7 @@ __global__ void __launch_bounds__(kSmallThreads, 1)
     for (int g0 = 0; g0 < mine; g0 += 4) {  // up to 256 columns at a time
       const int cols = min(4, mine - g0) * 64;
       if (t == 0) {
-        const uint32_t idesc = idesc_f16(128, cols, true);
+        const uint32_t idesc = idesc_f16(128, cols, false, true);
         for (int k = 0; k < RP / 16; ++k) {
           const uint32_t poff = (uint32_t)(k >> 2) * kChunk + (k & 3) * 32, qoff = (uint32_t)g0 * kChunk + k * 2048;
           const uint64_t bh = tc::desc_sw128(sah + poff, 16, 1024);
@@ -1278,10 +1257,10 @@ cudaError_t run_chunk(const MuonArgs& a, int t0, int n, char* ws, int sms, cudaS
   g.s = s;
   g.r = r;
   g.part = part;
-  const int nt = s.Rp / 64;
-  const dim3 red(nt * (nt + 1) / 2, s.nm);
+  const dim3 red(s.Rp / 64, s.Rp / 64, s.nm);
   // P P^T into dst, as `f` says
   auto square = [&](const CUtensorMap& p, int k, const Becomes& f, __half* dst) {
+    g.upper = f.am != nullptr;
     g.tm = g.tn = s.Rp / s.tile;
     g.chunks = k / kBk;
     g.S = splits_of(s, k, sms);
@@ -1296,6 +1275,7 @@ cudaError_t run_chunk(const MuonArgs& a, int t0, int n, char* ws, int sms, cudaS
     if ((e = square(mx[now], s.Lp, Becomes{a.a, a.b, a.c, nullptr}, am)) != cudaSuccess) return e;
     if ((e = square(ma, s.Rp, Becomes{a.a, a.b, a.c, am}, bm)) != cudaSuccess) return e;
     g.S = 1;
+    g.upper = true;
     g.chunks = s.Rp / kBk;
     g.tn = s.Lp / s.tile;
     g.dst = x[now ^ 1];
