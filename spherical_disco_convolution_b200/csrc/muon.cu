@@ -12,7 +12,8 @@
 // lo lo, is below 2^-22.  The two small products go into an accumulator of their own.  The tensor
 // core cuts what it adds to an accumulator instead of rounding it (chains of 512 values left a
 // 1024 x 9216 result 3.5e-5 off, 8 times fp32's error), so the large product is taken out and
-// added in registers every 64 values (192 in the one-launch form).  Scales: X by 2^12, A by 2^11, B by 2^9, so
+// added in registers every 64 values (the one-launch form spreads
+// it over three or four accumulators, 192 values in a chain at most).  Scales: X by 2^12, A by 2^11, B by 2^9, so
 // that |X| <= 16, |A| <= 32, |B| <= 128 stay finite in fp16; lo by 2^11 more, which puts it at hi's
 // size, so that it keeps its bits for entries far below the largest.
 #include <cuda.h>
@@ -877,24 +878,43 @@ __global__ void __launch_bounds__(kSmallThreads, 1)
     __syncthreads();
     tc::fence_after_sync();
   };
-  // P P^T of hi and lo planes with K-major chunks, K = 16 * steps
-  auto square = [&](uint32_t ph, uint32_t pl, int steps) {
+  // P P^T of hi and lo planes with K-major chunks, K = 64 * chunks.  The large products of the chunks
+  // go round kSums accumulators, which keeps the chains short that the tensor core cuts.
+  constexpr int kSums = RP == 64 ? 4 : 3;
+  auto sum_at = [](int j) -> uint32_t { return RP == 64 ? 256 + 64 * j : j < 2 ? 256 + 128 * j : 0; };
+  auto square = [&](uint32_t ph, uint32_t pl, int chunks) {
     constexpr uint32_t idesc = idesc_f16(128, RP, false, false);
-    for (int k = 0; k < steps; ++k) {
+    for (int k = 0; k < 4 * chunks; ++k) {
       const uint32_t off = (uint32_t)(k >> 2) * kChunk + (k & 3) * 32;
       const uint64_t h = tc::desc_sw128(ph + off, 16, 1024);
-      tc::mma_bf16(tmem, h, h, idesc, k != 0);
+      tc::mma_bf16(tmem + sum_at((k >> 2) % kSums), h, h, idesc, k >= 4 * kSums || (k & 3) != 0);
       const uint64_t l = tc::desc_sw128(pl + off, 16, 1024);
       tc::mma_bf16(tmem + 128, h, l, idesc, k != 0);
       tc::mma_bf16(tmem + 128, l, h, idesc, 1);
     }
     tc::mma_commit(done);
   };
+  // 16 columns of a lane's row of that product
+  auto drain = [&](int c, int chunks, float (&v)[16]) {
+    uint32_t e[16];
+    tc::tmem_ld16(tw + sum_at(0) + c, v);
+#pragma unroll
+    for (int j = 1; j < kSums; ++j) {
+      if (j < chunks) {
+        tc::tmem_ld_chunks<1>(tw + sum_at(j) + c, e);
+#pragma unroll
+        for (int i = 0; i < 16; ++i) v[i] += __uint_as_float(e[i]);
+      }
+    }
+    tc::tmem_ld_chunks<1>(tw + 128 + c, e);
+#pragma unroll
+    for (int i = 0; i < 16; ++i) v[i] = fmaf(__uint_as_float(e[i]), 1.0f / kSl, v[i]);
+  };
   constexpr int kRun = RP / kSides;  // columns of A a warp drains
   constexpr float kToA = kSa / (kSx * kSx);
   const int shift = 31 - __clz(RP / S);  // log2 of a block of A's columns
   for (int step = 0; step < a.steps; ++step) {
-    if (t == 0) square(sxh, sxl, mine * 4);
+    if (t == 0) square(sxh, sxl, mine);
     __syncwarp();
     finish();
     if (S > 1) {
@@ -902,7 +922,7 @@ __global__ void __launch_bounds__(kSmallThreads, 1)
 #pragma unroll
         for (int c = side * kRun; c < (side + 1) * kRun; c += 16) {
           float v[16];
-          drain16(tw + c, tw + 128 + c, v);
+          drain(c, mine, v);
 #pragma unroll
           for (int h = 0; h < 16; h += 8) {  // a block has 8 columns at least; a warp's row is 128 bytes
             const int col = c + h, dst = col >> shift, at = (q << shift) + (col & ((1 << shift) - 1));
@@ -950,7 +970,7 @@ __global__ void __launch_bounds__(kSmallThreads, 1)
 #pragma unroll
         for (int c = side * kRun; c < (side + 1) * kRun; c += 16) {
           float v[16];
-          drain16(tw + c, tw + 128 + c, v);
+          drain(c, mine, v);
 #pragma unroll
           for (int h = 0; h < 16; h += 8) {
             float w[8];
@@ -966,14 +986,14 @@ __global__ void __launch_bounds__(kSmallThreads, 1)
       }
       settle();
     }
-    if (t == 0) square(sah, sal, RP / 16);
+    if (t == 0) square(sah, sal, RP / 64);
     __syncwarp();
     finish();
     if (live) {
 #pragma unroll
       for (int c = side * kRun; c < (side + 1) * kRun; c += 16) {
         float v[16];
-        drain16(tw + c, tw + 128 + c, v);
+        drain(c, RP / 64, v);
 #pragma unroll
         for (int h = 0; h < 16; h += 8) {
           const uint32_t off = (uint32_t)((c + h) / 64) * kChunk + sw128(row, (c + h) % 64 * 2);
