@@ -1070,6 +1070,222 @@ __global__ void __launch_bounds__(kSmallThreads, 1)
   if (warp == 0) tc::tmem_dealloc(tmem, 512);
 }
 
+// ------------------------------------------------------------------ thin matrices: one launch, fp32
+//
+// Up to 32 rows are too few for the tensor core, whose M is 128 and whose answers take half a
+// microsecond: three waits a step.  Here X stays in shared memory as fp32 columns of RP values, in
+// plain fp32 arithmetic.  A cluster of S CTAs takes one matrix, each a run of its columns; only the
+// shares of X X^T (RP x RP) cross the cluster, each CTA sends its own to all and adds all in the same
+// order.  What bounds it is latency: four barriers a step, and one of the cluster.
+//
+// X X^T: a thread takes a 4 x 4 block of it over every (512 / blocks)-th column, 16 multiply-adds for
+// two 16-byte reads, and the partial blocks are added through shared memory.  B X: a task is one
+// column and 8 (or 4) rows of B, the column in registers, B's rows read as broadcasts.
+
+constexpr int kThinThreads = 512;
+
+struct ThinArgs {
+  Shape s;
+  Rule r;
+  float a, b, c;
+  double eps;
+  int steps, S, most;  // most: columns of a CTA
+};
+
+// Floats of a CTA's shared memory: two buffers of X, then A, B and the shares of two steps.
+struct ThinLayout {
+  int pitch, buffer, a, b, recv, total;
+};
+__host__ __device__ constexpr ThinLayout thin_layout(int rp, int S, int most) {
+  ThinLayout l{};
+  l.pitch = rp + 4;  // neighbouring columns lie 4 banks apart
+  // the idle buffer also holds the partial blocks of X X^T, 16 values a thread
+  l.buffer = most * l.pitch > kThinThreads * 16 ? most * l.pitch : kThinThreads * 16;
+  l.a = 2 * l.buffer;
+  l.b = l.a + rp * rp;
+  l.recv = l.b + rp * rp;
+  l.total = l.recv + (S > 1 ? 2 * S * rp * rp : 0);
+  return l;
+}
+
+template <typename T, int RP>
+__global__ void __launch_bounds__(kThinThreads, 1)
+    ns_thin_kernel(const __grid_constant__ Pointers ptr, const __grid_constant__ ThinArgs g) {
+  extern __shared__ __align__(16) float thin[];
+  __shared__ double norms[kSmallMaxCluster], warps[kThinThreads / 32];
+  constexpr int E = RP * RP, kBlocks = (RP / 4) * (RP / 4), kParts = kThinThreads / kBlocks;
+  const ThinLayout lay = thin_layout(RP, g.S, g.most);
+  const Shape& s = g.s;
+  const int t = threadIdx.x, lane = t & 31, warp = t >> 5;
+  const int S = g.S, q = S > 1 ? (int)cluster_rank() : 0, mi = blockIdx.x / S;
+  const int l_lo = (int)((long long)s.L * q / S), mine = (int)((long long)s.L * (q + 1) / S) - l_lo;
+  const int tn = mi / s.groups;
+  const size_t base = (size_t)(mi % s.groups) * s.rows * s.cols;
+  float* now = thin;
+  float* next = thin + lay.buffer;
+  float *am = thin + lay.a, *bm = thin + lay.b;
+  // element k of this CTA's columns, neighbours in k neighbours in memory
+  const int total = s.R * mine;
+  auto place = [&](int k, int& at, size_t& gl) {
+    int r, l;
+    if (s.tr) {
+      l = k / s.R;
+      r = k - l * s.R;
+      gl = (size_t)(l_lo + l) * s.cols + r;
+    } else {
+      r = k / mine;
+      l = k - r * mine;
+      gl = (size_t)r * s.cols + l_lo + l;
+    }
+    at = l * lay.pitch + r;
+  };
+  for (int k = t; k < mine * lay.pitch; k += kThinThreads) now[k] = 0.0f;  // rows R.. of a column
+  __syncthreads();
+  {
+    const T* in = static_cast<const T*>(ptr.in[tn]) + base;
+    const float* m = g.r.step ? ptr.m[tn] + base : nullptr;
+    float* mo = g.r.step ? ptr.m_out[tn] + base : nullptr;
+    double sum = 0.0;
+#pragma unroll 4
+    for (int k = t; k < total; k += kThinThreads) {
+      int at;
+      size_t gl;
+      place(k, at, gl);
+      float u = to_f32(in[gl]);
+      if (g.r.step) {
+        const float v = new_momentum(g.r, u, m[gl]);
+        mo[gl] = v;
+        u = update_of(g.r, u, v);
+      }
+      now[at] = u;
+      sum = fma((double)u, (double)u, sum);
+    }
+    sum = warp_sum(sum);
+    if (lane == 0) warps[warp] = sum;
+  }
+  if (S > 1) cluster_sync();  // everyone's shared memory may be written from here on
+  else __syncthreads();
+  if (t < S) {
+    double v = 0.0;
+    for (int k = 0; k < kThinThreads / 32; ++k) v += warps[k];
+    if (S > 1) st_remote(at_rank(tc::smem_u32(&norms[q]), t), v);
+    else norms[0] = v;
+  }
+  if (S > 1) cluster_sync();
+  else __syncthreads();
+  double all = 0.0;
+  for (int k = 0; k < S; ++k) all += norms[k];
+  const float scale = (float)(1.0 / (sqrt(all) + g.eps));
+  for (int k = t; k < mine * lay.pitch; k += kThinThreads) now[k] *= scale;
+  __syncthreads();
+
+  for (int step = 0; step < g.steps; ++step) {
+    {  // partial blocks of X X^T into the idle buffer: [part][block][16]
+      const int blk = t % kBlocks, bi = blk / (RP / 4) * 4, bj = blk % (RP / 4) * 4;
+      float acc[16] = {};
+#pragma unroll 2
+      for (int l = t / kBlocks; l < mine; l += kParts) {
+        const float4 x = *reinterpret_cast<const float4*>(now + l * lay.pitch + bi);
+        const float4 y = *reinterpret_cast<const float4*>(now + l * lay.pitch + bj);
+        const float xs[4] = {x.x, x.y, x.z, x.w}, ys[4] = {y.x, y.y, y.z, y.w};
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+#pragma unroll
+          for (int j = 0; j < 4; ++j) acc[4 * i + j] = fmaf(xs[i], ys[j], acc[4 * i + j]);
+      }
+      // value e of a thread at e * 512 + t: no bank conflicts
+#pragma unroll
+      for (int e = 0; e < 16; ++e) next[e * kThinThreads + t] = acc[e];
+    }
+    __syncthreads();
+    float* recv = thin + lay.recv + (step & 1) * S * E;
+    {  // entry e: its kParts values, by kLanes lanes
+      constexpr int kLanes = E < kThinThreads ? kThinThreads / E : 1;
+#pragma unroll
+      for (int e = t / kLanes; e < E; e += kThinThreads / kLanes) {
+        const int i = e / RP, j = e % RP, blk = i / 4 * (RP / 4) + j / 4, v = i % 4 * 4 + j % 4;
+        float sum = 0.0f;
+#pragma unroll 4
+        for (int p = t % kLanes; p < kParts; p += kLanes) sum += next[v * kThinThreads + p * kBlocks + blk];
+#pragma unroll
+        for (int m = 1; m < kLanes; m <<= 1) sum += __shfl_xor_sync(~0u, sum, m);
+        if (t % kLanes == 0) {
+          if (S > 1) {
+            for (int k = 0; k < S; ++k) st_remote(at_rank(tc::smem_u32(recv + q * E + e), k), sum);
+          } else {
+            am[e] = sum;
+          }
+        }
+      }
+    }
+    if (S > 1) {
+      cluster_sync();
+      for (int e = t; e < E; e += kThinThreads) {
+        float sum = 0.0f;
+        for (int k = 0; k < S; ++k) sum += recv[k * E + e];
+        am[e] = sum;
+      }
+    }
+    __syncthreads();
+    for (int e = t; e < E; e += kThinThreads) {
+      const int i = e / RP, j = e % RP;
+      float sum = 0.0f;
+#pragma unroll
+      for (int k = 0; k < RP; ++k) sum = fmaf(am[i * RP + k], am[k * RP + j], sum);
+      bm[e] = fmaf(g.c, sum, fmaf(g.b, am[e], i == j ? g.a : 0.0f));
+    }
+    __syncthreads();
+    {
+      constexpr int kTake = RP < 8 ? RP : 8, kSets = RP / kTake;
+      const int tasks = mine * kSets;
+      for (int k = t; k < tasks; k += kThinThreads) {
+        const int set = kSets == 1 ? 0 : k / mine, l = kSets == 1 ? k : k - set * mine;
+        float x[RP];
+#pragma unroll
+        for (int i = 0; i < RP; i += 4) {
+          const float4 v = *reinterpret_cast<const float4*>(now + l * lay.pitch + i);
+          x[i] = v.x;
+          x[i + 1] = v.y;
+          x[i + 2] = v.z;
+          x[i + 3] = v.w;
+        }
+#pragma unroll
+        for (int h = 0; h < kTake; h += 4) {
+          float o[4];
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            const float4* b = reinterpret_cast<const float4*>(bm + (set * kTake + h + i) * RP);
+            float sum = 0.0f;
+#pragma unroll
+            for (int j = 0; j < RP; j += 4) {
+              const float4 v = b[j / 4];
+              sum = fmaf(v.x, x[j], sum);
+              sum = fmaf(v.y, x[j + 1], sum);
+              sum = fmaf(v.z, x[j + 2], sum);
+              sum = fmaf(v.w, x[j + 3], sum);
+            }
+            o[i] = sum;
+          }
+          *reinterpret_cast<float4*>(next + l * lay.pitch + set * kTake + h) = make_float4(o[0], o[1], o[2], o[3]);
+        }
+      }
+    }
+    __syncthreads();
+    float* swap = now;
+    now = next;
+    next = swap;
+  }
+  T* out = static_cast<T*>(ptr.out[tn]) + base;
+  const T* w = g.r.step ? static_cast<const T*>(ptr.w[tn]) + base : nullptr;
+#pragma unroll 4
+  for (int k = t; k < total; k += kThinThreads) {
+    int at;
+    size_t gl;
+    place(k, at, gl);
+    out[gl] = from_f32<T>(result_of(g.r, g.r.step ? to_f32(w[gl]) : 0.0f, now[at]));
+  }
+}
+
 // ------------------------------------------------------------------ host side
 
 int up(int v, int to) { return (v + to - 1) / to * to; }
@@ -1210,25 +1426,63 @@ SmallPlan small_plan(const Shape& s, int sms) {
   return p;
 }
 
+template <typename K, typename... A>
+cudaError_t launch_clusters(K k, int ctas, int cluster, int threads, size_t smem, cudaStream_t st, const A&... args) {
+  cudaLaunchConfig_t cfg{};
+  cfg.gridDim = dim3((unsigned)ctas);
+  cfg.blockDim = dim3((unsigned)threads);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = st;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeClusterDimension;
+  attr[0].val.clusterDim.x = (unsigned)cluster;
+  attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  cudaError_t e = cudaLaunchKernelEx(&cfg, k, args...);
+  count_launch();
+  return e != cudaSuccess ? e : cudaGetLastError();
+}
+
 template <typename T, int RP>
 cudaError_t run_small(const Pointers& ptr, const SmallArgs& a, size_t smem, cudaStream_t st) {
   auto k = ns_small_kernel<T, RP>;
   cudaError_t e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
   if (e != cudaSuccess) return e;
-  cudaLaunchConfig_t cfg{};
-  cfg.gridDim = dim3((unsigned)(a.s.nm * a.S));
-  cfg.blockDim = dim3(kSmallThreads);
-  cfg.dynamicSmemBytes = smem;
-  cfg.stream = st;
-  cudaLaunchAttribute attr[1];
-  attr[0].id = cudaLaunchAttributeClusterDimension;
-  attr[0].val.clusterDim.x = (unsigned)a.S;
-  attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
-  cfg.attrs = attr;
-  cfg.numAttrs = 1;
-  e = cudaLaunchKernelEx(&cfg, k, ptr, a);
-  count_launch();
-  return e != cudaSuccess ? e : cudaGetLastError();
+  return launch_clusters(k, a.s.nm * a.S, a.S, kSmallThreads, smem, st, ptr, a);
+}
+
+struct ThinPlan {
+  bool ok = false;
+  int S = 0, most = 0, rp = 0;
+  size_t smem = 0;
+};
+
+// Up to 32 rows: the smallest cluster whose CTAs have little enough to do (an exchange costs about as
+// much as 192 columns of 32 rows) and fit shared memory, as far as there are SMs for all matrices.
+ThinPlan thin_plan(const Shape& s, int sms) {
+  ThinPlan p;
+  if (s.R > 32) return p;
+  p.rp = s.R <= 4 ? 4 : s.R <= 8 ? 8 : s.R <= 16 ? 16 : 32;
+  for (int S = 1; S <= kSmallMaxCluster && S <= s.L; S *= 2) {
+    const int most = (s.L + S - 1) / S;
+    const size_t smem = (size_t)thin_layout(p.rp, S, most).total * sizeof(float);
+    if (smem > kSmallSmem) continue;
+    if (p.ok && (long long)s.nm * S > sms) break;
+    p.ok = true;
+    p.S = S;
+    p.most = most;
+    p.smem = smem;
+    if ((long long)most * p.rp * p.rp <= 192 * 1024) break;
+  }
+  return p;
+}
+
+template <typename T, int RP>
+cudaError_t run_thin(const Pointers& ptr, const ThinArgs& a, size_t smem, cudaStream_t st) {
+  auto k = ns_thin_kernel<T, RP>;
+  cudaError_t e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+  return e != cudaSuccess ? e : launch_clusters(k, a.s.nm * a.S, a.S, kThinThreads, smem, st, ptr, a);
 }
 
 cudaError_t sm_count(int* sms) {
@@ -1252,6 +1506,16 @@ cudaError_t run_chunk(const MuonArgs& a, int t0, int n, char* ws, int sms, cudaS
     }
   }
   Rule r{a.step, a.nesterov, a.momentum, a.keep, a.rate};
+  const ThinPlan tp = thin_plan(s, sms);
+  if (tp.ok) {
+    const ThinArgs g{s, r, a.a, a.b, a.c, a.eps, a.steps, tp.S, tp.most};
+    switch (tp.rp) {
+      case 4: return run_thin<T, 4>(ptr, g, tp.smem, st);
+      case 8: return run_thin<T, 8>(ptr, g, tp.smem, st);
+      case 16: return run_thin<T, 16>(ptr, g, tp.smem, st);
+      default: return run_thin<T, 32>(ptr, g, tp.smem, st);
+    }
+  }
   const SmallPlan sp = small_plan(s, sms);
   if (sp.ok) {
     const SmallArgs g{s, r, a.a, a.b, a.c, a.eps, a.steps, sp.S, sp.nc, sp.max_chunks};
@@ -1310,7 +1574,7 @@ cudaError_t run_chunk(const MuonArgs& a, int t0, int n, char* ws, int sms, cudaS
 
 size_t muon_workspace(int n, int groups, int rows, int cols) {
   const Shape s = shape_of(std::min(n, kTensors), groups, rows, cols);
-  return small_plan(s, kMostSms).ok ? 256 : layout_of(s).total;
+  return thin_plan(s, kMostSms).ok || small_plan(s, kMostSms).ok ? 256 : layout_of(s).total;
 }
 
 cudaError_t launch_muon(const MuonArgs& a, void* workspace, cudaStream_t st) {
