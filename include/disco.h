@@ -310,13 +310,15 @@ disco_status disco_norm_backward(int B, int C, long long npts, disco_dtype dtype
  *
  * update, out, w, grad and w_out are in `dtype`, m and m_out fp32.  The pointer arrays are HOST
  * arrays of n device pointers, read before the call returns.  out[i] may be update[i], w_out[i]
- * may be w[i] and m_out[i] may be m[i]; no other overlap.  The iterates are held as fp16 pairs
- * (hi + lo, 22 bits), products are summed in fp32 and the Frobenius norm in fp64.
- * An update of zeros gives zeros; infinities and NaN spread over their own matrix only; an
- * iterate above 16 in magnitude (coefficients that diverge) ends as infinities or NaN.
+ * may be w[i] and m_out[i] may be m[i]; no other overlap.  The iterates are fp32 for matrices
+ * with a side of at most 32 and fp16 pairs (hi + lo, 22 bits) for others, products are summed in
+ * fp32 and the Frobenius norm in fp64: fp32 results are as close to the exact ones as fp32 matrix
+ * products would leave them.  An update of zeros gives zeros; infinities and NaN spread over their
+ * own matrix only; an iterate above 16 in magnitude (coefficients that diverge) may end as
+ * infinities or NaN.
  * Pointers need the alignment of their elements only.  Scratch comes in through `workspace`, at
  * least disco_orthogonalize_workspace_size bytes for the same n, groups, rows and cols, 256-byte
- * aligned.  Both calls are asynchronous on `stream`, allocate nothing and give the same bits every
+ * aligned (NULL where that is 0, as for matrices of few rows).  Both calls are asynchronous on `stream`, allocate nothing and give the same bits every
  * time.  Errors: DISCO_ERR_INVALID_ARG for a non-positive size, a NULL pointer or one off its
  * element's alignment, an unknown dtype, steps outside 1..32, a coefficient that is not finite or
  * above 32 in magnitude, eps below 1e-30 or not finite, a scalar that is not finite, momentum outside [0, 1),

@@ -58,8 +58,8 @@ disco_status check_update(int n, int groups, int rows, int cols, disco_dtype dty
     if (!std::isfinite(v) || std::fabs(v) > 32) return invalid("a coefficient that is not finite or above 32 in magnitude");
   // below that 1 / (|U| + eps) leaves fp32's range for an update of zeros
   if (!std::isfinite(ns->eps) || ns->eps < 1e-30) return invalid("eps must be finite and at least 1e-30");
-  if (!workspace || ws_bytes < disco::muon_workspace(n, groups, rows, cols))
-    return invalid("workspace missing or too small");
+  const size_t need = disco::muon_workspace(n, groups, rows, cols);
+  if (need && (!workspace || ws_bytes < need)) return invalid("workspace missing or too small");
   if (!aligned(workspace, 256)) return invalid("workspace must be 256-byte aligned");
   return DISCO_OK;
 }

@@ -1,20 +1,28 @@
-// The orthogonalised update of weights: Newton-Schulz products on tensor cores.
+// The orthogonalised update of weights: Newton-Schulz products.
 //
 // For each (rows x cols) matrix U of a call (transposed if rows > cols, so that R <= L):
 //   X = U / (|U|_F + eps), then `steps` times
 //   A = X X^T,  B = a I + b A + c A A,  X <- B X
 // which is the odd polynomial a s + b s^3 + c s^5 on each singular value s.
 //
-// Numbers.  A small singular value is multiplied by `a` in every step, and a rounding error of X
-// in its direction with it: an X rounded to 8 or 11 bits would leave the weak directions of an
-// update wrong by per cents.  So every matrix is kept as an fp16 pair hi + lo (22 bits) under a
-// power-of-two scale, and a product takes three MMAs, hi hi + hi lo + lo hi; what is left out,
-// lo lo, is below 2^-22.  The two small products go into an accumulator of their own.  The tensor
-// core cuts what it adds to an accumulator instead of rounding it (chains of 512 values left a
-// 1024 x 9216 result 3.5e-5 off, 8 times fp32's error), so the large product is taken out and
-// added in registers every 64 values (the one-launch form spreads
-// it over three or four accumulators, 192 values in a chain at most).  Scales: X by 2^12, A by 2^11, B by 2^9, so
-// that |X| <= 16, |A| <= 32, |B| <= 128 stay finite in fp16; lo by 2^11 more, which puts it at hi's
+// Three forms, by R alone unless the columns do not fit:
+//   up to 32 rows      one launch, fp32 on the CUDA cores, a cluster of CTAs per matrix;
+//   33 to 128 rows     one launch, tensor cores, X in shared memory for all steps, a cluster per matrix;
+//   more               a chain of tiled products on tensor cores, operands in global memory (L2).
+// Measured in fp32 (a call's time on the GPU): 4 x 12 in 6.6 us, 64 x 192 in 33, eight 128 x 576 in 62,
+// 256 x 2304 in 140, four 512 x 4608 in 379, 1024 x 9216 in 530.
+//
+// Numbers of the tensor-core forms.  A small singular value is multiplied by `a` in every step, and a
+// rounding error of X in its direction with it: an X rounded to 8 or 11 bits would leave the weak
+// directions of an update wrong by per cents.  So every matrix is kept as an fp16 pair hi + lo (22
+// bits) under a power-of-two scale, and a product takes three MMAs, hi hi + hi lo + lo hi; what is
+// left out, lo lo, is below 2^-22.  bf16 tensors get the same: with A and B from their hi parts alone
+// matrices of a few rows came out 4e-3 off, twice what their own rounding leaves.  The two small
+// products go into an accumulator of their own.  The tensor core cuts what it adds to an accumulator
+// instead of rounding it (chains of 512 values left a 1024 x 9216 result 3.5e-5 off, 8 times fp32's
+// error), so the large product is taken out and added in registers every 64 values, or spread over
+// three or four accumulators (192 values in a chain at most).  Scales: X by 2^12, A by 2^11, B by 2^9,
+// so that |X| <= 16, |A| <= 32, |B| <= 128 stay finite in fp16; lo by 2^11 more, which puts it at hi's
 // size, so that it keeps its bits for entries far below the largest.
 #include <cuda.h>
 #include <cuda_fp16.h>
@@ -1574,7 +1582,7 @@ cudaError_t run_chunk(const MuonArgs& a, int t0, int n, char* ws, int sms, cudaS
 
 size_t muon_workspace(int n, int groups, int rows, int cols) {
   const Shape s = shape_of(std::min(n, kTensors), groups, rows, cols);
-  return thin_plan(s, kMostSms).ok || small_plan(s, kMostSms).ok ? 256 : layout_of(s).total;
+  return thin_plan(s, kMostSms).ok || small_plan(s, kMostSms).ok ? 0 : layout_of(s).total;
 }
 
 cudaError_t launch_muon(const MuonArgs& a, void* workspace, cudaStream_t st) {

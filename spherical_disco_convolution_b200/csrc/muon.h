@@ -26,6 +26,7 @@ struct MuonArgs {
   bool nesterov;
 };
 
+// 0 where a matrix fits the one-launch forms.
 size_t muon_workspace(int n, int groups, int rows, int cols);
 cudaError_t launch_muon(const MuonArgs& a, void* workspace, cudaStream_t st);
 int take_muon_status();

@@ -11,6 +11,7 @@ all tensors of one shape together.  fp32 or bf16; momentum is always fp32.
 from __future__ import annotations
 
 import functools
+import operator
 
 import torch
 
@@ -52,9 +53,29 @@ def _buckets(ts):
 _workspace_size = functools.lru_cache(maxsize=1024)(D.disco_orthogonalize_workspace_size)
 
 
+_cached_rule = functools.lru_cache(maxsize=64)(D.newton_schulz)
+
+
+def _rule(steps, coefficients, eps):
+    a, b, c = coefficients
+    return _cached_rule(operator.index(steps), (float(a), float(b), float(c)), float(eps))
+
+
 def _workspace(x, n, groups, rows, cols):
+    """(tensor that holds it, pointer, bytes); small matrices need none."""
     nb = _workspace_size(n, groups, rows, cols)
-    return x.new_empty(nb, dtype=torch.uint8), nb
+    if nb == 0:
+        return None, None, 0
+    ws = x.new_empty(nb, dtype=torch.uint8)
+    return ws, ws.data_ptr(), nb
+
+
+def _outputs(x, n, dtype=None):
+    """n tensors like x; those of a list share one allocation where they stay on 16 bytes in it."""
+    dtype = dtype or x.dtype
+    if n > 1 and x.numel() * dtype.itemsize % 16 == 0:
+        return list(x.new_empty((n, *x.shape), dtype=dtype).unbind(0))
+    return [x.new_empty(x.shape, dtype=dtype) for _ in range(n)]
 
 
 def _pointers(ts, x, what, dtype=None):
@@ -72,16 +93,16 @@ def orthogonalize(update, groups: int = 1, steps: int = 5, coefficients=COEFFICI
     """The nearly orthogonal factor of each group's matrix of `update` (one tensor, or a list):
     X = U / (|U| + eps), then `steps` times X <- a X + b (X X^T) X + c (X X^T)^2 X."""
     ts, single = _as_list(update, "update")
-    ns = D.newton_schulz(steps, coefficients, eps)
+    ns = _rule(steps, coefficients, eps)
     outs = [None] * len(ts)
     for at in _buckets(ts):
         x = ts[at[0]]
         code = dense(x, "update")
         rows, cols = _matrix(x, groups)
         u = _pointers([ts[i] for i in at], x, "update")
-        out = [torch.empty_like(x, requires_grad=False) for _ in at]
-        ws, nb = _workspace(x, len(at), groups, rows, cols)
-        launch(x, D.disco_orthogonalize, groups, rows, cols, code, ns, u, [o.data_ptr() for o in out], ws.data_ptr(), nb)
+        out = _outputs(x, len(at))
+        ws, p, nb = _workspace(x, len(at), groups, rows, cols)
+        launch(x, D.disco_orthogonalize, groups, rows, cols, code, ns, u, [o.data_ptr() for o in out], p, nb)
         for i, o in zip(at, out):
             outs[i] = o
     return outs[0] if single else outs
@@ -99,7 +120,7 @@ def muon_update(weight, grad, momentum_buffer, lr: float, momentum: float = 0.95
     ms, _ = _as_list(momentum_buffer, "momentum_buffer")
     if not len(ws) == len(gs) == len(ms):
         raise ValueError(f"{len(ws)} weights, {len(gs)} gradients and {len(ms)} momentum buffers")
-    ns = D.newton_schulz(steps, coefficients, eps)
+    ns = _rule(steps, coefficients, eps)
     calls = []
     for at in _buckets(ws):  # everything is checked before anything is written
         x = ws[at[0]]
@@ -111,13 +132,16 @@ def muon_update(weight, grad, momentum_buffer, lr: float, momentum: float = 0.95
         calls.append((at, x, code, rows, cols, w, g, m))
     if inplace and len({p for c in calls for p in c[5] + c[7]}) < 2 * len(ws):
         raise ValueError("a tensor is given twice: each is updated once")
-    w_out = ws if inplace else [torch.empty_like(t, requires_grad=False) for t in ws]
-    m_out = ms if inplace else [torch.empty_like(t, requires_grad=False) for t in ms]
+    w_out, m_out = (ws, ms) if inplace else ([None] * len(ws), [None] * len(ws))
     for at, x, code, rows, cols, w, g, m in calls:
-        work, nb = _workspace(x, len(at), groups, rows, cols)
-        launch(x, D.disco_muon, groups, rows, cols, code, ns, lr, momentum, nesterov, weight_decay, w, g, m,
-               w if inplace else [w_out[i].data_ptr() for i in at], m if inplace else [m_out[i].data_ptr() for i in at],
-               work.data_ptr(), nb)
+        wp, mp = w, m
+        if not inplace:
+            wo, mo = _outputs(x, len(at)), _outputs(x, len(at), torch.float32)
+            wp, mp = [t.data_ptr() for t in wo], [t.data_ptr() for t in mo]
+            for i, a, b in zip(at, wo, mo):
+                w_out[i], m_out[i] = a, b
+        work, p, nb = _workspace(x, len(at), groups, rows, cols)
+        launch(x, D.disco_muon, groups, rows, cols, code, ns, lr, momentum, nesterov, weight_decay, w, g, m, wp, mp, p, nb)
     return (w_out[0], m_out[0]) if single else (w_out, m_out)
 
 

@@ -44,8 +44,8 @@ def _muon(lr=0.1, momentum=0.9, wd=0.0, w=(P,), g=(P,), m=(P,), wo=(P,), mo=(P,)
     (dict(groups=0), 1), (dict(rows=0), 1), (dict(cols=-3), 1), (dict(dtype=2), 1), (dict(steps=0), 1),
     (dict(steps=33), 1), (dict(coef=(math.nan, 0, 0)), 1), (dict(coef=(1, 33, 0)), 1), (dict(coef=(1, 0, -math.inf)), 1),
     (dict(eps=0.0), 1), (dict(eps=-1.0), 1), (dict(eps=9e-31), 1), (dict(eps=math.inf), 1), (dict(eps=math.nan), 1), (dict(ps=(None,)), 1), (dict(outs=(None,)), 1),
-    (dict(ps=(P + 2,)), 1), (dict(outs=(P + 1,), dtype=1), 1), (dict(ws=None), 1), (dict(ws=P + 128), 1),
-    (dict(nb=64), 1), (dict(ps=(), outs=()), 1), (dict(groups=65536), 2), (dict(rows=32769), 2), (dict(cols=40000), 2),
+    (dict(ps=(P + 2,)), 1), (dict(outs=(P + 1,), dtype=1), 1), (dict(ws=None, rows=200, cols=300), 1),
+    (dict(ws=P + 128), 1), (dict(nb=64, rows=200, cols=300), 1), (dict(ps=(), outs=()), 1), (dict(groups=65536), 2), (dict(rows=32769), 2), (dict(cols=40000), 2),
 ])
 def test_orthogonalize_refuses(kw, want):
     assert _status(lambda: _orth(**kw)) == want
@@ -64,7 +64,8 @@ def test_null_rule_and_workspace_size():
     assert D.library().disco_orthogonalize(1, 1, 4, 8, 0, None, None, None, None, 0, None) == D.DISCO_ERR_INVALID_ARG
     assert D.library().disco_orthogonalize_workspace_size(1, 1, 4, 8, None) == D.DISCO_ERR_INVALID_ARG
     assert _status(D.disco_orthogonalize_workspace_size, 0, 1, 4, 8) == D.DISCO_ERR_INVALID_ARG
-    assert D.disco_orthogonalize_workspace_size(2, 2, 64, 192) > 0
+    assert D.disco_orthogonalize_workspace_size(2, 2, 64, 192) == 0
+    assert D.disco_orthogonalize_workspace_size(2, 2, 200, 300) > 0
 
 
 def test_python_refuses():
@@ -316,7 +317,7 @@ def test_bases_off_sixteen_bytes_and_neighbours_untouched(shape, dtype, cuda):
     src = torch.zeros(n + 8, dtype=dtype, device=cuda)
     v = src[3:3 + n].view(shape).copy_(u)
     nb = D.disco_orthogonalize_workspace_size(1, 1, *shape)
-    ws = torch.empty(nb, dtype=torch.uint8, device=cuda)
+    ws = torch.empty(nb + 256, dtype=torch.uint8, device=cuda)
     code = D.DISCO_F32 if dtype == F32 else D.DISCO_BF16
     D.disco_orthogonalize(1, *shape, code, D.newton_schulz(5, NS, 1e-7), [v.data_ptr()], [buf[31:].data_ptr()],
                           ws.data_ptr(), nb, torch.cuda.current_stream().cuda_stream)
@@ -330,7 +331,7 @@ def test_the_result_may_replace_the_update(shape, cuda):
     u = update(shape, F32, 17, cuda)
     want = muon.orthogonalize(u)
     nb = D.disco_orthogonalize_workspace_size(1, 1, *shape)
-    ws = torch.empty(nb, dtype=torch.uint8, device=cuda)
+    ws = torch.empty(nb + 256, dtype=torch.uint8, device=cuda)
     D.disco_orthogonalize(1, *shape, D.DISCO_F32, D.newton_schulz(5, NS, 1e-7), [u.data_ptr()], [u.data_ptr()],
                           ws.data_ptr(), nb, torch.cuda.current_stream().cuda_stream)
     assert torch.equal(u, want)
