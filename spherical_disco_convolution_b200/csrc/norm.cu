@@ -439,6 +439,7 @@ __global__ void norm_reduce_kernel(const float* __restrict__ part, int rows, int
   const int col = blockIdx.x * 32 + threadIdx.x;
   float s = 0.0f;
   if (col < 2 * C)
+#pragma unroll 4
     for (int r = threadIdx.y; r < rows; r += 32) s += part[(size_t)r * 2 * C + col];
   sum[threadIdx.y][threadIdx.x] = s;
   __syncthreads();
@@ -562,6 +563,8 @@ cudaError_t pick_bwd(const Plan& p, const NormArgs& a, int rows, cudaStream_t st
 
 }  // namespace
 
+int norm_partials(int sms) { return kBwdCtasPerSm * sms; }
+
 cudaError_t launch_norm(bool bf16, const NormArgs& a, int sms, cudaStream_t st) {
   int r = 0;
   cudaError_t err;
@@ -594,7 +597,7 @@ cudaError_t launch_norm_backward(bool bf16, const NormArgs& a, int sms, cudaStre
   const int es = bf16 ? 2 : 4;
   const int vec = vec_of(es, a.npts, {a.x, a.dout, a.dx});
   const Plan p = plan_of(es, vec, a.B, a.C, a.npts, sms);
-  const int rows = (int)std::min<long long>(p.tiles, (long long)kBwdCtasPerSm * sms);
+  const int rows = (int)std::min<long long>(p.tiles, norm_partials(sms));
   if (bf16) {
     switch (vec) {
       case 8: return pick_bwd<__nv_bfloat16, 8>(p, a, rows, st);

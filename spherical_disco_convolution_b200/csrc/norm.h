@@ -27,7 +27,7 @@ struct NormArgs {
 constexpr int kNormMaxChannels = 16384;
 
 // Most rows of 2C partial sums the backward pass leaves for its reduction on a device of `sms` SMs.
-int norm_partials(int C, int sms);
+int norm_partials(int sms);
 // The ring form (norm_ring.cu) of either pass; false where its tiles do not fit.  *rows: rows of
 // partial sums the backward pass leaves (at most norm_partials).
 bool launch_norm_ring(bool bf16, const NormArgs& a, bool bwd, int sms, cudaStream_t st, int* rows, cudaError_t* err);

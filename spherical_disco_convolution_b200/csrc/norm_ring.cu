@@ -603,8 +603,9 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
   }
   if (!a.part) return;
-  // one row of 2C sums per group
-  float* row = a.part + ((size_t)blockIdx.x * G + group) * 2 * a.C;
+  // one row of 2C sums per CTA, its groups added in order; the ring is idle and holds theirs
+  float* sums = reinterpret_cast<float*>(ring.stage);
+  __syncthreads();
 #pragma unroll
   for (int j = 0; j < NC; ++j) {
     const int c = w + kRows * j;
@@ -615,9 +616,16 @@ __global__ void __launch_bounds__(kThreads, 1)
       d += __shfl_xor_sync(~0u, d, m);
     }
     if (lane == 0 && c < a.C) {
-      row[c] = g;
-      row[a.C + c] = d;
+      sums[group * 2 * a.C + c] = g;
+      sums[(group * 2 + 1) * a.C + c] = d;
     }
+  }
+  __syncthreads();
+  for (int i = threadIdx.x; i < 2 * a.C; i += kThreads) {
+    float v = 0.0f;
+#pragma unroll
+    for (int g = 0; g < G; ++g) v += sums[g * 2 * a.C + i];
+    a.part[(size_t)blockIdx.x * 2 * a.C + i] = v;
   }
 }
 
@@ -687,7 +695,7 @@ bool try_form(Call& call, int least) {
   const int grid = (int)std::min<long long>(call.sms, a.tiles);
   const size_t smem = (size_t)stages * stage + tail;
   const bool bf16 = sizeof(T) == 2;
-  call.rows = F::G * grid;
+  call.rows = grid;
   CUtensorMap mx{}, md{};
   if (F::kTma && (!field_map(&mx, bf16, n.x, a, F::kPts) || (call.bwd && !field_map(&md, bf16, n.dout, a, F::kPts)))) {
     call.err = cudaErrorInvalidValue;
@@ -760,9 +768,6 @@ bool launch_norm_ring(bool bf16, const NormArgs& n, bool bwd, int sms, cudaStrea
   *err = c.err;
   return ran;
 }
-
-// One row per group of the backward pass's forms.
-int norm_partials(int C, int sms) { return (C <= 16 ? 16 : C <= 32 ? 8 : C <= 64 ? 4 : 2) * sms; }
 
 int take_norm_status() {
   int v = 0, z = 0;
