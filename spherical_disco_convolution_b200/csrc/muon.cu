@@ -40,7 +40,8 @@ namespace {
 constexpr float kSx = 4096.0f, kSa = 2048.0f, kSb = 512.0f, kSl = 2048.0f;
 constexpr int kTile = 128;       // a CTA's rows of a product's tile, and its share of the operands
 constexpr int kBk = 64;          // K values per stage: one 128-byte swizzle row of fp16
-constexpr int kMaxSplits = 8;    // of the K range of a symmetric product
+constexpr int kMaxSplits = 8;    // of the K range of a product
+constexpr int kLeastJoin = 8;      // chunks of a product that a cluster of single CTAs shares, at least
 constexpr int kStages = 3;
 constexpr uint32_t kOperand = kTile * 128;   // one [128][64] fp16 operand tile, bytes
 constexpr uint32_t kStageBytes = 4 * kOperand;
@@ -227,6 +228,7 @@ __global__ void __launch_bounds__(256) ns_load_kernel(const __grid_constant__ Po
 // ------------------------------------------------------------------ the products
 
 enum Product { kSymmetric, kUpdate, kFinal };
+enum Team { kAlone, kPair, kJoined };  // who makes a tile: one CTA, a pair, a cluster over parts of K
 
 // What becomes of the entries of a symmetric product: A from those of X X^T (am null), or
 // B = a I + b A + c A A from those of A A.
@@ -307,7 +309,9 @@ __device__ __forceinline__ void become(const Becomes& f, size_t plane, size_t at
 // PAIR: two CTAs (cta_group::2) make a 256 x 256 tile.  Each brings 128 rows of P and 128 columns of Q
 // and gets 128 rows of D, so that 64 KB from L2 feed 1536 cycles of MMA; one CTA with a 128 x 128 tile
 // needs 64 KB for 768, more than L2 gives when all SMs ask (1024 x 9216: 2.4x slower).  Below one
-// tile for every pair latency counts instead, and one CTA makes a 128 x 128 tile.
+// tile for every pair latency counts instead, and one CTA makes a 128 x 128 tile, or a cluster of S
+// CTAs does, each over its part of K: then each adds a band of rows of all their sums, in an order of
+// its own that never changes, and writes it.  (Pairs split only symmetric products, through partial sums in global memory.)
 //
 // Warp 16 streams the four operand tiles of each K chunk by TMA, all counted on the first CTA's
 // barrier; lane 0 of the first CTA's warp 17 issues the MMAs for both; warps 0..15 of both CTAs add
@@ -325,6 +329,14 @@ __device__ __forceinline__ uint32_t at_rank(uint32_t addr, uint32_t rank) {
   uint32_t r;
   asm("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(r) : "r"(addr), "r"(rank));
   return r;
+}
+__device__ __forceinline__ float4 ld_remote(uint32_t addr) {
+  float4 v;
+  asm volatile("ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [%4];"
+               : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w)
+               : "r"(addr)
+               : "memory");
+  return v;
 }
 // The same box load, counted on a barrier of either CTA of the pair.
 __device__ __forceinline__ void pair_load_3d(void* dst, const CUtensorMap* map, uint32_t bar, int c0, int c1, int c2) {
@@ -357,10 +369,11 @@ __device__ __forceinline__ void arrive_remote(uint32_t bar) {
   asm volatile("mbarrier.arrive.shared::cluster.b64 _, [%0];" ::"r"(bar) : "memory");
 }
 
-template <typename T, Product MODE, bool PAIR>
+template <typename T, Product MODE, Team TEAM>
 __global__ void __launch_bounds__(kProductThreads, 1)
     ns_product_kernel(const __grid_constant__ CUtensorMap map_p, const __grid_constant__ CUtensorMap map_q,
                       const __grid_constant__ Pointers ptr, const __grid_constant__ ProductArgs a) {
+  constexpr bool PAIR = TEAM == kPair, joined = TEAM == kJoined;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = align1024(smem_raw);
   uint64_t* full = reinterpret_cast<uint64_t*>(smem + kStages * kStageBytes);
@@ -372,10 +385,10 @@ __global__ void __launch_bounds__(kProductThreads, 1)
   constexpr bool kMn = MODE != kSymmetric;
   constexpr int kCtas = PAIR ? 2 : 1, kSide = kCtas * kTile, kCols = kSide / 4;  // columns of a warp
   const Shape& s = a.s;
-  const uint32_t rank = PAIR ? cluster_rank() : 0;
+  const uint32_t rank = PAIR ? cluster_rank() : 0;  // of the pair
   const int job = (int)blockIdx.x / kCtas;
   int tile = job / a.S, bm = 0, bn = 0;
-  const int split_k = job % a.S;
+  const int split_k = job % a.S;                    // and the rank of a joined CTA in its cluster
   if (MODE == kSymmetric) {
     while (tile >= a.tn - bm) tile -= a.tn - bm++;
     bn = bm + tile;
@@ -391,7 +404,7 @@ __global__ void __launch_bounds__(kProductThreads, 1)
   auto p_mn = [&](int k) { return a.upper && k * kBk / kSide < bm; };
   auto q_mn = [&](int k) { return kMn || (a.upper && k * kBk / kSide < bn); };
   auto all_sync = [] {
-    if constexpr (PAIR) cluster_sync();
+    if constexpr (PAIR || joined) cluster_sync();
     else __syncthreads();
   };
 
@@ -484,6 +497,14 @@ __global__ void __launch_bounds__(kProductThreads, 1)
     commit(done);
   }
   __syncwarp();
+  bool ok = true;
+  // The tile goes through the operand buffers, which are free: 128 rows of kSide fp32 values, the
+  // 16-byte blocks of a row exchanged by the row's last bits.  What is made of it then runs in
+  // short loops: unrolled over a thread's registers the code came cold from L2 and cost 8 us.
+  constexpr uint32_t kRowBytes = kSide * 4;
+  auto block_of = [&](int r, int block) {
+    return reinterpret_cast<float4*>(smem + r * kRowBytes + (((uint32_t)block ^ ((uint32_t)r & 7u)) << 4));
+  };
   if (warp < kDrainWarps) {
     const int quarter = (warp & 3) * 32, c0 = (warp >> 2) * kCols;
     const uint32_t tw = tmem + ((uint32_t)quarter << 16) + c0;
@@ -491,7 +512,6 @@ __global__ void __launch_bounds__(kProductThreads, 1)
     float acc[kCols];
 #pragma unroll
     for (int i = 0; i < kCols; ++i) acc[i] = 0.0f;
-    bool ok = true;
     for (int i = 0; i < k_hi - k_lo && ok; ++i) {
       ok = tc::mbar_wait(tfull, i & 1);
       tc::fence_after_sync();
@@ -513,13 +533,6 @@ __global__ void __launch_bounds__(kProductThreads, 1)
     }
     ok = ok && tc::mbar_wait(done, 0);
     tc::fence_after_sync();
-    // The tile goes through the operand buffers, which are free: 128 rows of kSide fp32 values, the
-    // 16-byte blocks of a row exchanged by the row's last bits.  What is made of it then runs in
-    // short loops: unrolled over a thread's registers the code came cold from L2 and cost 8 us.
-    constexpr uint32_t kRowBytes = kSide * 4;
-    auto block_of = [&](int r, int block) {
-      return reinterpret_cast<float4*>(smem + r * kRowBytes + (((uint32_t)block ^ ((uint32_t)r & 7u)) << 4));
-    };
 #pragma unroll
     for (int c = 0; c < kCols; c += 16) {
       float v[16];
@@ -530,23 +543,49 @@ __global__ void __launch_bounds__(kProductThreads, 1)
             make_float4(fmaf(v[i], 1.0f / kSl, acc[c + i]), fmaf(v[i + 1], 1.0f / kSl, acc[c + i + 1]),
                         fmaf(v[i + 2], 1.0f / kSl, acc[c + i + 2]), fmaf(v[i + 3], 1.0f / kSl, acc[c + i + 3]));
     }
-    tc::named_bar_sync(1, kDrainWarps * 32);
+    tc::fence_before_sync();
+  }
+  if constexpr (joined) cluster_sync();  // the sums of all CTAs of the cluster are in their buffers
+  else __syncthreads();
+  // 16 bytes of the tile, over all parts of K
+  auto sum_of = [&](int r, int block) {
+    float4 v = *block_of(r, block);
+    if constexpr (joined) {  // from itself on: all would ask the same CTA at a time otherwise
+      const uint32_t addr = tc::smem_u32(block_of(r, block));
+      float4 x[kMaxSplits];
+#pragma unroll
+      for (int k = 1; k < kMaxSplits; ++k)
+        if (k < a.S) x[k] = ld_remote(at_rank(addr, (split_k + k) & (a.S - 1)));
+#pragma unroll
+      for (int k = 1; k < kMaxSplits; ++k) {
+        if (k < a.S) {
+          v.x += x[k].x;
+          v.y += x[k].y;
+          v.z += x[k].z;
+          v.w += x[k].w;
+        }
+      }
+    }
+    return v;
+  };
+  if (warp < kDrainWarps && ok) {
     const size_t pa = (size_t)s.nm * s.Rp * s.Rp, px = (size_t)s.nm * s.Rp * s.Lp;
     const size_t tensor = (size_t)(mi % s.groups) * s.rows * s.cols;
-    if (ok && MODE == kSymmetric && a.S > 1) {
+    if (PAIR && MODE == kSymmetric && a.S > 1) {
 #pragma unroll 2
       for (int r = warp; r < kTile; r += kDrainWarps) {  // a warp takes a row, a lane 4 columns of each 128
         float* dst = a.part + (size_t)split_k * pa + ((size_t)mi * s.Rp + m0 + r) * s.Rp + n0 + lane * 4;
 #pragma unroll
         for (int h = 0; h < kCtas; ++h) *reinterpret_cast<float4*>(dst + 128 * h) = *block_of(r, lane + 32 * h);
       }
-    } else if (ok && !(MODE == kFinal && s.tr)) {
+    } else if (!(MODE == kFinal && s.tr)) {
       constexpr int kLanes = kSide / 8;  // lanes of a row, 8 columns each
       const int lr = lane % kLanes;
+      const int r_lo = joined ? kTile * split_k / a.S : 0, r_hi = joined ? kTile * (split_k + 1) / a.S : kTile;
 #pragma unroll 2
-      for (int r = warp * (32 / kLanes) + lane / kLanes; r < kTile; r += kDrainWarps * (32 / kLanes)) {
-        const float4 *b0 = block_of(r, 2 * lr), *b1 = block_of(r, 2 * lr + 1);
-        float v[8] = {b0->x, b0->y, b0->z, b0->w, b1->x, b1->y, b1->z, b1->w};
+      for (int r = r_lo + warp * (32 / kLanes) + lane / kLanes; r < r_hi; r += kDrainWarps * (32 / kLanes)) {
+        const float4 x = sum_of(r, 2 * lr), y = sum_of(r, 2 * lr + 1);
+        float v[8] = {x.x, x.y, x.z, x.w, y.x, y.y, y.z, y.w};
         const int row = m0 + r, col = n0 + lr * 8;
         if constexpr (MODE == kSymmetric) {
           const size_t at = ((size_t)mi * s.Rp + row) * s.Rp + col;
@@ -575,23 +614,26 @@ __global__ void __launch_bounds__(kProductThreads, 1)
           }
         }
       }
-    }
-    if (MODE == kFinal && s.tr) {
+    } else {
+      // a warp takes 32 rows of 4 columns, of this CTA's share of the columns
+      const int b_lo = joined ? kSide / 4 * split_k / a.S : 0, b_hi = joined ? kSide / 4 * (split_k + 1) / a.S : kSide / 4;
 #pragma unroll 2
-      for (int k = warp; k < kSide * 4 && ok; k += kDrainWarps) {  // a warp takes 32 rows of a column
-        const int c = k / 4, r = k % 4 * 32 + lane;
-        const float v = reinterpret_cast<const float*>(block_of(r, c / 4))[c % 4];
-        const int row = m0 + r, col = n0 + c;
-        if (row < s.R && col < s.L) {
-          const size_t at = tensor + (size_t)col * s.cols + row;
-          const float w = a.r.step ? to_f32(static_cast<const T*>(ptr.w[mi / s.groups])[at]) : 0.0f;
-          static_cast<T*>(ptr.out[mi / s.groups])[at] = from_f32<T>(result_of(a.r, w, v * (1.0f / (kSb * kSx))));
+      for (int k = b_lo * 4 + warp; k < b_hi * 4; k += kDrainWarps) {
+        const int r = k % 4 * 32 + lane, row = m0 + r, col = n0 + k / 4 * 4;
+        const float4 x = sum_of(r, k / 4);
+        const float v[4] = {x.x, x.y, x.z, x.w};
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          if (row < s.R && col + i < s.L) {
+            const size_t at = tensor + (size_t)(col + i) * s.cols + row;
+            const float w = a.r.step ? to_f32(static_cast<const T*>(ptr.w[mi / s.groups])[at]) : 0.0f;
+            static_cast<T*>(ptr.out[mi / s.groups])[at] = from_f32<T>(result_of(a.r, w, v[i] * (1.0f / (kSb * kSx))));
+          }
         }
       }
     }
-    tc::fence_before_sync();
   }
-  // neither CTA leaves before the other's last arrival and MMA
+  // no CTA leaves before another's last arrival, MMA or read
   all_sync();
   if (warp == kDrainWarps + 1) {
     if constexpr (PAIR)
@@ -1315,15 +1357,23 @@ Shape shape_of(int n, int groups, int rows, int cols) {
   return s;
 }
 
-// Splits of the K range of a symmetric product: as many as give every SM work, each of 256 values at
-// least, unless the second kernel that they need (7 us) costs more than the chunks (1.0 us on a
-// pair, 0.5 us on one CTA) that they save.
-int splits_of(const Shape& s, int k, int sms) {
-  const int nt = s.Rp / s.tile, chunks = k / kBk, ctas = s.tile / kTile;
-  const long long tiles = (long long)nt * (nt + 1) / 2 * s.nm;
-  const int room = (int)std::max<long long>(1, sms / ctas / tiles);
-  const int S = std::max(1, std::min({room, chunks / 4, kMaxSplits}));
-  return (chunks - chunks / S) * ctas < 14 ? 1 : S;
+// Parts of the K range of a product.
+// Pairs (symmetric products only): as many as give every two SMs a pair, each of 256 values at least,
+// unless the second kernel that they need (7 us) costs more than the chunks (1 us) that they save.
+// Single CTAs: a cluster as large as there are SMs for all tiles', for 512 values at least (a chunk takes
+// 0.75 us, the exchange 3 us; 300 x 513 in 144 us, without clusters 155; at 256 values 12 of 200 x 300
+// take 140 us instead of 134); of clusters of 8, 4 and 2 some 16, 32 and 70 run at a time.
+int splits_of(const Shape& s, long long tiles, int k, int sms) {
+  const int chunks = k / kBk;
+  if (s.tile == 256) {
+    const int S = std::max(1, std::min({(int)std::max<long long>(1, sms / 2 / tiles), chunks / 4, kMaxSplits}));
+    return chunks - chunks / S < 7 ? 1 : S;
+  }
+  return chunks < kLeastJoin ? 1 : tiles <= 16 && chunks >= 8 ? 8 : tiles <= 32 ? 4 : tiles <= 70 ? 2 : 1;
+}
+long long symmetric_tiles(const Shape& s) {
+  const long long nt = s.Rp / s.tile;
+  return nt * (nt + 1) / 2 * s.nm;
 }
 
 // The next kernel of a chain, brought up while the one before it runs.
@@ -1368,7 +1418,10 @@ Layout layout_of(const Shape& s) {
   l.x[1] = take(4 * nx);
   l.a = take(4 * na);
   l.b = take(4 * na);
-  l.part = take(4 * na * std::max(splits_of(s, s.Lp, kMostSms), splits_of(s, s.Rp, kMostSms)));
+  if (s.tile == 256) {
+    const long long t = symmetric_tiles(s);
+    l.part = take(4 * na * std::max(splits_of(s, t, s.Lp, kMostSms), splits_of(s, t, s.Rp, kMostSms)));
+  }
   l.norm = take(sizeof(double) * s.nm * kNormBlocks);
   l.total = at;
   return l;
@@ -1388,20 +1441,22 @@ bool plane_map(CUtensorMap* m, const void* base, int cols, int rows, int z) {
 
 constexpr size_t kProductSmem = kStages * kStageBytes + 1024 + 128;
 
-template <typename T, Product MODE, bool PAIR>
-cudaError_t product_on(const CUtensorMap& p, const CUtensorMap& q, const Pointers& ptr, const ProductArgs& a,
+template <typename T, Product MODE, Team TEAM>
+cudaError_t product_by(const CUtensorMap& p, const CUtensorMap& q, const Pointers& ptr, const ProductArgs& a,
                        cudaStream_t st) {
-  auto k = ns_product_kernel<T, MODE, PAIR>;
+  auto k = ns_product_kernel<T, MODE, TEAM>;
   cudaError_t e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kProductSmem);
   if (e != cudaSuccess) return e;
-  const int tiles = MODE == kSymmetric ? a.tn * (a.tn + 1) / 2 : a.tm * a.tn, ctas = PAIR ? 2 : 1;
-  return chain(k, dim3(ctas * tiles * a.S, a.s.nm), ctas, kProductThreads, kProductSmem, st, p, q, ptr, a);
+  const int tiles = MODE == kSymmetric ? a.tn * (a.tn + 1) / 2 : a.tm * a.tn, ctas = TEAM == kPair ? 2 : 1;
+  return chain(k, dim3(ctas * tiles * a.S, a.s.nm), TEAM == kPair ? 2 : TEAM == kJoined ? a.S : 1, kProductThreads,
+               kProductSmem, st, p, q, ptr, a);
 }
 
 template <typename T, Product MODE>
 cudaError_t product(const CUtensorMap& p, const CUtensorMap& q, const Pointers& ptr, const ProductArgs& a,
                     cudaStream_t st) {
-  return a.s.tile == 256 ? product_on<T, MODE, true>(p, q, ptr, a, st) : product_on<T, MODE, false>(p, q, ptr, a, st);
+  if (a.s.tile == 256) return product_by<T, MODE, kPair>(p, q, ptr, a, st);
+  return a.S > 1 ? product_by<T, MODE, kJoined>(p, q, ptr, a, st) : product_by<T, MODE, kAlone>(p, q, ptr, a, st);
 }
 
 struct SmallPlan {
@@ -1556,21 +1611,21 @@ cudaError_t run_chunk(const MuonArgs& a, int t0, int n, char* ws, int sms, cudaS
     g.upper = f.am != nullptr;
     g.tm = g.tn = s.Rp / s.tile;
     g.chunks = k / kBk;
-    g.S = splits_of(s, k, sms);
+    g.S = splits_of(s, symmetric_tiles(s), k, sms);
     g.f = f;
     g.dst = dst;
     cudaError_t err = product<T, kSymmetric>(p, p, ptr, g, st);
-    if (err == cudaSuccess && g.S > 1) err = chain(ns_reduce_kernel, red, 1, 256, 0, st, (const float*)part, s, g.S, f, dst);
+    if (err == cudaSuccess && s.tile == 256 && g.S > 1) err = chain(ns_reduce_kernel, red, 1, 256, 0, st, (const float*)part, s, g.S, f, dst);
     return err;
   };
   for (int k = 0; k < a.steps; ++k) {
     const int now = k & 1;
     if ((e = square(mx[now], s.Lp, Becomes{a.a, a.b, a.c, nullptr}, am)) != cudaSuccess) return e;
     if ((e = square(ma, s.Rp, Becomes{a.a, a.b, a.c, am}, bm)) != cudaSuccess) return e;
-    g.S = 1;
     g.upper = true;
     g.chunks = s.Rp / kBk;
     g.tn = s.Lp / s.tile;
+    g.S = s.tile == 256 ? 1 : splits_of(s, (long long)g.tm * g.tn * s.nm, s.Rp, sms);
     g.dst = x[now ^ 1];
     e = k + 1 < a.steps ? product<T, kUpdate>(mb, mx[now], ptr, g, st) : product<T, kFinal>(mb, mx[now], ptr, g, st);
     if (e != cudaSuccess) return e;
