@@ -7,6 +7,10 @@
 //   dx = r (e - sum(e) / C - xh sum(e xh) / C)
 //   dgain_c = sum_n dout xh,  dbias_c = sum_n dout
 //
+// This is the form for planes shorter than 64 points and for more channels than the tiles of
+// norm_ring.cu hold (1024 forward, 512 backward); long planes with fewer go there (the 64 channels of
+// 721 x 1440 points in bf16 took 107 us forward and 266 backward here, and take 56 and 90 there).
+//
 // The channels of a point lie P elements apart, so a warp reads runs of consecutive points of
 // one channel (16 bytes a lane where the alignment allows) and the sums over channels cross the
 // warps of a CTA.  A CTA is TX lanes over points times TY rows over channels; a thread keeps
