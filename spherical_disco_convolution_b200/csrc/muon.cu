@@ -9,7 +9,7 @@
 //   up to 32 rows      one launch, fp32 on the CUDA cores, a cluster of CTAs per matrix;
 //   33 to 128 rows     one launch, tensor cores, X in shared memory for all steps, a cluster per matrix;
 //   more               a chain of tiled products on tensor cores, operands in global memory (L2).
-// Measured in fp32 (a call's time on the GPU): 4 x 12 in 6.6 us, 64 x 192 in 33, eight 128 x 576 in 62,
+// Measured in fp32 (a call's time on the GPU): 4 x 12 in 6.6 us, 32 x 96 in 18.5, 64 x 192 in 33, eight 128 x 576 in 62,
 // 256 x 2304 in 140, four 512 x 4608 in 379, 1024 x 9216 in 530.
 //
 // Numbers of the tensor-core forms.  A small singular value is multiplied by `a` in every step, and a
@@ -1277,12 +1277,27 @@ __global__ void __launch_bounds__(kThinThreads, 1)
       }
     }
     __syncthreads();
-    for (int e = t; e < E; e += kThinThreads) {
-      const int i = e / RP, j = e % RP;
-      float sum = 0.0f;
+    if (t < E) {  // entries of one column of A A, rows 512 / RP apart
+      constexpr int kPer = E > kThinThreads ? E / kThinThreads : 1, kApart = kThinThreads / RP;
+      const int i = t / RP, j = t % RP;
+      float sum[kPer] = {};
 #pragma unroll
-      for (int k = 0; k < RP; ++k) sum = fmaf(am[i * RP + k], am[k * RP + j], sum);
-      bm[e] = fmaf(g.c, sum, fmaf(g.b, am[e], i == j ? g.a : 0.0f));
+      for (int k = 0; k < RP; k += 4) {
+        const float c[4] = {am[k * RP + j], am[(k + 1) * RP + j], am[(k + 2) * RP + j], am[(k + 3) * RP + j]};
+#pragma unroll
+        for (int p = 0; p < kPer; ++p) {
+          const float4 r = *reinterpret_cast<const float4*>(am + (i + p * kApart) * RP + k);
+          sum[p] = fmaf(r.x, c[0], sum[p]);
+          sum[p] = fmaf(r.y, c[1], sum[p]);
+          sum[p] = fmaf(r.z, c[2], sum[p]);
+          sum[p] = fmaf(r.w, c[3], sum[p]);
+        }
+      }
+#pragma unroll
+      for (int p = 0; p < kPer; ++p) {
+        const int row = i + p * kApart, e = row * RP + j;
+        bm[e] = fmaf(g.c, sum[p], fmaf(g.b, am[e], row == j ? g.a : 0.0f));
+      }
     }
     __syncthreads();
     {
@@ -1521,8 +1536,9 @@ struct ThinPlan {
   size_t smem = 0;
 };
 
-// Up to 32 rows: the smallest cluster whose CTAs have little enough to do (an exchange costs about as
-// much as 192 columns of 32 rows) and fit shared memory, as far as there are SMs for all matrices.
+// Up to 32 rows: the smallest cluster whose CTAs have little enough to do (24 columns of 32 rows or as
+// much work of fewer: 32 x 96 takes 22 us on one CTA and 18.5 on four, 9 x 2000 takes 43 on one, 28 on
+// two and 21 on eight) and fit shared memory, as far as there are SMs for all matrices.
 ThinPlan thin_plan(const Shape& s, int sms) {
   ThinPlan p;
   if (s.R > 32) return p;
@@ -1536,7 +1552,7 @@ ThinPlan thin_plan(const Shape& s, int sms) {
     p.S = S;
     p.most = most;
     p.smem = smem;
-    if ((long long)most * p.rp * p.rp <= 192 * 1024) break;
+    if ((long long)most * p.rp * p.rp <= 24 * 1024) break;
   }
   return p;
 }
