@@ -1525,7 +1525,8 @@ cudaError_t launch_clusters(K k, int ctas, int cluster, int threads, size_t smem
 template <typename T, int RP>
 cudaError_t run_small(const Pointers& ptr, const SmallArgs& a, size_t smem, cudaStream_t st) {
   auto k = ns_small_kernel<T, RP>;
-  cudaError_t e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+  // the same limit in every call: another thread may be between its own two calls here
+  cudaError_t e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kSmallSmem);
   if (e != cudaSuccess) return e;
   return launch_clusters(k, a.s.nm * a.S, a.S, kSmallThreads, smem, st, ptr, a);
 }
@@ -1560,7 +1561,7 @@ ThinPlan thin_plan(const Shape& s, int sms) {
 template <typename T, int RP>
 cudaError_t run_thin(const Pointers& ptr, const ThinArgs& a, size_t smem, cudaStream_t st) {
   auto k = ns_thin_kernel<T, RP>;
-  cudaError_t e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+  cudaError_t e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kSmallSmem);
   return e != cudaSuccess ? e : launch_clusters(k, a.s.nm * a.S, a.S, kThinThreads, smem, st, ptr, a);
 }
 

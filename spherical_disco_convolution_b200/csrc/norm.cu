@@ -531,7 +531,8 @@ cudaError_t bwd(const Plan& p, const NormArgs& a, int rows, cudaStream_t st) {
   const size_t smem = p.red * sizeof(float2) + (NC == 0 ? 2 * (size_t)p.g.C * sizeof(float) : 0);
   auto k = norm_bwd_kernel<T, VEC, NC>;
   if (smem > 48 * 1024) {
-    cudaError_t e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+    // the same limit in every call: another thread may be between its own two calls here
+    cudaError_t e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, 227 * 1024);
     if (e != cudaSuccess) return e;
   }
   k<<<rows, dim3(p.g.TX, p.g.TY), smem, st>>>(

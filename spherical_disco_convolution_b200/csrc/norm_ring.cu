@@ -702,7 +702,8 @@ bool try_form(Call& call, int least) {
     return true;
   }
   auto run = [&](auto k, auto... maps) {
-    cudaError_t e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+    // the same limit in every call: another thread may be between its own two calls here
+    cudaError_t e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kRingSmem);
     if (e != cudaSuccess) return e;
     k<<<grid, kThreads, smem, call.st>>>(maps..., a);
     count_launch();

@@ -10,6 +10,7 @@ Frobenius norm of each matrix.  The store adds half a step of the type, relative
 """
 
 import math
+from concurrent.futures import ThreadPoolExecutor
 
 import pytest
 
@@ -373,6 +374,24 @@ def test_streams_graphs_and_the_same_bits(cuda):
         torch.cuda.synchronize()
         assert all(torch.equal(o, want) for _, o in graphs)
     D.disco_sync_status(torch.cuda.current_stream().cuda_stream)
+
+
+@gpu
+def test_two_threads_at_once(cuda):
+    # sizes of one kernel each that differ in the shared memory they ask for
+    for shapes in [((30, 60), (30, 1500)), ((60, 64), (60, 2000)), ((200, 300), (140, 900))]:
+        us = [update(s, F32, 40 + i, cuda) for i, s in enumerate(shapes)]
+        want = [muon.orthogonalize(u) for u in us]
+        torch.cuda.synchronize()
+
+        def work(i):
+            with torch.cuda.stream(torch.cuda.Stream()):
+                got = [muon.orthogonalize(us[i]) for _ in range(200)]
+            torch.cuda.synchronize()
+            return all(torch.equal(o, want[i]) for o in got)
+
+        with ThreadPoolExecutor(2) as pool:
+            assert all(pool.map(work, range(2)))
 
 
 @gpu

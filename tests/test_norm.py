@@ -14,6 +14,7 @@ and the store rounds to the field's type, half a step relative to the value.
 """
 
 import math
+from concurrent.futures import ThreadPoolExecutor
 
 import pytest
 
@@ -387,6 +388,29 @@ def test_module_takes_any_strides_and_frozen_parameters(cuda):
     assert m.weight.grad is None and m.bias.grad is not None and x.grad is not None
     with pytest.raises(RuntimeError):
         torch.autograd.grad(torch.autograd.grad(m(x).square().sum(), x, create_graph=True)[0].sum(), x)
+
+
+@gpu
+@pytest.mark.parametrize("shapes", [((1, 70, 60, 72), (1, 120, 60, 72)), ((1, 9000, 5, 5), (1, 16000, 5, 5))])
+def test_two_threads_at_once(shapes, cuda):
+    # channels of one kernel each that differ in the shared memory they ask for
+    xs = [field(s, F32, 30 + i, cuda) for i, s in enumerate(shapes)]
+
+    def call(x):
+        out, stats = norm.layer_norm(x)
+        return (out, stats, *norm.layer_norm_backward(x, x, stats))
+
+    want = [call(x) for x in xs]
+    torch.cuda.synchronize()
+
+    def work(i):
+        with torch.cuda.stream(torch.cuda.Stream()):
+            got = [call(xs[i]) for _ in range(100)]
+        torch.cuda.synchronize()
+        return all(torch.equal(a, b) for g in got for a, b in zip(g, want[i]))
+
+    with ThreadPoolExecutor(2) as pool:
+        assert all(pool.map(work, range(2)))
 
 
 @gpu
