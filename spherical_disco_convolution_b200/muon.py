@@ -142,6 +142,8 @@ def muon_update(weight, grad, momentum_buffer, lr: float, momentum: float = 0.95
                 w_out[i], m_out[i] = a, b
         work, p, nb = _workspace(x, len(at), groups, rows, cols)
         launch(x, D.disco_muon, groups, rows, cols, code, ns, lr, momentum, nesterov, weight_decay, w, g, m, wp, mp, p, nb)
+        if inplace:  # a backward pass that kept one of them then raises, as after any in-place operation
+            torch.autograd.graph.increment_version([t[i] for t in (ws, ms) for i in at])
     return (w_out[0], m_out[0]) if single else (w_out, m_out)
 
 

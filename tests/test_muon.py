@@ -377,6 +377,18 @@ def test_streams_graphs_and_the_same_bits(cuda):
 
 
 @gpu
+def test_a_step_in_place_is_seen_by_autograd(cuda):
+    w = torch.nn.Parameter(torch.randn(8, 12, device=cuda))
+    x = torch.randn(5, 8, device=cuda, requires_grad=True)
+    y = (x @ w).sum()
+    opt = muon.Muon([w])
+    w.grad = torch.randn_like(w)
+    opt.step()
+    with pytest.raises(RuntimeError, match="modified by an inplace operation"):
+        y.backward()
+
+
+@gpu
 def test_two_threads_at_once(cuda):
     # sizes of one kernel each that differ in the shared memory they ask for
     for shapes in [((30, 60), (30, 1500)), ((60, 64), (60, 2000)), ((200, 300), (140, 900))]:
