@@ -152,7 +152,7 @@ class Muon(torch.optim.Optimizer):
 
     A parameter group may set `groups` to its layers' group count.  Vectors (biases, norms) belong
     to another optimizer.  The rate and the other scalars are read at every step, and become
-    constants of a CUDA graph that captures it."""
+    constants of a CUDA graph that captures it; a first step, which makes the momentum, is not captured."""
 
     def __init__(self, params, lr: float = 0.02, momentum: float = 0.95, nesterov: bool = True,
                  weight_decay: float = 0.0, groups: int = 1, steps: int = 5, coefficients=COEFFICIENTS,
@@ -186,6 +186,8 @@ class Muon(torch.optim.Optimizer):
                 continue
             for p in ps:
                 if "momentum_buffer" not in self.state[p]:
+                    if torch.cuda.is_current_stream_capturing():  # a replay would start from zeros every time
+                        raise RuntimeError("run one step of Muon before a CUDA graph captures it: it makes the momentum")
                     self.state[p]["momentum_buffer"] = torch.zeros_like(p, dtype=torch.float32)
             muon_update(ps, [p.grad.contiguous() for p in ps], [self.state[p]["momentum_buffer"] for p in ps],
                         group["lr"], group["momentum"], group["nesterov"], group["weight_decay"], group["groups"],

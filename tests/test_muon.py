@@ -97,6 +97,16 @@ def test_momentum_stays_fp32_through_a_checkpoint():
     assert got.dtype == F32 and torch.equal(got, m) and got.data_ptr() != m.data_ptr()
 
 
+def test_a_first_step_is_not_captured(monkeypatch):
+    p = torch.nn.Parameter(torch.zeros(4, 6))
+    p.grad = torch.ones(4, 6)
+    opt = muon.Muon([p])
+    monkeypatch.setattr(torch.cuda, "is_current_stream_capturing", lambda: True)
+    with pytest.raises(RuntimeError, match="before a CUDA graph"):
+        opt.step()
+    assert "momentum_buffer" not in opt.state[p]
+
+
 # ------------------------------------------------------------------ the GPU's results
 
 gpu = pytest.mark.gpu
@@ -374,6 +384,26 @@ def test_streams_graphs_and_the_same_bits(cuda):
         torch.cuda.synchronize()
         assert all(torch.equal(o, want) for _, o in graphs)
     D.disco_sync_status(torch.cuda.current_stream().cuda_stream)
+
+
+@gpu
+@pytest.mark.parametrize("shape", [(12, 20), (64, 192), (200, 300)])
+def test_captured_steps_go_on_from_each_other(shape, cuda):
+    p = torch.nn.Parameter(update(shape, F32, 50, cuda))
+    p.grad = update(shape, F32, 51, cuda)
+    w, m = p.detach().clone(), torch.zeros(shape, device=cuda)
+    opt = muon.Muon([p], lr=0.1)
+    opt.step()
+    w, m = muon.muon_update(w, p.grad, m, 0.1)
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        opt.step()
+    for k in range(2):
+        p.grad.copy_(update(shape, F32, 52 + k, cuda))
+        g.replay()
+        w, m = muon.muon_update(w, p.grad, m, 0.1)
+        torch.cuda.synchronize()
+        assert torch.equal(p.detach(), w) and torch.equal(opt.state[p]["momentum_buffer"], m)
 
 
 @gpu
