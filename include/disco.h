@@ -318,12 +318,13 @@ disco_status disco_norm_backward(int B, int C, long long npts, disco_dtype dtype
  * infinities or NaN.
  * Pointers need the alignment of their elements only.  Scratch comes in through `workspace`, at
  * least disco_orthogonalize_workspace_size bytes for the same n, groups, rows and cols, 256-byte
- * aligned (NULL where that is 0, as for matrices of few rows).  Both calls are asynchronous on `stream`, allocate nothing and give the same bits every
- * time.  Errors: DISCO_ERR_INVALID_ARG for a non-positive size, a NULL pointer or one off its
- * element's alignment, an unknown dtype, steps outside 1..32, a coefficient that is not finite or
- * above 32 in magnitude, eps below 1e-30 or not finite, a scalar that is not finite, momentum outside [0, 1),
- * or a missing or short workspace; DISCO_ERR_UNSUPPORTED for n * groups above 65535 or a matrix
- * side above 32768; DISCO_ERR_CUDA for a failed launch. */
+ * aligned (NULL where that is 0, as for matrices of few rows).  Both calls are asynchronous on
+ * `stream`, allocate nothing and give the same bits every time.  Errors: DISCO_ERR_INVALID_ARG for a
+ * non-positive size, a NULL pointer or one off its element's alignment, an unknown dtype, steps
+ * outside 1..32, a coefficient that is not finite or above 32 in magnitude, eps below 1e-30 or not
+ * finite, a scalar that is not finite, momentum outside [0, 1), or a missing or short workspace;
+ * DISCO_ERR_UNSUPPORTED for n * groups above 65535 or a matrix side above 32768; DISCO_ERR_CUDA for
+ * a failed launch. */
 typedef struct {
   int steps;
   double a, b, c;

@@ -1654,7 +1654,10 @@ cudaError_t run_chunk(const MuonArgs& a, int t0, int n, char* ws, int sms, cudaS
 
 size_t muon_workspace(int n, int groups, int rows, int cols) {
   const Shape s = shape_of(std::min(n, kTensors), groups, rows, cols);
-  return thin_plan(s, kMostSms).ok || small_plan(s, kMostSms).ok ? 0 : layout_of(s).total;
+  if (thin_plan(s, kMostSms).ok || small_plan(s, kMostSms).ok) return 0;
+  // the last tensors of many: fewer matrices, but perhaps more parts of K each
+  const int rest = n > kTensors ? n % kTensors : 0;
+  return std::max(layout_of(s).total, rest ? layout_of(shape_of(rest, groups, rows, cols)).total : 0);
 }
 
 cudaError_t launch_muon(const MuonArgs& a, void* workspace, cudaStream_t st) {

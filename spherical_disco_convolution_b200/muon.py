@@ -91,7 +91,7 @@ def _pointers(ts, x, what, dtype=None):
 
 def orthogonalize(update, groups: int = 1, steps: int = 5, coefficients=COEFFICIENTS, eps: float = 1e-7):
     """The nearly orthogonal factor of each group's matrix of `update` (one tensor, or a list):
-    X = U / (|U| + eps), then `steps` times X <- a X + b (X X^T) X + c (X X^T)^2 X."""
+    X = U / (|U| + eps), then `steps` times X <- a X + b (X X^T) X + c (X X^T)^2 X.  It has no gradient."""
     ts, single = _as_list(update, "update")
     ns = _rule(steps, coefficients, eps)
     outs = [None] * len(ts)

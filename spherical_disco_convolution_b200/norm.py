@@ -29,7 +29,8 @@ def _sizes(x):
 def layer_norm(x: torch.Tensor, gain=None, bias=None, eps: float = 1e-5):
     """(out, stats) of x (B, C, *points): out = gain * (x - mean) * r + bias with mean and r =
     1 / sqrt(var + eps) over the channels of each point; stats (2, B, *points) holds mean and r in
-    fp32, which layer_norm_backward takes.  gain and bias are (C,), in x's type, or None."""
+    fp32, which layer_norm_backward takes.  gain and bias are (C,), in x's type, or None.  Autograd
+    does not see this call; LayerNormS2 has the gradients."""
     code = dense(x, "x")
     B, C, n = _sizes(x)
     gain = like(gain, x, (C,), "gain")

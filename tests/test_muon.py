@@ -69,6 +69,14 @@ def test_null_rule_and_workspace_size():
     assert D.disco_orthogonalize_workspace_size(2, 2, 200, 300) > 0
 
 
+@pytest.mark.parametrize("rows,cols", [(200, 300), (300, 600), (512, 4608), (1000, 1000)])
+def test_the_workspace_of_many_tensors_serves_the_last_few(rows, cols):
+    # 64 tensors go into one set of launches
+    size = [D.disco_orthogonalize_workspace_size(n, 1, rows, cols) for n in range(1, 130)]
+    for n in range(65, 130):
+        assert size[n - 1] >= max(size[63], size[n % 64 - 1] if n % 64 else 0)
+
+
 def test_python_refuses():
     w = torch.zeros(4, 3, 5)
     for call in (lambda: muon.orthogonalize(w), lambda: muon.orthogonalize([]), lambda: muon.muon_update(w, w, w, 0.1),
