@@ -7,6 +7,7 @@
 // is read from HBM once and from shared memory once: its sums are added on the way into registers
 // (at most 32 of packed values a thread), the stage is free for the next tile at once, and the
 // result is formed from the registers after the sums over channels have crossed the group.
+// The number of stages is a multiple of the number of groups, so each stage has one group's tiles.
 // LPR = 32, 16 or 8 lanes take a channel row, VEC points each, so a group has W * 32 / LPR rows of
 // lanes and row r takes the channels r, r + rows, ....  Few channels take small groups (one warp
 // has no barrier at all), many take large ones.
@@ -670,8 +671,11 @@ bool try_form(Call& call, int least) {
   const size_t stage = up128(array * (call.bwd ? 2 : 1) + (call.bwd && F::kTma ? 8 * F::kPts : 0));
   const size_t tail = ring_tail<F>(n.C) + 128;
   int stages = (int)std::min<size_t>(kMaxStages, (kRingSmem - tail) / stage);
-  // rows copied by their own lanes stay with their group; at most four tiles of copies in flight
-  if (!F::kTma) stages = std::min(stages / F::G, 4) * F::G;
+  // A stage stays with one group, whose warps then wait for each of its phases in order: were it to
+  // go from group to group, a fast one could be two phases ahead, which a wait for a parity cannot
+  // tell from none (13 stages and 4 groups: it may take tile 3 for tile 29).
+  // Of rows copied by their own lanes at most four tiles are in flight.
+  stages = (F::kTma ? stages / F::G : std::min(stages / F::G, 4)) * F::G;
   if (stages < (F::kTma ? 3 : 2 * F::G)) return false;
   a.tiles_per_plane = (int)((n.npts + F::kPts - 1) / F::kPts);
   a.tiles = (long long)n.B * a.tiles_per_plane;

@@ -318,6 +318,28 @@ def test_the_same_bits_every_time(cuda):
 
 
 @gpu
+@pytest.mark.parametrize("C", [12, 30, 60, 64, 100])
+def test_many_tiles_in_groups_out_of_step(C, cuda):
+    # groups of 1 to 8 warps, each through hundreds of tiles, beside copies that slow some SMs
+    for dtype in (F32, BF16):
+        x, dout = field((1, C, 361, 720), dtype, 27, cuda), field((1, C, 361, 720), dtype, 28, cuda)
+        check_forward(x, None, None, 1e-5)
+        check_backward(dout, x, None, 1e-5)
+        want = norm.layer_norm(x)
+        want += norm.layer_norm_backward(dout, x, want[1])
+        side = torch.cuda.Stream()
+        other = torch.zeros(1 << 24, device=cuda)
+        side.wait_stream(torch.cuda.current_stream())
+        for _ in range(20):
+            with torch.cuda.stream(side):
+                other.add_(1)
+            got = norm.layer_norm(x)
+            got += norm.layer_norm_backward(dout, x, got[1])
+            assert all(torch.equal(a, b) for a, b in zip(got, want))
+        torch.cuda.current_stream().wait_stream(side)
+
+
+@gpu
 def test_shapes_types_and_devices_are_refused(cuda):
     x = torch.zeros(2, 4, 6, 8, device=cuda)
     stats = torch.zeros(2, 2, 6, 8, device=cuda)
