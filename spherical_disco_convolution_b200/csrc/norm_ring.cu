@@ -278,14 +278,21 @@ __device__ __forceinline__ uint32_t past16(const void* base, size_t at) {
 // What a group does when it has read stage st: the next tile comes into its place.
 template <typename F, bool BWD>
 __device__ __forceinline__ void release(const RingArgs& a, const CUtensorMap* map_x, const CUtensorMap* map_d,
-                                        const Ring& r, int k, int st, int t, int lane, int w) {
+                                        const Ring& r, int k, int st, int t, int lane, int w, bool ok) {
   __syncwarp();
   if (F::kTma) {
     if ((threadIdx.x & 31) == 0) tc::mbar_arrive(&r.empty[st]);
-    if (t < 32 && tc::mbar_wait(&r.empty[st], (k / a.stages) & 1)) load_boxes<F, BWD>(a, map_x, map_d, r, k + a.stages);
+    if (t < 32 && ok && tc::mbar_wait(&r.empty[st], (k / a.stages) & 1)) load_boxes<F, BWD>(a, map_x, map_d, r, k + a.stages);
   } else {
     load_rows<F, BWD>(a, r, k + a.stages, lane, w);
   }
+}
+
+// After a wait that ran out (the status word says so, the results are void) a warp waits and loads
+// no more, which ends the kernel soon; the copies in flight get 2 ms to land before the CTA goes.
+__device__ __noinline__ void give_up() {
+  const unsigned long long t0 = tc::globaltimer();
+  while (tc::globaltimer() - t0 < 2000000ull) __nanosleep(1000);
 }
 
 template <typename F, bool BWD>
@@ -335,12 +342,13 @@ __global__ void __launch_bounds__(kThreads, 1)
   const float inv_c = 1.0f / (float)a.C;
   const int n_lo = a.C / kRows, extra = a.C % kRows;
   int k = group;
+  bool ok = true;
   for (long long tile = blockIdx.x + (long long)group * gridDim.x; tile < a.tiles;
        tile += (long long)G * gridDim.x, k += G) {
     const int st = k % a.stages;
     const Tile tl = tile_of<F>(a, tile);
     const uint8_t* rows = ring.stage + (size_t)st * a.stage_bytes;
-    if (F::kTma) tc::mbar_wait(&ring.full[st], (k / a.stages) & 1);
+    if (F::kTma) ok = ok && tc::mbar_wait(&ring.full[st], (k / a.stages) & 1);
     else wait_rows(a.stages / G - 1);
     uint32_t raw[NC][F::kWords];
     F2 s[NP], q[NP], first[NP];
@@ -351,7 +359,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       const int c = w + kRows * j;
       if (F::kFull || c < a.C) read_row<F>(rows + c * F::kPitch + past16<F>(a.x, tl.at + (size_t)c * a.npts), lane, raw[j]);
     }
-    release<F, false>(a, &map_x, nullptr, ring, k, st, t, lane, w);
+    release<F, false>(a, &map_x, nullptr, ring, k, st, t, lane, w, ok);
     if (F::kFull || nch > 0) {
 #pragma unroll
       for (int i = 0; i < NP; ++i) first[i] = neg2(pair_of<F>(raw[0], i));
@@ -447,6 +455,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
     }
   }
+  if (F::kTma && !ok) give_up();
 }
 
 template <typename F>
@@ -483,6 +492,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
   };
   int k = group;
+  bool ok = true;
   const long long tile0 = blockIdx.x + (long long)group * gridDim.x;
   if (!F::kTma) fetch_stats(tile0);
   for (long long tile = tile0; tile < a.tiles; tile += (long long)G * gridDim.x, k += G) {
@@ -490,7 +500,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     const Tile tl = tile_of<F>(a, tile);
     const uint8_t* rows = ring.stage + (size_t)st * a.stage_bytes;
     if (F::kTma) {
-      tc::mbar_wait(&ring.full[st], (k / a.stages) & 1);
+      ok = ok && tc::mbar_wait(&ring.full[st], (k / a.stages) & 1);
       const float* sm = reinterpret_cast<const float*>(rows + a.stat_off) + lane * VEC;
       const bool in = lane * VEC < tl.valid;  // planes are whole vectors long
 #pragma unroll
@@ -534,7 +544,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
       }
     }
-    release<F, true>(a, &map_x, &map_d, ring, k, st, t, lane, w);
+    release<F, true>(a, &map_x, &map_d, ring, k, st, t, lane, w, ok);
 #pragma unroll
     for (int j = 0; j < NC; ++j) {
       const int c = w + kRows * j;
@@ -603,6 +613,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
     }
   }
+  if (F::kTma && !ok) give_up();
   if (!a.part) return;
   // one row of 2C sums per CTA, its groups added in order; the ring is idle and holds theirs
   float* sums = reinterpret_cast<float*>(ring.stage);
