@@ -275,10 +275,15 @@ __device__ __forceinline__ uint32_t past16(const void* base, size_t at) {
   return ((uint32_t)reinterpret_cast<uintptr_t>(base) + (uint32_t)at * (uint32_t)sizeof(typename F::T)) & 15u;
 }
 
-// What a group does when it has read stage st: the next tile comes into its place.
+// What a group does when it has read stage st: the next tile comes into its place.  A box is written
+// by the async proxy, which an arrival alone does not order behind this proxy's reads: without the
+// fence the last loads of a busy SM were still in flight when the next tile landed (64 bytes of a
+// channel from tile k + stages, in 1 of some 300 calls of one form).  Rows copied by cp.async need none:
+// the copies are this proxy's, and a warp's own.
 template <typename F, bool BWD>
 __device__ __forceinline__ void release(const RingArgs& a, const CUtensorMap* map_x, const CUtensorMap* map_d,
                                         const Ring& r, int k, int st, int t, int lane, int w, bool ok) {
+  if (F::kTma) tc::fence_proxy_async();
   __syncwarp();
   if (F::kTma) {
     if ((threadIdx.x & 31) == 0) tc::mbar_arrive(&r.empty[st]);

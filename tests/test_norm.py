@@ -490,3 +490,27 @@ def test_offsets_beyond_32_bits(cuda):
     size = torch.stack([sum(x[b, c].abs().sum(dtype=torch.float64) for b in range(B)) for c in range(C)])
     # a thread adds up to 2^28 / (2 * 148 * 32 lanes) of a channel's values in a row
     check(dbias, want, (2 ** 28 / (2 * 148 * 32) + 128) * U * size + half_step(want, BF16) * (1 + 2 ** -6), "dbias")
+
+
+@gpu
+@pytest.mark.parametrize("dtype", [F32, BF16])
+@pytest.mark.parametrize("C", [8, 24, 64, 100, 128, 200, 500])
+def test_a_tile_is_read_before_the_next_one_lands(C, dtype, cuda):
+    """Calls that start together with another stream's kernel, behind work that empties the L2 cache:
+    the same bits as a call alone (a tile overwritten while it was read showed up here)."""
+    n = 2 ** 25 // C // 8 * 8
+    x, dout = field((1, C, n), dtype, 63, cuda), field((1, C, n), dtype, 64, cuda)
+    want = norm.layer_norm(x)
+    want += norm.layer_norm_backward(dout, x, want[1])
+    torch.cuda.synchronize()
+    for _ in range(60):
+        torch.randn(2 ** 25, device=cuda).mul_(2)
+        side = torch.cuda.Stream()
+        other = torch.zeros(1 << 24, device=cuda)
+        side.wait_stream(torch.cuda.current_stream())
+        with torch.cuda.stream(side):
+            other.add_(1)
+        got = norm.layer_norm(x)
+        got += norm.layer_norm_backward(dout, x, got[1])
+        torch.cuda.current_stream().wait_stream(side)
+        assert all(torch.equal(a, b) for a, b in zip(got, want))
