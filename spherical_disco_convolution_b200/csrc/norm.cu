@@ -17,10 +17,12 @@
 // its NC channels of PT points in registers from the load to the store, so x (and dout) cross
 // HBM once.  What bounds both passes is HBM.
 //
-// Sums are fp32.  The deviation is never formed as a difference of large sums: a thread takes
-// the sum and the squared deviations about its own mean over its NC channels, and partial
-// results combine as (n, s, m2) + (n', s', m2') -> m2 + m2' + (s/n - s'/n')^2 n n' / (n + n')
-// (the pairwise update of Chan, Golub and LeVeque).
+// Sums are fp32.  Neither the mean nor the deviation is formed from large sums: a thread adds the
+// differences of its NC channels from the first of them and their squares (k being one of n values,
+// m2 = sum (x - k)^2 - (sum (x - k))^2 / n loses log2(n) + 1 = 4 bits at most; the looping form adds
+// squared deviations from the running mean), and partial results combine as (n, m, m2) + (n', m', m2') -> mean m + (m' - m) n' / (n + n'),
+// m2 + m2' + (m - m')^2 n n' / (n + n') (the pairwise update of Chan, Golub and LeVeque).  So the mean
+// of equal channels is their value to the bit, and a mean far from zero is rounded about once.
 //
 // The gradients of gain and bias are sums over all points: a thread adds up its channels over
 // every tile its CTA visits, the TX lanes of a channel are added by shuffles, each CTA writes
@@ -55,23 +57,23 @@ struct NormShape {
   int TX, TY;
 };
 
-// Combines (n, s, m2) with the lane `mask` away; n = 0 stands for no values.
-__device__ __forceinline__ void combine_shfl(float& n, float& s, float& m2, int mask) {
-  const float n2 = __shfl_xor_sync(~0u, n, mask), s2 = __shfl_xor_sync(~0u, s, mask),
+// Combines (n, mean, m2) with the lane `mask` away; n = 0 stands for no values.
+__device__ __forceinline__ void combine_shfl(float& n, float& mean, float& m2, int mask) {
+  const float n2 = __shfl_xor_sync(~0u, n, mask), mean2 = __shfl_xor_sync(~0u, mean, mask),
               q2 = __shfl_xor_sync(~0u, m2, mask);
-  const float d = (n > 0.0f && n2 > 0.0f) ? s / n - s2 / n2 : 0.0f;
-  const float w = n + n2 > 0.0f ? n * n2 / (n + n2) : 0.0f;
-  m2 = m2 + q2 + d * d * w;
-  s += s2;
-  n += n2;
+  const float all = n + n2, share = all > 0.0f ? n2 / all : 0.0f;
+  const float d = (n > 0.0f && n2 > 0.0f) ? mean2 - mean : 0.0f;
+  mean = n > 0.0f ? fmaf(d, share, mean) : mean2;
+  m2 = m2 + q2 + d * d * n * share;
+  n = all;
 }
 
 // Channels row ty of a CTA owns: c = ty + TY * i.
 __device__ __forceinline__ int row_channels(int C, int TY, int ty) { return ty < C ? (C - ty + TY - 1) / TY : 0; }
 
-// One tile's statistics: every thread comes with s and m2 of its channels for its PT points and
+// One tile's statistics: every thread comes with mean and m2 of its channels for its PT points and
 // leaves with mean and 1/deviation of the points.  `red` holds TYW rows (one per warp-sized
-// piece of the channel rows) of (s, m2) and one row of results; point (v, e) of the tile sits at
+// piece of the channel rows) of (mean, m2) and one row of results; point (v, e) of the tile sits at
 // e * (V + 1) + v, so that lanes along v and lanes along e are both free of bank conflicts.
 template <int VEC, int NV>
 __device__ __forceinline__ void tile_stats(const NormShape& g, float eps, float2* red, float (&s)[NV * VEC],
@@ -96,17 +98,19 @@ __device__ __forceinline__ void tile_stats(const NormShape& g, float eps, float2
   __syncthreads();
   float2* fin = red + tyw * row;
   const int t = ty * g.TX + tx, nt = g.TX * g.TY;
+  const int least = g.C / g.TY, extra = g.C - least * g.TY;
   for (int p = t; p < V * VEC; p += nt) {
     const int v = p / VEC, e = p % VEC, at = e * (V + 1) + v;
+    // channels of row r of red; row 0 has some
+    auto channels = [&](int r) { return (float)(rpw * least + min(max(extra - r * rpw, 0), rpw)); };
+    const float of = red[at].x;
     float S = 0.0f;
-    for (int r = 0; r < tyw; ++r) S += red[r * row + at].x;
-    const float mean = S / (float)g.C;
+    for (int r = 1; r < tyw; ++r) S = fmaf(red[r * row + at].x - of, channels(r), S);
+    const float mean = of + S / (float)g.C;
     float M = 0.0f;
     for (int r = 0; r < tyw; ++r) {
       const float2 q = red[r * row + at];
-      float n = 0.0f;
-      for (int k = 0; k < rpw; ++k) n += (float)row_channels(g.C, g.TY, r * rpw + k);
-      const float d = n > 0.0f ? q.x / n - mean : 0.0f;
+      const float n = channels(r), d = n > 0.0f ? q.x - mean : 0.0f;
       M += q.y + d * d * n;
     }
     const float rstd = 1.0f / sqrtf(M / (float)g.C + eps);
@@ -168,38 +172,52 @@ __global__ void __launch_bounds__(kMaxThreads) norm_fwd_kernel(NormShape g, cons
       }
     const float inv = nch > 0 ? 1.0f / (float)nch : 0.0f;
 #pragma unroll
-    for (int v = 0; v < NV; ++v)
+    for (int v = 0; v < NV; ++v) {
+#pragma unroll
+      for (int i = 1; i < NC; ++i)  // a channel that is not there adds the first one's difference, 0
+        if (i >= nch) d[i][v] = d[0][v];
 #pragma unroll
       for (int e = 0; e < VEC; ++e) {
+        const float k = to_f32(d[0][v].v[e]);
         float t = 0.0f, q = 0.0f;
 #pragma unroll
-        for (int i = 0; i < NC; ++i) t += to_f32(d[i][v].v[e]);
-        const float m = t * inv;
-#pragma unroll
-        for (int i = 0; i < NC; ++i) {
-          const float u = to_f32(d[i][v].v[e]) - m;
-          if (i < nch) q = fmaf(u, u, q);
+        for (int i = 1; i < NC; ++i) {
+          const float u = to_f32(d[i][v].v[e]) - k;
+          t += u;
+          q = fmaf(u, u, q);
         }
-        s[v * VEC + e] = t;
-        m2[v * VEC + e] = q;
+        s[v * VEC + e] = fmaf(t, inv, k);
+        m2[v * VEC + e] = fmaxf(fmaf(t * -inv, t, q), 0.0f);
       }
+    }
   } else {
-    // running (sum, m2): one value at a time joins the n before it
-    for (int i = 0; i < nch; ++i) {
-      const float n = (float)i, w = n / (n + 1.0f), inv = i > 0 ? 1.0f / n : 0.0f;
+    // running (sum, m2) of the differences from the first: one at a time joins the n before it
+    float k[NV * VEC];
+#pragma unroll
+    for (int v = 0; v < NV; ++v) {
+      P p;
+      if (nch > 0 && live[v]) p = src[v][0];
+#pragma unroll
+      for (int e = 0; e < VEC; ++e) k[v * VEC + e] = nch > 0 && live[v] ? to_f32(p.v[e]) : 0.0f;
+    }
+    for (int i = 1; i < nch; ++i) {
+      const float n = (float)i, w = n / (n + 1.0f), inv = 1.0f / n;
 #pragma unroll
       for (int v = 0; v < NV; ++v) {
         if (!live[v]) continue;
         const P p = src[v][i * step];
 #pragma unroll
         for (int e = 0; e < VEC; ++e) {
-          const float u = to_f32(p.v[e]);
+          const float u = to_f32(p.v[e]) - k[v * VEC + e];
           const float dd = u - s[v * VEC + e] * inv;
           m2[v * VEC + e] += dd * dd * w;
           s[v * VEC + e] += u;
         }
       }
     }
+    const float inv = nch > 0 ? 1.0f / (float)nch : 0.0f;
+#pragma unroll
+    for (int e = 0; e < NV * VEC; ++e) s[e] = fmaf(s[e], inv, k[e]);
   }
   tile_stats<VEC, NV>(g, eps, red, s, m2, tile_vec, stats);
   auto put = [&](int i, int v, const P& p) {

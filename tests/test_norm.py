@@ -514,3 +514,71 @@ def test_a_tile_is_read_before_the_next_one_lands(C, dtype, cuda):
         got += norm.layer_norm_backward(dout, x, got[1])
         torch.cuda.current_stream().wait_stream(side)
         assert all(torch.equal(a, b) for a, b in zip(got, want))
+
+
+# ------------------------------------------------------------------ every form of the kernels
+#
+# Planes of at least 64 points with few enough channels pass through tiles in shared memory, in boxes
+# where rows start on 16 bytes and copied by their own lanes where they do not; the others stay in
+# registers.  These shapes reach each: whole and partial last tiles, several tiles a CTA, one group of
+# warps and many, rows of any phase in 16 bytes.
+FORMS = [(1, 6, 5, 7), (3, 5, 1, 1), (1, 24, 3, 5), (2, 100, 5, 9), (1, 600, 8, 8), (2, 1500, 3, 5),
+         (1, 1, 8, 8), (2, 5, 9, 8), (1, 24, 16, 16), (2, 24, 13, 17), (1, 48, 181, 360), (2, 64, 91, 181), (1, 100, 61, 121),
+         (1, 130, 40, 72), (1, 300, 33, 40), (1, 513, 12, 20), (2, 1000, 9, 11)]
+
+
+def far_adds(x):
+    # additions in a row over deviations from one channel, as in `adds`
+    return adds(x) + 8
+
+
+@gpu
+@pytest.mark.parametrize("dtype", [F32, BF16])
+@pytest.mark.parametrize("value", [3.25, 1013.25, -9999.123, 300.1])
+@pytest.mark.parametrize("shape", FORMS)
+def test_equal_channels_leave_the_bias(shape, value, dtype, cuda):
+    """Points whose channels are all equal (a fill value, say): their mean is the value and xh is 0, to
+    the bit, however large 1 / deviation = 1 / sqrt(eps) is; dx = r (e - mean e)."""
+    C = shape[1]
+    x = torch.full(shape, value, device=cuda).to(dtype)
+    gen = torch.Generator(device=cuda).manual_seed(60)
+    gain, bias = (torch.randn(C, generator=gen, device=cuda).to(dtype) for _ in range(2))
+    out, stats = norm.layer_norm(x, gain, bias, 1e-5)
+    assert torch.equal(stats[0].unsqueeze(1), x[:, :1].float())
+    assert torch.equal(out, bias.view((1, -1) + (1,) * (x.dim() - 2)).expand_as(x))
+    assert torch.allclose(stats[1], torch.full_like(stats[1], 1e-5 ** -0.5), rtol=2 ** -22)
+    dout = field(shape, dtype, 61, cuda)
+    dx, dgain, _ = norm.layer_norm_backward(dout, x, stats, gain)
+    assert (dgain == 0).all()
+    e = dout.double() * col(gain, x)
+    r = stats[1].double().unsqueeze(1)
+    want = r * (e - e.mean(1, keepdim=True))
+    check(dx, want, (adds(x) + 8) * U * r * e.abs().amax(1, keepdim=True) + half_step(want, dtype) * (1 + 2 ** -6) + 1e-37, "dx")
+
+
+@gpu
+@pytest.mark.parametrize("offset", [30.0, 1000.0, -9999.123])
+@pytest.mark.parametrize("shape", FORMS)
+def test_far_from_zero_only_the_mean_is_rounded(shape, offset, cuda):
+    """With k the first channel of a row of lanes and D = max_c |x - k|: the row's mean is k plus the mean
+    of the differences, rounded once to u |mean| besides n u D for the sums; the mean of the point is
+    the first row's plus the mean of the rows' differences from it, rounded once more (in the register
+    form up to 4 rows of a warp join in two steps before that): off by j u |mean| + n u D, j = 2 for
+    tiles and 4 for registers.  x - mean then is off by u |x - mean|, so that
+    |d xh| <= r (j u |mean| + n u D) + (n + 8) u |xh| (1 + r D)."""
+    x = (field(shape, F32, 62, cuda, offset=0.0) + offset).to(F32)
+    out, stats = norm.layer_norm(x)
+    want, mean, r, xh = oracle(x, None, None, 1e-5)
+    xd, n = x.double(), far_adds(x)
+    D = (xd.amax(1, keepdim=True) - xd.amin(1, keepdim=True))
+    j = 2 if x[0, 0].numel() >= 64 and x.shape[1] <= 1024 else 4
+    off = j * U * mean.abs() + n * U * D
+    check(stats[0].unsqueeze(1), mean, off, "mean")
+    tol = r * off + (n + 8) * U * xh.abs() * (1 + r * D) + 1e-37
+    check(out, want, tol, "out")
+    # the backward pass's xh, from the statistics rounded to 32 bits
+    dout = torch.zeros_like(x)
+    at = [0] * (x.dim() - 2)
+    dout[(0, slice(None), *at)] = 1.0
+    _, dgain, _ = norm.layer_norm_backward(dout, x, stats, None, False, True, False)
+    check(dgain, want[(0, slice(None), *at)], tol[(0, slice(None), *at)] + U * xh[(0, slice(None), *at)].abs(), "xh")
