@@ -272,7 +272,9 @@ disco_status disco_mix_weight(int B, int C_in, int C_out, int groups, int K, lon
  *                         dx = r * (e - sum_c e / C - xh * sum_c (e * xh) / C)
  *                         dgain[c] = sum_{b,n} dout * xh,  dbias[c] = sum_{b,n} dout
  *
- * x, gain, bias, out, dout, dx, dgain and dbias are in `dtype`; statistics and sums are fp32.
+ * x, gain, bias, out, dout, dx, dgain and dbias are in `dtype`; statistics and sums over channels are
+ * fp32.  The sums over points (dgain, dbias) are fp32 over eight tiles' values at most and fp64 from
+ * there on, so their error does not grow with the field.
  *   gain, bias : may be NULL (ones, zeros).
  *   stats      : 2 x (B * npts) floats, all means and then all r.  disco_norm writes them (NULL:
  *                it does not), disco_norm_backward reads them.

@@ -35,10 +35,10 @@ disco_status check_norm(int B, int C, long long npts, disco_dtype dtype) {
   return DISCO_OK;
 }
 
-// The backward pass's rows of partial sums; more rows than any GPU of this kind has use for.
+// The backward pass's rows of 2C partial sums, two floats each; more rows than any GPU of this kind has use for.
 constexpr int kWorkspaceSms = 160;
 
-size_t norm_bytes(int C) { return (size_t)disco::norm_partials(kWorkspaceSms) * 2 * C * sizeof(float); }
+size_t norm_bytes(int C) { return (size_t)disco::norm_partials(kWorkspaceSms) * 4 * C * sizeof(float); }
 
 disco_status check_matrices(int n, int groups, int rows, int cols) {
   if (n <= 0 || groups <= 0 || rows <= 0 || cols <= 0) return invalid("n, groups, rows and cols must be positive");

@@ -21,7 +21,7 @@ struct NormArgs {
   void* dx;          // may be null
   void* dgain;       // [C], may be null
   void* dbias;       // [C], may be null
-  float* part;       // backward: norm_partials() x 2C floats
+  float* part;       // backward: norm_partials() x 2C sums of two floats
 };
 
 constexpr int kNormMaxChannels = 16384;

@@ -34,6 +34,7 @@
 #include "common.cuh"
 #include "kernels.h"
 #include "norm.h"
+#include "norm_partial.cuh"
 #include "tc_common.cuh"
 
 namespace disco {
@@ -265,12 +266,17 @@ __device__ __forceinline__ uint8_t* align128(uint8_t* p) {
   return reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(p) + 127) & ~uintptr_t(127));
 }
 
-// Shared memory behind the ring: barriers, gain and bias of every channel, and per group two
-// sums per point of each row of lanes and one row of results.
+// Shared memory behind the ring: barriers, gain and bias of every channel (backward: gain, and per group
+// 2C fp64 sums over points), and per group two sums per point of each row of lanes and one row of results.
 template <typename F>
-constexpr size_t ring_tail(int C) {
-  return 2 * kMaxStages * 8 + 16 * (size_t)C + (size_t)F::G * (F::kRows * F::kSumPitch + F::kPts) * 8;
+constexpr size_t ring_tail(int C, bool bwd) {
+  return 2 * kMaxStages * 8 + (8 + (bwd ? 16 * F::G : 0)) * (size_t)C + (size_t)F::G * (F::kRows * F::kSumPitch + F::kPts) * 8;
 }
+
+// Tiles whose parameter sums a thread adds in fp32 before they go on in fp64.  Going on with every tile
+// took the bf16 backward of 64 channels at 721 x 1440 from 93 to 109 us (conversions), this none; that of
+// 256 channels, one group of warps at a time, 2 x 361 x 720, goes from 173 to 181.
+constexpr int kFlush = 8;
 
 // Bytes by which element `at` of an array at `base` lies past a 16-byte boundary (0 for GRAN 16).
 template <typename F>
@@ -478,17 +484,57 @@ __global__ void __launch_bounds__(kThreads, 1)
   const Ring ring = ring_setup<F>(a, align128(smem_raw));
   float* par = reinterpret_cast<float*>(ring.empty + kMaxStages);
   const T* gain = static_cast<const T*>(a.gain);
+  double* sums = reinterpret_cast<double*>(par + 2 * a.C);  // over points: [group][2C]
   for (int c = threadIdx.x; c < a.C; c += kThreads) par[c] = gain ? to_f32(gain[c]) : 1.0f;
+  for (int i = threadIdx.x; i < G * 2 * a.C; i += kThreads) sums[i] = 0.0;
   __syncthreads();
   const int group = threadIdx.x / F::kGroup, t = threadIdx.x % F::kGroup;
   const int lane = threadIdx.x % LPR, w = t / LPR;  // row of lanes
   fill_ring<F, true>(a, &map_x, &map_d, ring, group, lane, w);
-  float2* red = reinterpret_cast<float2*>(par + 2 * a.C) + group * (kRows * F::kSumPitch + kPts);
+  float2* red = reinterpret_cast<float2*>(sums + G * 2 * a.C) + group * (kRows * F::kSumPitch + kPts);
   float2* fin = red + kRows * F::kSumPitch;
   const float inv_c = 1.0f / (float)a.C;
-  float ag[NC], ab[NC];
+  float ag[NC], ab[NC];  // sums over points of `held` tiles
 #pragma unroll
   for (int i = 0; i < NC; ++i) ag[i] = ab[i] = 0.0f;
+  int held = 0;
+  // The 2 NC sums of a row of lanes are added and spread over its lanes in one go (a lane keeps half of
+  // the values at each step), and each lane adds its own to the group's: no other row has its channels.
+  auto flush = [&]() {
+    float v[2 * NC];
+#pragma unroll
+    for (int j = 0; j < NC; ++j) {
+      v[j] = ag[j];
+      v[NC + j] = ab[j];
+      ag[j] = ab[j] = 0.0f;
+    }
+    int left = 2 * NC, at = 0;
+    bool mine = true;
+#pragma unroll
+    for (int m = LPR / 2; m; m >>= 1) {
+      const bool up = lane & m;
+      if (left > 1) {
+        left /= 2;
+        at += up ? left : 0;
+#pragma unroll
+        for (int i = 0; i < NC; ++i)
+          if (i < left) {
+            const float keep = up ? v[left + i] : v[i], give = up ? v[i] : v[left + i];
+            v[i] = keep + __shfl_xor_sync(~0u, give, m);
+          }
+      } else {
+        v[0] += __shfl_xor_sync(~0u, v[0], m);
+        mine = mine && !up;
+      }
+    }
+#pragma unroll
+    for (int i = 0; i < NC; ++i)
+      if (i < left && mine) {
+        const int c = w + kRows * ((at + i) % NC);
+        if (c < a.C) sums[(group * 2 + (at + i) / NC) * a.C + c] += (double)v[i];
+      }
+    held = 0;
+  };
   // GRAN < 16: the statistics of a tile are fetched while the tile before it is finished
   float mean[2 * NP], rstd[2 * NP];
   auto fetch_stats = [&](long long tile) {
@@ -560,7 +606,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       const int c = w + kRows * j;
       if (F::kFull || c < a.C) {
         const F2 ga = twice(par[c]);
-        F2 tg = pack(ag[j], 0.0f), tb = pack(ab[j], 0.0f);
+        F2 tg = twice(0.0f), tb = twice(0.0f);
 #pragma unroll
         for (int i = 0; i < NP; ++i) {
           const F2 ui = pair_of<F>(u[j], i);
@@ -572,10 +618,11 @@ __global__ void __launch_bounds__(kThreads, 1)
           s2[i] = fma2(e, xh, s2[i]);
         }
         const float2 p = unpack(tg), q = unpack(tb);
-        ag[j] = p.x + p.y;
-        ab[j] = q.x + q.y;
+        ag[j] += p.x + p.y;
+        ab[j] += q.x + q.y;
       }
     }
+    if (a.part && ++held == kFlush) flush();
     if (!F::kTma) fetch_stats(tile + (long long)G * gridDim.x);
     if (!a.out) continue;
 #pragma unroll
@@ -625,29 +672,15 @@ __global__ void __launch_bounds__(kThreads, 1)
   }
   if (F::kTma && !ok) give_up();
   if (!a.part) return;
-  // one row of 2C sums per CTA, its groups added in order; the ring is idle and holds theirs
-  float* sums = reinterpret_cast<float*>(ring.stage);
+  flush();
   __syncthreads();
-#pragma unroll
-  for (int j = 0; j < NC; ++j) {
-    const int c = w + kRows * j;
-    float g = ag[j], d = ab[j];
-#pragma unroll
-    for (int m = LPR / 2; m; m >>= 1) {
-      g += __shfl_xor_sync(~0u, g, m);
-      d += __shfl_xor_sync(~0u, d, m);
-    }
-    if (lane == 0 && c < a.C) {
-      sums[group * 2 * a.C + c] = g;
-      sums[(group * 2 + 1) * a.C + c] = d;
-    }
-  }
-  __syncthreads();
+  // one row of 2C sums per CTA, its groups added in order
+  float* row = a.part + (size_t)blockIdx.x * 4 * a.C;
   for (int i = threadIdx.x; i < 2 * a.C; i += kThreads) {
-    float v = 0.0f;
+    double v = 0.0;
 #pragma unroll
     for (int g = 0; g < G; ++g) v += sums[g * 2 * a.C + i];
-    a.part[(size_t)blockIdx.x * 2 * a.C + i] = v;
+    put_partial(row, a.C, i, v);
   }
 }
 
@@ -690,7 +723,7 @@ bool try_form(Call& call, int least) {
   auto up128 = [](size_t v) { return (v + 127) & ~size_t(127); };
   const size_t array = up128(rows * F::kPitch);
   const size_t stage = up128(array * (call.bwd ? 2 : 1) + (call.bwd && F::kTma ? 8 * F::kPts : 0));
-  const size_t tail = ring_tail<F>(n.C) + 128;
+  const size_t tail = ring_tail<F>(n.C, call.bwd) + 128;
   int stages = (int)std::min<size_t>(kMaxStages, (kRingSmem - tail) / stage);
   // A stage stays with one group, whose warps then wait for each of its phases in order: were it to
   // go from group to group, a fast one could be two phases ahead, which a wait for a parity cannot

@@ -3,7 +3,8 @@
 The norm between two DISCO layers: the field is (B, C, nlat, nlon), as the convolution takes and
 gives it, and every grid point is normalised over its C channels.  Everything runs in libdisco's
 CUDA kernels (there is no CPU path); PyTorch supplies memory, streams and autograd bookkeeping.
-fp32 or bf16, all tensors of a call in one type; statistics and sums are fp32.
+fp32 or bf16, all tensors of a call in one type; statistics and sums over channels are fp32, sums over
+points go on in fp64 after some tiles.
 """
 
 from __future__ import annotations

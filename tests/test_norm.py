@@ -582,3 +582,23 @@ def test_far_from_zero_only_the_mean_is_rounded(shape, offset, cuda):
     dout[(0, slice(None), *at)] = 1.0
     _, dgain, _ = norm.layer_norm_backward(dout, x, stats, None, False, True, False)
     check(dgain, want[(0, slice(None), *at)], tol[(0, slice(None), *at)] + U * xh[(0, slice(None), *at)].abs(), "xh")
+
+
+@gpu
+@pytest.mark.parametrize("shape", [(1, 64, 721, 1440), (1, 64, 721, 1441), (1, 8, 721, 1440), (2, 256, 181, 360), (1, 12, 721, 1441),
+                                   (100000, 16, 7), (4000, 520, 63), (3000, 1500, 9)])
+def test_parameter_sums_over_many_points(shape, cuda):
+    """The same value at every point, so that roundings do not cancel: xh = 1/3 (mean 0, r 1) and dout
+    = 1/3.  In 32 bits are added: 4 points of a tile at most by a thread, 8 tiles at most, and the
+    lanes of a channel (32, of which 3 to 5 additions are one behind the other; 8 lanes where a thread
+    adds 4 points); all that follows is in 64 bits.  With the product's rounding and the result's
+    those are 1 + 3 + 8 + 3 + 1 or 1 + 1 + 8 + 5 + 1, at most 16, each u relative to a sum of equal
+    signs."""
+    third = torch.tensor(1 / 3, device=cuda)
+    x = third.expand(shape).contiguous()
+    stats = torch.zeros((2, shape[0], *shape[2:]), device=cuda)
+    stats[1] = 1.0
+    _, dgain, dbias = norm.layer_norm_backward(x, x, stats, None, False, True, True)
+    n, t = shape[0] * math.prod(shape[2:]), third.double()
+    for got, want, what in ((dgain, n * t * t, "dgain"), (dbias, n * t, "dbias")):
+        check(got, want.expand(shape[1]), 16 * U * want, what)
