@@ -48,9 +48,7 @@ constexpr size_t kRingSmem = 225 * 1024;  // of 227 KB
 struct F2 {
   float x, y;
 };
-__device__ __forceinline__ F2 pack(float a, float b) { return F2{a, b}; }
 __device__ __forceinline__ F2 twice(float a) { return F2{a, a}; }
-__device__ __forceinline__ float2 unpack(F2 a) { return make_float2(a.x, a.y); }
 __device__ __forceinline__ F2 add2(F2 a, F2 b) { return F2{a.x + b.x, a.y + b.y}; }
 __device__ __forceinline__ F2 mul2(F2 a, F2 b) { return F2{a.x * b.x, a.y * b.y}; }
 __device__ __forceinline__ F2 fma2(F2 a, F2 b, F2 c) { return F2{fmaf(a.x, b.x, c.x), fmaf(a.y, b.y, c.y)}; }
@@ -83,7 +81,7 @@ struct Form {
   static constexpr int VEC = VEC_, LPR = LPR_, W = W_, GRAN = GRAN_;
   static constexpr int NC = NC_;  // channels per row of lanes, at most
   static constexpr int kGroup = W * 32, G = kThreads / kGroup;
-  static constexpr int kPts = LPR * VEC, NP = (VEC + 1) / 2;
+  static constexpr int kPts = LPR * VEC, NP = VEC / 2;
   static constexpr int kRows = W * (32 / LPR);
   static constexpr bool kTma = GRAN == 16, kFull = FULL_;
   using Filled = Form<T_, VEC_, LPR_, W_, NC_, GRAN_, true>;
@@ -94,7 +92,7 @@ struct Form {
   // the sums of a point are joined by kJoin lanes; rows of sums are kSumPitch apart, which keeps
   // those lanes on different banks
   static constexpr int kJoin = kGroup > kPts ? kGroup / kPts : 1, kSumPitch = kPts + (kJoin < 16 ? 16 / kJoin : 1);
-  static_assert(VEC % kRun == 0 && kJoin <= 32 && kRows % kJoin == 0 && kPts % (kGroup / kJoin) == 0, "shape");
+  static_assert(VEC % 2 == 0 && VEC % kRun == 0 && kJoin <= 32 && kRows % kJoin == 0 && kPts % (kGroup / kJoin) == 0, "shape");
   // the tile's point that value e of a lane is
   static __device__ __forceinline__ int point(int lane, int e) {
     return (lane + LPR * (e / kRun)) * kRun + e % kRun;
@@ -131,9 +129,8 @@ __device__ __forceinline__ void read_row(const uint8_t* row, int lane, uint32_t 
 // Pair k of a lane's values.
 template <typename F>
 __device__ __forceinline__ F2 pair_of(const uint32_t (&v)[F::kWords], int k) {
-  if constexpr (sizeof(typename F::T) == 2) return pack(__uint_as_float(v[k] << 16), __uint_as_float(v[k] & 0xffff0000u));
-  else if constexpr (F::VEC == 1) return pack(__uint_as_float(v[0]), 0.0f);
-  else return pack(__uint_as_float(v[2 * k]), __uint_as_float(v[2 * k + 1]));
+  if constexpr (sizeof(typename F::T) == 2) return F2{__uint_as_float(v[k] << 16), __uint_as_float(v[k] & 0xffff0000u)};
+  else return F2{__uint_as_float(v[2 * k]), __uint_as_float(v[2 * k + 1])};
 }
 
 template <typename F>
@@ -143,13 +140,13 @@ __device__ __forceinline__ void write_row(typename F::T* dst, int lane, int vali
   uint32_t w[F::kWords];
 #pragma unroll
   for (int k = 0; k < F::NP; ++k) {
-    const float2 q = unpack(v[k]);
+    const F2 q = v[k];
     if constexpr (sizeof(T) == 2) {
       const __nv_bfloat162 h = __floats2bfloat162_rn(q.x, q.y);
       w[k] = *reinterpret_cast<const uint32_t*>(&h);
     } else {
       w[2 * k] = __float_as_uint(q.x);
-      if constexpr (F::VEC > 1) w[2 * k + 1] = __float_as_uint(q.y);
+      w[2 * k + 1] = __float_as_uint(q.y);
     }
   }
 #pragma unroll
@@ -268,9 +265,9 @@ __device__ __forceinline__ uint8_t* align128(uint8_t* p) {
 
 // Shared memory behind the ring: barriers, gain and bias of every channel (backward: gain, and per group
 // 2C fp64 sums over points), and per group two sums per point of each row of lanes and one row of results.
-template <typename F>
-constexpr size_t ring_tail(int C, bool bwd) {
-  return 2 * kMaxStages * 8 + (8 + (bwd ? 16 * F::G : 0)) * (size_t)C + (size_t)F::G * (F::kRows * F::kSumPitch + F::kPts) * 8;
+template <typename F, bool BWD>
+constexpr size_t ring_tail(int C) {
+  return 2 * kMaxStages * 8 + (8 + (BWD ? 16 * F::G : 0)) * (size_t)C + (size_t)F::G * (F::kRows * F::kSumPitch + F::kPts) * 8;
 }
 
 // Tiles whose parameter sums a thread adds in fp32 before they go on in fp64.  Going on with every tile
@@ -368,7 +365,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     uint32_t raw[NC][F::kWords];
     F2 s[NP], q[NP], first[NP];
 #pragma unroll
-    for (int i = 0; i < NP; ++i) s[i] = q[i] = first[i] = pack(0.0f, 0.0f);
+    for (int i = 0; i < NP; ++i) s[i] = q[i] = first[i] = F2{0.0f, 0.0f};
 #pragma unroll
     for (int j = 0; j < NC; ++j) {
       const int c = w + kRows * j;
@@ -395,9 +392,9 @@ __global__ void __launch_bounds__(kThreads, 1)
     for (int i = 0; i < NP; ++i) {
       const F2 mean = fma2(s[i], twice(inv_own), neg2(first[i]));  // of the row's channels
       const F2 m2 = fma2(mul2(s[i], twice(-inv_own)), s[i], q[i]);
-      const float2 mv = unpack(mean), qv = unpack(m2);
+      const F2 mv = mean, qv = m2;
       red[w * F::kSumPitch + 2 * i * LPR + lane] = make_float2(mv.x, qv.x);
-      if (2 * i + 1 < VEC) red[w * F::kSumPitch + (2 * i + 1) * LPR + lane] = make_float2(mv.y, qv.y);
+      red[w * F::kSumPitch + (2 * i + 1) * LPR + lane] = make_float2(mv.y, qv.y);
     }
     group_sync<F>(group);
 #pragma unroll
@@ -425,23 +422,23 @@ __global__ void __launch_bounds__(kThreads, 1)
     group_sync<F>(group);
     F2 nm[NP], rr[NP];  // -mean, r
     {
-      float mean[2 * NP], r[2 * NP];
+      float mean[VEC], r[VEC];
 #pragma unroll
-      for (int e = 0; e < 2 * NP; ++e) {
-        const float2 f = e < VEC ? fin[e * LPR + lane] : make_float2(0.0f, 0.0f);
+      for (int e = 0; e < VEC; ++e) {
+        const float2 f = fin[e * LPR + lane];
         mean[e] = f.x;
         r[e] = f.y;
       }
 #pragma unroll
       for (int i = 0; i < NP; ++i) {
-        rr[i] = pack(r[2 * i], r[2 * i + 1]);
-        nm[i] = pack(-mean[2 * i], -mean[2 * i + 1]);
+        rr[i] = F2{r[2 * i], r[2 * i + 1]};
+        nm[i] = F2{-mean[2 * i], -mean[2 * i + 1]};
       }
       for (int which = w; a.stats && which < 2; which += kRows) {
         float* dst = a.stats + ((size_t)which * a.B + tl.b) * a.npts + tl.p0;
-        float v[2 * NP];
+        float v[VEC];
 #pragma unroll
-        for (int e = 0; e < 2 * NP; ++e) v[e] = which == 0 ? mean[e] : r[e];
+        for (int e = 0; e < VEC; ++e) v[e] = which == 0 ? mean[e] : r[e];
         if constexpr (F::kTma) {  // planes are whole vectors long
           if (lane * VEC < tl.valid) {
 #pragma unroll
@@ -536,13 +533,13 @@ __global__ void __launch_bounds__(kThreads, 1)
     held = 0;
   };
   // GRAN < 16: the statistics of a tile are fetched while the tile before it is finished
-  float mean[2 * NP], rstd[2 * NP];
+  float mean[VEC], rstd[VEC];
   auto fetch_stats = [&](long long tile) {
     const Tile tl = tile_of<F>(a, tile);
     const float* p = a.stats_in + (size_t)tl.b * a.npts + tl.p0;
 #pragma unroll
-    for (int e = 0; e < 2 * NP; ++e) {
-      const bool in = tile < a.tiles && e < VEC && F::point(lane, e) < tl.valid;
+    for (int e = 0; e < VEC; ++e) {
+      const bool in = tile < a.tiles && F::point(lane, e) < tl.valid;
       mean[e] = in ? p[F::point(lane, e)] : 0.0f;
       rstd[e] = in ? p[(size_t)a.B * a.npts + F::point(lane, e)] : 0.0f;
     }
@@ -575,9 +572,9 @@ __global__ void __launch_bounds__(kThreads, 1)
     F2 rr[NP], nm[NP], s1[NP], s2[NP];
 #pragma unroll
     for (int i = 0; i < NP; ++i) {
-      rr[i] = pack(rstd[2 * i], rstd[2 * i + 1]);
-      nm[i] = pack(-mean[2 * i], -mean[2 * i + 1]);
-      s1[i] = s2[i] = pack(0.0f, 0.0f);
+      rr[i] = F2{rstd[2 * i], rstd[2 * i + 1]};
+      nm[i] = F2{-mean[2 * i], -mean[2 * i + 1]};
+      s1[i] = s2[i] = F2{0.0f, 0.0f};
     }
     uint32_t x[NC][F::kWords], u[NC][F::kWords];
 #pragma unroll
@@ -617,7 +614,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           s1[i] = add2(s1[i], e);
           s2[i] = fma2(e, xh, s2[i]);
         }
-        const float2 p = unpack(tg), q = unpack(tb);
+        const F2 p = tg, q = tb;
         ag[j] += p.x + p.y;
         ab[j] += q.x + q.y;
       }
@@ -627,9 +624,9 @@ __global__ void __launch_bounds__(kThreads, 1)
     if (!a.out) continue;
 #pragma unroll
     for (int i = 0; i < NP; ++i) {
-      const float2 p = unpack(s1[i]), q = unpack(s2[i]);
+      const F2 p = s1[i], q = s2[i];
       red[w * F::kSumPitch + 2 * i * LPR + lane] = make_float2(p.x, q.x);
-      if (2 * i + 1 < VEC) red[w * F::kSumPitch + (2 * i + 1) * LPR + lane] = make_float2(p.y, q.y);
+      red[w * F::kSumPitch + (2 * i + 1) * LPR + lane] = make_float2(p.y, q.y);
     }
     group_sync<F>(group);
 #pragma unroll
@@ -650,9 +647,9 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
     for (int i = 0; i < NP; ++i) {
       const float2 p = fin[2 * i * LPR + lane];
-      const float2 q = 2 * i + 1 < VEC ? fin[(2 * i + 1) * LPR + lane] : make_float2(0.0f, 0.0f);
-      s1[i] = pack(-p.x, -q.x);
-      s2[i] = pack(-p.y, -q.y);
+      const float2 q = fin[(2 * i + 1) * LPR + lane];
+      s1[i] = F2{-p.x, -q.x};
+      s2[i] = F2{-p.y, -q.y};
     }
     T* out = static_cast<T*>(a.out) + tl.at;
 #pragma unroll
@@ -701,7 +698,6 @@ bool field_map(CUtensorMap* m, bool bf16, const void* base, const RingArgs& a, i
 // What a call has chosen so far, and what it left to report.
 struct Call {
   NormArgs n;
-  bool bwd;
   int sms;
   cudaStream_t st;
   int rows = 0;
@@ -710,7 +706,7 @@ struct Call {
 
 // Runs form F if its tiles fit: NC channels per row of lanes, three stages (two per group where
 // rows are copied by their own lanes); `least` tiles per SM, or the caller tries a narrower form.
-template <typename F>
+template <typename F, bool BWD>
 bool try_form(Call& call, int least) {
   using T = typename F::T;
   const NormArgs& n = call.n;
@@ -722,8 +718,8 @@ bool try_form(Call& call, int least) {
   const size_t rows = F::kTma ? (size_t)a.boxes * a.box_rows : n.C;
   auto up128 = [](size_t v) { return (v + 127) & ~size_t(127); };
   const size_t array = up128(rows * F::kPitch);
-  const size_t stage = up128(array * (call.bwd ? 2 : 1) + (call.bwd && F::kTma ? 8 * F::kPts : 0));
-  const size_t tail = ring_tail<F>(n.C, call.bwd) + 128;
+  const size_t stage = up128(array * (BWD ? 2 : 1) + (BWD && F::kTma ? 8 * F::kPts : 0));
+  const size_t tail = ring_tail<F, BWD>(n.C) + 128;
   int stages = (int)std::min<size_t>(kMaxStages, (kRingSmem - tail) / stage);
   // A stage stays with one group, whose warps then wait for each of its phases in order: were it to
   // go from group to group, a fast one could be two phases ahead, which a wait for a parity cannot
@@ -746,7 +742,7 @@ bool try_form(Call& call, int least) {
   a.gain = n.gain;
   a.bias = n.bias;
   a.eps = n.eps;
-  a.out = call.bwd ? n.dx : n.out;
+  a.out = BWD ? n.dx : n.out;
   a.stats = n.stats;
   a.stats_in = n.stats;
   a.part = n.dgain || n.dbias ? n.part : nullptr;
@@ -755,7 +751,7 @@ bool try_form(Call& call, int least) {
   const bool bf16 = sizeof(T) == 2;
   call.rows = grid;
   CUtensorMap mx{}, md{};
-  if (F::kTma && (!field_map(&mx, bf16, n.x, a, F::kPts) || (call.bwd && !field_map(&md, bf16, n.dout, a, F::kPts)))) {
+  if (F::kTma && (!field_map(&mx, bf16, n.x, a, F::kPts) || (BWD && !field_map(&md, bf16, n.dout, a, F::kPts)))) {
     call.err = cudaErrorInvalidValue;
     return true;
   }
@@ -767,42 +763,51 @@ bool try_form(Call& call, int least) {
     count_launch();
     return cudaGetLastError();
   };
+  auto launch = [&](auto form) {
+    using G = decltype(form);
+    if constexpr (BWD) return run(norm_ring_bwd_kernel<G>, mx, md);
+    else return run(norm_ring_fwd_kernel<G>, mx);
+  };
   if constexpr (F::kTma) {
     if (n.C == F::kRows * F::NC) {
-      call.err = call.bwd ? run(norm_ring_bwd_kernel<typename F::Filled>, mx, md)
-                          : run(norm_ring_fwd_kernel<typename F::Filled>, mx);
+      call.err = launch(typename F::Filled{});
       return true;
     }
   }
-  call.err = call.bwd ? run(norm_ring_bwd_kernel<F>, mx, md) : run(norm_ring_fwd_kernel<F>, mx);
+  call.err = launch(F{});
   return true;
 }
 
 // The forms of either pass, few channels first.  A form has at most 32 registers of packed values;
 // of those that hold the channels the first ones have the longer rows (runs of HBM) and the
 // smaller groups (cheaper barriers).
-template <typename T, int GRAN>
+template <typename T, int GRAN, bool BWD>
 bool run_forms(Call& c) {
   constexpr int v16 = 16 / (int)sizeof(T), v8 = 8 / (int)sizeof(T);
   for (int least = 2; least >= 0; least -= 2) {
-    if (!c.bwd) {
-      if (least && (try_form<Form<T, v16, 32, 1, 8, GRAN>>(c, least) || try_form<Form<T, v16, 16, 1, 8, GRAN>>(c, least) ||
-                    try_form<Form<T, v16, 16, 2, 8, GRAN>>(c, least) || try_form<Form<T, v16, 16, 4, 8, GRAN>>(c, least) ||
-                    try_form<Form<T, v16, 16, 8, 8, GRAN>>(c, least)))
+    if constexpr (!BWD) {
+      if (least && (try_form<Form<T, v16, 32, 1, 8, GRAN>, BWD>(c, least) || try_form<Form<T, v16, 16, 1, 8, GRAN>, BWD>(c, least) ||
+                    try_form<Form<T, v16, 16, 2, 8, GRAN>, BWD>(c, least) || try_form<Form<T, v16, 16, 4, 8, GRAN>, BWD>(c, least) ||
+                    try_form<Form<T, v16, 16, 8, 8, GRAN>, BWD>(c, least)))
         return true;
-      if (try_form<Form<T, v8, 16, 8, 4, GRAN>>(c, least) || try_form<Form<T, v8, 16, 8, 16, GRAN>>(c, least) ||
-          try_form<Form<T, v8, 16, 16, 16, GRAN>>(c, least) || try_form<Form<T, v8, 8, 16, 16, GRAN>>(c, least))
+      if (try_form<Form<T, v8, 16, 8, 4, GRAN>, BWD>(c, least) || try_form<Form<T, v8, 16, 8, 16, GRAN>, BWD>(c, least) ||
+          try_form<Form<T, v8, 16, 16, 16, GRAN>, BWD>(c, least) || try_form<Form<T, v8, 8, 16, 16, GRAN>, BWD>(c, least))
         return true;
     } else {
-      if (least && (try_form<Form<T, v8, 32, 1, 8, GRAN>>(c, least) || try_form<Form<T, v8, 16, 1, 8, GRAN>>(c, least) ||
-                    try_form<Form<T, v8, 16, 2, 8, GRAN>>(c, least) || try_form<Form<T, v8, 16, 4, 8, GRAN>>(c, least)))
+      if (least && (try_form<Form<T, v8, 32, 1, 8, GRAN>, BWD>(c, least) || try_form<Form<T, v8, 16, 1, 8, GRAN>, BWD>(c, least) ||
+                    try_form<Form<T, v8, 16, 2, 8, GRAN>, BWD>(c, least) || try_form<Form<T, v8, 16, 4, 8, GRAN>, BWD>(c, least)))
         return true;
-      if (try_form<Form<T, v8, 16, 8, 4, GRAN>>(c, least) || try_form<Form<T, v8, 16, 8, 8, GRAN>>(c, least) ||
-          try_form<Form<T, v8, 16, 16, 8, GRAN>>(c, least) || try_form<Form<T, v8, 8, 16, 8, GRAN>>(c, least))
+      if (try_form<Form<T, v8, 16, 8, 4, GRAN>, BWD>(c, least) || try_form<Form<T, v8, 16, 8, 8, GRAN>, BWD>(c, least) ||
+          try_form<Form<T, v8, 16, 16, 8, GRAN>, BWD>(c, least) || try_form<Form<T, v8, 8, 16, 8, GRAN>, BWD>(c, least))
         return true;
     }
   }
   return false;
+}
+
+template <typename T, int GRAN>
+bool run_pass(Call& c, bool bwd) {
+  return bwd ? run_forms<T, GRAN, true>(c) : run_forms<T, GRAN, false>(c);
 }
 
 // The widest of 16, 4 and 2 bytes that every plane starts on.
@@ -818,11 +823,15 @@ int granule(const NormArgs& n, int es) {
 
 bool launch_norm_ring(bool bf16, const NormArgs& n, bool bwd, int sms, cudaStream_t st, int* rows, cudaError_t* err) {
   if (n.npts < 64) return false;
-  Call c{n, bwd, sms, st};
+  Call c{n, sms, st};
   const int gran = granule(n, bf16 ? 2 : 4);
   bool ran;
-  if (bf16) ran = gran == 16 ? run_forms<__nv_bfloat16, 16>(c) : gran == 4 ? run_forms<__nv_bfloat16, 4>(c) : run_forms<__nv_bfloat16, 2>(c);
-  else ran = gran == 16 ? run_forms<float, 16>(c) : run_forms<float, 4>(c);
+  if (bf16) {
+    ran = gran == 16 ? run_pass<__nv_bfloat16, 16>(c, bwd)
+          : gran == 4 ? run_pass<__nv_bfloat16, 4>(c, bwd) : run_pass<__nv_bfloat16, 2>(c, bwd);
+  } else {
+    ran = gran == 16 ? run_pass<float, 16>(c, bwd) : run_pass<float, 4>(c, bwd);
+  }
   *rows = c.rows;
   *err = c.err;
   return ran;
