@@ -30,8 +30,15 @@ def _sizes(x):
 def layer_norm(x: torch.Tensor, gain=None, bias=None, eps: float = 1e-5):
     """(out, stats) of x (B, C, *points): out = gain * (x - mean) * r + bias with mean and r =
     1 / sqrt(var + eps) over the channels of each point; stats (2, B, *points) holds mean and r in
-    fp32, which layer_norm_backward takes.  gain and bias are (C,), in x's type, or None.  Autograd
-    does not see this call; LayerNormS2 has the gradients."""
+    fp32, which layer_norm_backward takes.  gain and bias are (C,), in x's type, or None.  out has
+    gradients where autograd records and x, gain or bias asks for them; stats has none."""
+    if torch.is_grad_enabled() and (x.requires_grad or (gain is not None and gain.requires_grad)
+                                    or (bias is not None and bias.requires_grad)):
+        return _LayerNormFn.apply(x, gain, bias, eps)
+    return _forward(x, gain, bias, eps)
+
+
+def _forward(x, gain, bias, eps):
     code = dense(x, "x")
     B, C, n = _sizes(x)
     gain = like(gain, x, (C,), "gain")
@@ -71,15 +78,14 @@ def layer_norm_backward(dout: torch.Tensor, x: torch.Tensor, stats: torch.Tensor
 class _LayerNormFn(torch.autograd.Function):
     @staticmethod
     def forward(ctx, x, gain, bias, eps):
-        x = x.contiguous()
-        gain = None if gain is None else gain.contiguous()
-        out, stats = layer_norm(x, gain, None if bias is None else bias.contiguous(), eps)
+        out, stats = _forward(x, gain, bias, eps)
         ctx.save_for_backward(x, stats, gain)
-        return out
+        ctx.mark_non_differentiable(stats)
+        return out, stats
 
     @staticmethod
     @torch.autograd.function.once_differentiable
-    def backward(ctx, dout):
+    def backward(ctx, dout, _):
         x, stats, gain = ctx.saved_tensors
         need = ctx.needs_input_grad
         return (*layer_norm_backward(dout.contiguous(), x, stats, gain, need[0], need[1], need[2]), None)
@@ -104,4 +110,5 @@ class LayerNormS2(torch.nn.Module):
     def forward(self, x):
         if x.dim() < 2 or x.shape[1] != self.channels:
             raise ValueError(f"x has shape {tuple(x.shape)}, expected (B, {self.channels}, *points)")
-        return _LayerNormFn.apply(x, self.weight, self.bias, self.eps)
+        gain, bias = (None if p is None else p.contiguous() for p in (self.weight, self.bias))
+        return _LayerNormFn.apply(x.contiguous(), gain, bias, self.eps)[0]

@@ -602,3 +602,29 @@ def test_parameter_sums_over_many_points(shape, cuda):
     n, t = shape[0] * math.prod(shape[2:]), third.double()
     for got, want, what in ((dgain, n * t * t, "dgain"), (dbias, n * t, "dbias")):
         check(got, want.expand(shape[1]), 16 * U * want, what)
+
+
+@gpu
+@pytest.mark.parametrize("which", [(1, 1, 1), (0, 1, 0), (0, 0, 1), (1, 0, 0)])
+def test_the_function_has_the_module_s_gradients(which, cuda):
+    m = norm.LayerNormS2(10, device=cuda)
+    with torch.no_grad():
+        m.weight.add_(0.3 * torch.randn(10, device=cuda))
+    x, v = field((2, 10, 6, 9), F32, 65, cuda), field((2, 10, 6, 9), F32, 66, cuda)
+    a = x.clone().requires_grad_()
+    m(a).backward(v)
+    want = [a.grad, m.weight.grad, m.bias.grad]
+    leaves = [t.detach().clone().requires_grad_(bool(w)) for t, w in zip((x, m.weight, m.bias), which)]
+    out, stats = norm.layer_norm(*leaves, eps=m.eps)
+    assert out.requires_grad and not stats.requires_grad
+    out.backward(v)
+    for t, w, g in zip(leaves, which, want):
+        assert (t.grad is None) != bool(w)
+        assert not w or torch.equal(t.grad, g)
+    with torch.no_grad():
+        assert not norm.layer_norm(*leaves, eps=m.eps)[0].requires_grad
+    assert not norm.layer_norm(x)[0].requires_grad
+    with pytest.raises(ValueError):
+        norm.layer_norm(leaves[0].transpose(2, 3).requires_grad_() if not which[0] else leaves[0].transpose(2, 3), *leaves[1:])
+    with pytest.raises(RuntimeError):
+        torch.autograd.grad(torch.autograd.grad(norm.layer_norm(a)[0].square().sum(), a, create_graph=True)[0].sum(), a)
