@@ -71,10 +71,8 @@ def _workspace(x, n, groups, rows, cols):
 
 
 def _outputs(x, n, dtype=None):
-    """n tensors like x; those of a list share one allocation where they stay on 16 bytes in it."""
-    dtype = dtype or x.dtype
-    if n > 1 and x.numel() * dtype.itemsize % 16 == 0:
-        return list(x.new_empty((n, *x.shape), dtype=dtype).unbind(0))
+    """n tensors like x, each with memory of its own: views of one allocation would share a version
+    counter, and an in-place change of one would spoil what autograd saved of the others."""
     return [x.new_empty(x.shape, dtype=dtype) for _ in range(n)]
 
 

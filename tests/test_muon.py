@@ -506,3 +506,34 @@ def test_a_block_trains_with_norm_and_update(dtype, fused, cuda):
     opt.step()
     assert torch.equal(c1.weight.detach(), want[0]) and torch.equal(c2.weight.detach(), want[1])
     assert torch.isfinite(c2(ln(c1(x)))).all()
+
+
+def _independent(outs):
+    """Results share neither memory nor a version: one changed in place leaves what autograd saved of
+    another, and one kept or saved holds no memory of the others."""
+    assert len({o.untyped_storage().data_ptr() for o in outs}) == len(outs)
+    assert all(o.untyped_storage().nbytes() == o.numel() * o.element_size() for o in outs)
+    w = outs[1].detach().requires_grad_()
+    y = (w * outs[0]).sum()
+    for o in outs[1:]:
+        before = outs[0]._version
+        with torch.no_grad():
+            o.add_(1)
+        assert outs[0]._version == before
+    y.backward()
+
+
+@pytest.mark.parametrize("shape", [(4, 6), (4, 8, 3), (3, 5)])
+@pytest.mark.parametrize("dtype", [F32, BF16])
+def test_results_of_a_list_are_independent(shape, dtype):
+    _independent(muon._outputs(torch.zeros(shape, dtype=dtype), 4))
+
+
+@gpu
+@pytest.mark.parametrize("shape", [(4, 8, 3), (3, 5), (64, 64)])
+def test_results_of_calls_are_independent(shape, cuda):
+    us = [update(shape, F32, 70 + i, cuda) for i in range(3)]
+    _independent(muon.orthogonalize(us))
+    ws, ms = muon.muon_update(us, us, [u.clone() for u in us], 0.1)
+    _independent(ws)
+    _independent(ms)
