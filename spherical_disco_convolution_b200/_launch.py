@@ -8,8 +8,6 @@ import torch
 from . import disco as D
 
 DTYPES = {torch.float32: D.DISCO_F32, torch.bfloat16: D.DISCO_BF16}
-_device = torch._C._cuda_getDevice
-_raw_stream = torch._C._cuda_getCurrentRawStream
 
 
 def dense(t: torch.Tensor, what: str) -> int:
@@ -39,9 +37,11 @@ def like(t, x: torch.Tensor, shape, what: str):
 
 def launch(x: torch.Tensor, fn, *args) -> None:
     """fn(*args, stream) with x's device current, on that device's current stream."""
+    # looked up here, since a torch without CUDA has neither (and then no x comes this far)
+    device, stream = torch._C._cuda_getDevice, torch._C._cuda_getCurrentRawStream
     index = x.get_device()
-    if index == _device():
-        fn(*args, _raw_stream(index))
+    if index == device():
+        fn(*args, stream(index))
     else:
         with torch.cuda.device(index):
-            fn(*args, _raw_stream(index))
+            fn(*args, stream(index))
