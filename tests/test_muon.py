@@ -537,3 +537,84 @@ def test_results_of_calls_are_independent(shape, cuda):
     ws, ms = muon.muon_update(us, us, [u.clone() for u in us], 0.1)
     _independent(ws)
     _independent(ms)
+
+
+# ------------------------------------------------------------------ every form of the tiled products
+#
+# What each reaches (tiles of 128 or 256 rows; S parts of K for X X^T / A A / B X):
+#   (1024, 1024, 9), (9216, 1024)  256, on pairs, with partial sums: 7 / 4 / 1, the second one transposed
+#   (1200, 70, 60) in 4 groups, (1000, 4501), (4610, 1000)  256, padded, rows off 16 bytes, transposed
+#   (512, 512, 9), (512, 1000), (512, 2000)   128: 8 / 8 / 1, 8 / 8 / 4 and 8 / 8 / 2
+#   (400, 500), (500, 400)                    128: 8 / 8 / 8, the second one's store transposed
+#   (1000, 512)                               128: the transposed store of a cluster of 4
+# and sides of at most 32 that are too long for the fp32 form: (32, 4608), (24, 12000) on 64-row and
+# 128-row tiles, (32, 9216), (6000, 20), (8, 20000).
+TILED = [((1024, 1024, 9), 1), ((9216, 1024), 1), ((1200, 70, 60), 4), ((1000, 4501), 1), ((4610, 1000), 1), ((512, 512, 9), 1),
+         ((512, 1000), 1), ((512, 2000), 1), ((400, 500), 1), ((500, 400), 1), ((1000, 512), 1), ((32, 4608), 1), ((24, 12000), 1),
+         ((32, 9216), 1), ((6000, 20), 1), ((8, 20000), 1)]
+
+
+@gpu
+@pytest.mark.parametrize("dtype", [F32, BF16])
+@pytest.mark.parametrize("shape,groups", TILED)
+def test_tiled_forms_match_the_definition(shape, groups, dtype, cuda):
+    u = update(shape, dtype, 80, cuda)
+    want, tol = oracle(u, groups)
+    got = muon.orthogonalize(u, groups)
+    check(got, want, tol, dtype, groups, f"{shape}")
+    assert torch.equal(muon.orthogonalize(u, groups), got)
+
+
+@gpu
+@pytest.mark.parametrize("dtype", [F32, BF16])
+@pytest.mark.parametrize("shape,groups", [((1024, 512, 9), 1), ((4610, 1000), 1), ((1200, 70, 60), 4), ((512, 1000), 1),
+                                          ((500, 400), 1), ((32, 9216), 1), ((6000, 20), 1), ((300, 513), 1)])
+def test_tiled_steps_in_place(shape, groups, dtype, cuda):
+    lr, mom, wd = 0.05, 0.9, 0.1
+    w = torch.randn(shape, device=cuda).to(dtype)
+    g, m = update(shape, dtype, 81, cuda), update(shape, F32, 82, cuda)
+    w0, m0 = w.clone(), m.clone()
+    w1, m1 = muon.muon_update(w, g, m, lr, mom, True, wd, groups)
+    assert torch.equal(w, w0) and torch.equal(m, m0)
+    md = mom * m.double() + g.double()
+    assert ((m1.double() - md).abs() <= 2.0 ** -23 * (m.double().abs() + g.double().abs())).all()
+    want, tol = oracle(g.double() + mom * md, groups)
+    rate = lr * math.sqrt(max(1.0, shape[0] / groups / math.prod(shape[1:])))
+    step = (1 - lr * wd) * matrices(w, groups) - rate * want
+    check(w1, step, 2 * rate * tol + 2.0 ** -22 * torch.linalg.matrix_norm(matrices(w, groups)), dtype, groups, "w'")
+    muon.muon_update(w, g, m, lr, mom, True, wd, groups, inplace=True)
+    assert torch.equal(w, w1) and torch.equal(m, m1)
+
+
+@gpu
+@pytest.mark.parametrize("count,shape", [(8, (300, 70, 60)), (70, (200, 700)), (79, (200, 700)), (66, (300, 513)), (65, (140, 260)), (130, (150, 40))])
+def test_many_tensors_in_tiled_forms(count, shape, cuda):
+    """Several sets of 64 tensors through one workspace of the exact size, the last set on tiles and
+    splits of its own; what lies behind workspace and results stays as it was."""
+    us = [update(shape, F32, 83 + i, cuda) for i in range(count)]
+    n = math.prod(shape)
+    rows, cols = shape[0], n // shape[0]
+    nb = D.disco_orthogonalize_workspace_size(count, 1, rows, cols)
+    ws = torch.full((nb + 4096,), 0xff, dtype=torch.uint8, device=cuda)  # NaN in every type
+    outs = [torch.full((n + 8,), 5.0, device=cuda) for _ in us]
+    D.disco_orthogonalize(1, rows, cols, D.DISCO_F32, D.newton_schulz(5, NS, 1e-7), [u.data_ptr() for u in us],
+                          [o.data_ptr() for o in outs], ws.data_ptr() if nb else None, nb, torch.cuda.current_stream().cuda_stream)
+    assert (ws[nb:] == 0xff).all()
+    for u, o in zip(us, outs):
+        assert (o[n:] == 5).all()
+        want, tol = oracle(u)
+        check(o[:n].view(shape), want, tol, F32, 1, "one of many")
+    assert all(torch.equal(a, o[:n].view(shape)) for a, o in zip(muon.orthogonalize(us), outs))
+
+
+@gpu
+@pytest.mark.parametrize("shape,groups", [((1200, 70, 60), 4), ((512, 1000), 1), ((24, 12000), 1)])
+def test_bad_values_spread_over_their_own_matrix_only(shape, groups, cuda):
+    us = [update(shape, F32, 90 + i, cuda) for i in range(2)]
+    want = muon.orthogonalize(us, groups)
+    bad = [us[0], us[1].clone()]
+    bad[1][1, 2] = math.nan
+    got = muon.orthogonalize(bad, groups)
+    assert torch.equal(got[0], want[0]) and torch.isnan(got[1]).any()
+    rows = shape[0] // groups
+    assert torch.equal(got[1][rows:], want[1][rows:])

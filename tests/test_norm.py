@@ -628,3 +628,97 @@ def test_the_function_has_the_module_s_gradients(which, cuda):
         norm.layer_norm(leaves[0].transpose(2, 3).requires_grad_() if not which[0] else leaves[0].transpose(2, 3), *leaves[1:])
     with pytest.raises(RuntimeError):
         torch.autograd.grad(torch.autograd.grad(norm.layer_norm(a)[0].square().sum(), a, create_graph=True)[0].sum(), a)
+
+
+LONG = [s for s in FORMS if math.prod(s[2:]) >= 64]
+
+
+@gpu
+@pytest.mark.parametrize("bad", [math.nan, math.inf, -math.inf])
+@pytest.mark.parametrize("dtype", [F32, BF16])
+@pytest.mark.parametrize("shape", LONG)
+def test_bad_points_of_long_planes_stay_their_own(shape, dtype, bad, cuda):
+    x, dout = field(shape, dtype, 67, cuda), field(shape, dtype, 68, cuda)
+    B, C, n = shape[0], shape[1], math.prod(shape[2:])
+    y, e = x.clone().view(B, C, n), dout.clone().view(B, C, n)
+    hit = torch.zeros(B, 1, n, dtype=torch.bool, device=cuda)
+    for b, c, p in [(0, 0, 5), (B - 1, C - 1, n - 1), (B - 1, C // 2, n // 2 + 1)]:
+        y[b, c, p] = bad
+        e[b, C - 1 - c, (p + 17) % n] = bad
+        hit[b, 0, p] = hit[b, 0, (p + 17) % n] = True
+    hit = hit.expand(B, C, n).reshape(shape)
+    y, e = y.view(shape), e.view(shape)
+    a, sa = norm.layer_norm(x)
+    b, sb = norm.layer_norm(y)
+    assert torch.equal(a[~hit], b[~hit])
+    assert torch.isnan(b.view(B, C, n)[B - 1, :, n - 1]).any()
+    da = norm.layer_norm_backward(dout, x, sa)[0]
+    db = norm.layer_norm_backward(e, y, sb)[0]
+    assert torch.equal(da[~hit], db[~hit])
+
+
+@gpu
+@pytest.mark.parametrize("dtype", [F32, BF16])
+@pytest.mark.parametrize("shift", [0, 1, 2, 3, 4, 8])
+@pytest.mark.parametrize("shape", LONG)
+def test_any_base_guards_and_overlap(shape, shift, dtype, cuda):
+    """Tensors at any element of an allocation, results between guards, workspace at its exact size;
+    then in place, the input's gradient over dout, and over x."""
+    B, C, n = shape[0], shape[1], math.prod(shape[2:])
+    N, code, es = B * C * n, D.DISCO_F32 if dtype == F32 else D.DISCO_BF16, dtype.itemsize
+    st = torch.cuda.current_stream().cuda_stream
+    bufs = []
+
+    def place(count, k, t=dtype, values=None):
+        buf = torch.full((count + 64,), 7, dtype=t, device=cuda)
+        v = buf[16 + k:16 + k + count]
+        if values is not None:
+            v.copy_(values.reshape(-1))
+        bufs.append((buf, 16 + k, count))
+        return v
+
+    def guarded():
+        return all((b[:o] == 7).all() and (b[o + c:] == 7).all() for b, o, c in bufs)
+
+    x, dout = field(shape, dtype, 69, cuda), field(shape, dtype, 70, cuda)
+    gain, bias = field((1, C), dtype, 71, cuda)[0], field((1, C), dtype, 72, cuda)[0]
+    xs, ds = place(N, shift, values=x), place(N, (shift + 3) % 8, values=dout)
+    ga, bi = place(C, 1, values=gain), place(C, 2, values=bias)
+    out, dx, dg, db = place(N, (shift + 1) % 8), place(N, (shift + 2) % 8), place(C, 3), place(C, 1)
+    stats = place(2 * B * n, shift, F32)
+    nb = D.disco_norm_workspace_size(B, C, n, code)
+    ws = place(nb // 4, 1, F32)
+    D.disco_norm(B, C, n, code, xs.data_ptr(), ga.data_ptr(), bi.data_ptr(), 1e-5, out.data_ptr(), stats.data_ptr(), st)
+    D.disco_norm_backward(B, C, n, code, ds.data_ptr(), xs.data_ptr(), stats.data_ptr(), ga.data_ptr(), dx.data_ptr(),
+                          dg.data_ptr(), db.data_ptr(), ws.data_ptr(), nb, st)
+    assert guarded()
+    check_forward_at(out.view(shape), stats.view(2, B, *shape[2:]), x, gain, bias)
+    e = dout.double() * col(gain, x)
+    _, mean, r, xh = oracle(x, None, None, 1e-5)
+    want = r * (e - e.mean(1, keepdim=True) - xh * (e * xh).mean(1, keepdim=True))
+    A, XH, E = (t.amax(1, keepdim=True) for t in (x.double().abs() * r, xh.abs(), e.abs()))
+    # the statistics are the forward pass's own here: xh off by up to (n + 8) u (A + XH (1 + A))
+    k = adds(x) + 8
+    tol = U * r * E * (k * (1 + XH ** 2) + 2 * k * (1 + XH) * (A + XH * (1 + A))) + half_step(want, dtype) * (1 + 2 ** -6) + 1e-37
+    check(dx.view(shape), want, tol, "dx")
+    keep = dx.clone()
+    for over in (ds, xs):
+        saved = over.clone()
+        D.disco_norm_backward(B, C, n, code, ds.data_ptr(), xs.data_ptr(), stats.data_ptr(), ga.data_ptr(),
+                              over.data_ptr(), None, None, None, 0, st)
+        # another phase in 16 bytes may take another form, whose sums differ in their order
+        check(over.view(shape), keep.view(shape).double(), 2 * tol, "dx over an input")
+        over.copy_(saved)
+    D.disco_norm(B, C, n, code, xs.data_ptr(), ga.data_ptr(), bi.data_ptr(), 1e-5, xs.data_ptr(), None, st)
+    check_forward_at(xs.view(shape), None, x, gain, bias)
+    assert guarded()
+
+
+def check_forward_at(out, stats, x, gain, bias):
+    want, mean, r, xh = oracle(x, gain, bias, 1e-5)
+    A, n = x.double().abs().amax(1, keepdim=True) * r, adds(x)
+    check(out, want, (n + 8) * U * (A + xh.abs() * (1 + A)) * col(gain, x).abs() + U * col(bias, x).abs()
+          + half_step(want, x.dtype) * (1 + 2 ** -6) + 1e-37, "out")
+    if stats is not None:
+        check(stats[0].unsqueeze(1), mean, (n + 1) * U * x.double().abs().amax(1, keepdim=True) + 1e-37, "mean")
+        check(stats[1].unsqueeze(1), r, ((n + 1) * U * A + (n + 1) * U) * r, "1 / deviation")
