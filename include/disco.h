@@ -341,6 +341,19 @@ disco_status disco_muon(int n, int groups, int rows, int cols, disco_dtype dtype
                         const void* const* grad, const float* const* m, void* const* w_out, float* const* m_out,
                         void* workspace, size_t ws_bytes, void* stream);
 
+/* Self test of what a step does when one of its device-side waits runs out, as disco_wait_selftest is
+ * for the wait itself: disco_muon of matrices of more than 32 rows and columns, except that a first
+ * product is withheld and the waits for it are given up after limit_us microseconds (1 to 1000000).
+ * Every kernel of the call ends, m_out holds the new momentum, w_out is left as it was, and the next
+ * disco_sync_status reports DISCO_ERR_TIMEOUT.  (After a wait that runs out by itself the same holds,
+ * but for matrices, and tiles of a last product, that were done beside it.)  Errors as disco_muon's,
+ * INVALID_ARG for a limit out of range, UNSUPPORTED for a smaller matrix. */
+disco_status disco_muon_wait_selftest(unsigned int limit_us, int n, int groups, int rows, int cols, disco_dtype dtype,
+                                      const disco_newton_schulz_t* ns, double lr, double momentum, int nesterov,
+                                      double weight_decay, const void* const* w, const void* const* grad,
+                                      const float* const* m, void* const* w_out, float* const* m_out, void* workspace,
+                                      size_t ws_bytes, void* stream);
+
 /* Weight gradient that allocates nothing (the pages have no counterpart to this entry point).
  *
  * disco_bwd_weight needs a caller-provided workspace for its split-K partial sums.  Some

@@ -87,6 +87,34 @@ disco::MuonArgs muon_args(int n, int groups, int rows, int cols, disco_dtype dty
   return a;
 }
 
+disco_status muon(unsigned int hold_us, int n, int groups, int rows, int cols, disco_dtype dtype, const disco_newton_schulz_t* ns,
+                  double lr, double momentum, int nesterov, double weight_decay, const void* const* w,
+                  const void* const* grad, const float* const* m, void* const* w_out, float* const* m_out,
+                  void* workspace, size_t ws_bytes, void* stream) {
+  disco_status s = check_update(n, groups, rows, cols, dtype, ns, workspace, ws_bytes);
+  if (s) return s;
+  if (!std::isfinite(lr) || !std::isfinite(weight_decay)) return invalid("lr and weight_decay must be finite");
+  if (!(momentum >= 0 && momentum < 1)) return invalid("momentum outside [0, 1)");
+  const size_t es = dtype == DISCO_BF16 ? 2 : 4;
+  if (bad_pointers(w, n, es) || bad_pointers(grad, n, es) || bad_pointers(w_out, n, es) || bad_pointers(m, n, 4) ||
+      bad_pointers(m_out, n, 4))
+    return invalid("w, grad, m, w_out and m_out hold n device pointers on their element's alignment");
+  disco::MuonArgs a = muon_args(n, groups, rows, cols, dtype, ns);
+  a.in = grad;
+  a.out = w_out;
+  a.step = true;
+  a.w = w;
+  a.m = m;
+  a.m_out = m_out;
+  a.keep = (float)(1 - lr * weight_decay);
+  a.rate = (float)(lr * std::sqrt(std::max(1.0, (double)rows / cols)));
+  a.momentum = (float)momentum;
+  a.nesterov = nesterov != 0;
+  a.hold_ns = 1000ull * hold_us;
+  cudaError_t e = disco::launch_muon(a, workspace, static_cast<cudaStream_t>(stream));
+  return e == cudaSuccess ? DISCO_OK : set_cuda_error(e, "update launch");
+}
+
 }  // namespace
 
 extern "C" {
@@ -185,27 +213,19 @@ disco_status disco_muon(int n, int groups, int rows, int cols, disco_dtype dtype
                         double lr, double momentum, int nesterov, double weight_decay, const void* const* w,
                         const void* const* grad, const float* const* m, void* const* w_out, float* const* m_out,
                         void* workspace, size_t ws_bytes, void* stream) {
-  disco_status s = check_update(n, groups, rows, cols, dtype, ns, workspace, ws_bytes);
-  if (s) return s;
-  if (!std::isfinite(lr) || !std::isfinite(weight_decay)) return invalid("lr and weight_decay must be finite");
-  if (!(momentum >= 0 && momentum < 1)) return invalid("momentum outside [0, 1)");
-  const size_t es = dtype == DISCO_BF16 ? 2 : 4;
-  if (bad_pointers(w, n, es) || bad_pointers(grad, n, es) || bad_pointers(w_out, n, es) || bad_pointers(m, n, 4) ||
-      bad_pointers(m_out, n, 4))
-    return invalid("w, grad, m, w_out and m_out hold n device pointers on their element's alignment");
-  disco::MuonArgs a = muon_args(n, groups, rows, cols, dtype, ns);
-  a.in = grad;
-  a.out = w_out;
-  a.step = true;
-  a.w = w;
-  a.m = m;
-  a.m_out = m_out;
-  a.keep = (float)(1 - lr * weight_decay);
-  a.rate = (float)(lr * std::sqrt(std::max(1.0, (double)rows / cols)));
-  a.momentum = (float)momentum;
-  a.nesterov = nesterov != 0;
-  cudaError_t e = disco::launch_muon(a, workspace, static_cast<cudaStream_t>(stream));
-  return e == cudaSuccess ? DISCO_OK : set_cuda_error(e, "update launch");
+  return muon(0, n, groups, rows, cols, dtype, ns, lr, momentum, nesterov, weight_decay, w, grad, m, w_out, m_out,
+              workspace, ws_bytes, stream);
+}
+
+disco_status disco_muon_wait_selftest(unsigned int limit_us, int n, int groups, int rows, int cols, disco_dtype dtype,
+                                      const disco_newton_schulz_t* ns, double lr, double momentum, int nesterov,
+                                      double weight_decay, const void* const* w, const void* const* grad,
+                                      const float* const* m, void* const* w_out, float* const* m_out, void* workspace,
+                                      size_t ws_bytes, void* stream) {
+  if (limit_us < 1 || limit_us > 1000000) return invalid("limit_us must be in [1, 1000000]");
+  if (std::min(rows, cols) <= 32) return set_error(DISCO_ERR_UNSUPPORTED, "matrices of up to 32 rows may have no wait");
+  return muon(limit_us, n, groups, rows, cols, dtype, ns, lr, momentum, nesterov, weight_decay, w, grad, m, w_out, m_out,
+              workspace, ws_bytes, stream);
 }
 
 }  // extern "C"

@@ -5,6 +5,11 @@
 //   A = X X^T,  B = a I + b A + c A A,  X <- B X
 // which is the odd polynomial a s + b s^3 + c s^5 on each singular value s.
 //
+// Waits.  Every wait on an mbarrier is bounded.  After one that ran out a CTA waits and multiplies no
+// more, still reaches every barrier of its cluster, lets what is in flight land and stores nothing; the
+// others of its cluster store nothing either, and in a chain of kernels a word in the workspace tells
+// the later ones, so that no weight is overwritten from void products.
+//
 // Three forms, by R alone unless the columns do not fit:
 //   up to 32 rows      one launch, fp32 on the CUDA cores, a cluster of CTAs per matrix;
 //   33 to 128 rows     one launch, tensor cores, X in shared memory for all steps, a cluster per matrix;
@@ -132,11 +137,12 @@ __device__ __forceinline__ float result_of(const Rule& r, float w, float x) {
 }
 
 // Sums of squares of a slice of each matrix; for a whole step the momentum is updated on the way.
-// fp64: no update is too large or too small for its square.
+// fp64: no update is too large or too small for its square.  *fail: the chain's failure word.
 template <typename T>
 __global__ void __launch_bounds__(256) ns_norm_kernel(const __grid_constant__ Pointers p, Shape s, Rule r,
-                                                      double* __restrict__ part) {
+                                                      double* __restrict__ part, int* fail) {
   __shared__ double warps[8];
+  if (blockIdx.x == 0 && blockIdx.y == 0 && threadIdx.x == 0) *fail = 0;
   let_next_start();
   const int mi = blockIdx.y, t = mi / s.groups, g = mi % s.groups;
   const size_t n = (size_t)s.rows * s.cols, base = g * n;
@@ -244,6 +250,8 @@ struct ProductArgs {
   float* part;            // kSymmetric, S > 1: [S][nm][Rp][Rp]
   Becomes f;              // kSymmetric, S = 1: what the product becomes, into dst
   __half* dst;            // kUpdate: the next X
+  int* fail;              // set when a wait of the chain ran out
+  unsigned long long hold_ns;  // self test: nothing is loaded, and waits are given up after this
   Rule r;
 };
 
@@ -325,6 +333,8 @@ __device__ __forceinline__ uint32_t cluster_rank() {
 __device__ __forceinline__ void cluster_sync() {
   asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
 }
+__device__ __forceinline__ void cluster_arrive() { asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory"); }
+__device__ __forceinline__ void cluster_wait() { asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory"); }
 __device__ __forceinline__ uint32_t at_rank(uint32_t addr, uint32_t rank) {
   uint32_t r;
   asm("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(r) : "r"(addr), "r"(rank));
@@ -363,6 +373,14 @@ __device__ __forceinline__ void pair_commit(uint64_t* bar) {
       "h"((uint16_t)3)
       : "memory");
 }
+__device__ __forceinline__ void st_remote(uint32_t addr, int v) {
+  asm volatile("st.shared::cluster.b32 [%0], %1;" ::"r"(addr), "r"(v) : "memory");
+}
+// Sets `bad` of this CTA, and of all S of its cluster.
+__device__ __forceinline__ void mark_bad(int* bad, int S) {
+  *reinterpret_cast<volatile int*>(bad) = 1;
+  for (int k = 0; S > 1 && k < S; ++k) st_remote(at_rank(tc::smem_u32(bad), k), 1);
+}
 // Arrives on a barrier of either CTA.  What it orders is this warp's reads of TMEM, which are
 // complete (wait::ld), and no memory: a release over the cluster would cost a fence a chunk.
 __device__ __forceinline__ void arrive_remote(uint32_t bar) {
@@ -382,6 +400,7 @@ __global__ void __launch_bounds__(kProductThreads, 1)
   uint64_t* tempty = tfull + 1;       // and every CTA has read it
   uint64_t* done = tempty + 1;
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(done + 1);
+  int* bad = reinterpret_cast<int*>(tmem_slot + 1);  // a wait ran out here, in the cluster that shares K or before
   constexpr bool kMn = MODE != kSymmetric;
   constexpr int kCtas = PAIR ? 2 : 1, kSide = kCtas * kTile, kCols = kSide / 4;  // columns of a warp
   const Shape& s = a.s;
@@ -419,6 +438,7 @@ __global__ void __launch_bounds__(kProductThreads, 1)
     tc::mbar_init(tempty, kCtas * kDrainWarps);
     tc::mbar_init(done, 1);
     tc::fence_barrier_init();
+    *bad = 0;
   }
   if (warp == kDrainWarps + 1) {
     if constexpr (PAIR) {
@@ -437,11 +457,18 @@ __global__ void __launch_bounds__(kProductThreads, 1)
   tc::fence_after_sync();
   const uint32_t tmem = *tmem_slot;
   wait_previous();
+  // whether no wait ran out before this kernel; the loads do not wait for the answer (0.5 us a product)
+  auto sound = [&] { return *reinterpret_cast<const volatile int*>(a.fail) == 0; };
+  bool ok = true;
+  const unsigned long long limit = a.hold_ns ? a.hold_ns : tc::kWaitNs;
+  auto wait = [&](uint64_t* bar, uint32_t parity) { return tc::mbar_wait(bar, parity, limit); };
 
   if (warp == kDrainWarps && lane == 0) {
-    for (int k = k_lo; k < k_hi; ++k) {
+    for (int k = a.hold_ns ? k_hi : k_lo; k < k_hi; ++k) {
       const int i = k - k_lo, st = i % kStages;
-      if (i >= kStages && !tc::mbar_wait(&empty[st], ((i / kStages) & 1) ^ 1)) break;
+      if (i == kStages) ok = sound();
+      ok = ok && (i < kStages || wait(&empty[st], ((i / kStages) & 1) ^ 1));
+      if (!ok) break;
       uint8_t* base = smem + st * kStageBytes;
       const uint32_t bar = PAIR ? at_rank(tc::smem_u32(&full[st]), 0) : 0;
       if (rank == 0) tc::mbar_arrive_expect_tx(&full[st], kCtas * kStageBytes);
@@ -468,10 +495,11 @@ __global__ void __launch_bounds__(kProductThreads, 1)
       if constexpr (PAIR) pair_commit(bar);
       else tc::mma_commit(bar);
     };
+    ok = sound();
     for (int k = k_lo; k < k_hi; ++k) {
       const int i = k - k_lo, st = i % kStages;
-      if (!tc::mbar_wait(&full[st], (i / kStages) & 1)) break;
-      if (i > 0 && !tc::mbar_wait(tempty, (i & 1) ^ 1)) break;
+      ok = ok && wait(&full[st], (i / kStages) & 1) && (i == 0 || wait(tempty, (i & 1) ^ 1));
+      if (!ok) break;
       tc::fence_after_sync();
       const uint32_t p0 = tc::smem_u32(smem + st * kStageBytes), q0 = p0 + 2 * kOperand;
       const bool pm = p_mn(k), qm = q_mn(k);
@@ -497,7 +525,6 @@ __global__ void __launch_bounds__(kProductThreads, 1)
     commit(done);
   }
   __syncwarp();
-  bool ok = true;
   // The tile goes through the operand buffers, which are free: 128 rows of kSide fp32 values, the
   // 16-byte blocks of a row exchanged by the row's last bits.  What is made of it then runs in
   // short loops: unrolled over a thread's registers the code came cold from L2 and cost 8 us.
@@ -512,8 +539,10 @@ __global__ void __launch_bounds__(kProductThreads, 1)
     float acc[kCols];
 #pragma unroll
     for (int i = 0; i < kCols; ++i) acc[i] = 0.0f;
+    ok = sound();
     for (int i = 0; i < k_hi - k_lo && ok; ++i) {
-      ok = tc::mbar_wait(tfull, i & 1);
+      ok = __all_sync(~0u, wait(tfull, i & 1));
+      if (!ok) break;
       tc::fence_after_sync();
 #pragma unroll
       for (int h = 0; h < kCols; h += 32) {
@@ -531,22 +560,26 @@ __global__ void __launch_bounds__(kProductThreads, 1)
         for (int c = 0; c < 32; ++c) acc[h + c] += __uint_as_float(v[c]);
       }
     }
-    ok = ok && tc::mbar_wait(done, 0);
-    tc::fence_after_sync();
+    ok = ok && __all_sync(~0u, wait(done, 0));
+    if (ok) {  // so all chunks were loaded and multiplied, and the operand buffers are free
+      tc::fence_after_sync();
 #pragma unroll
-    for (int c = 0; c < kCols; c += 16) {
-      float v[16];
-      tc::tmem_ld16(tw + kSide + c, v);
+      for (int c = 0; c < kCols; c += 16) {
+        float v[16];
+        tc::tmem_ld16(tw + kSide + c, v);
 #pragma unroll
-      for (int i = 0; i < 16; i += 4)
-        *block_of(quarter + lane, (c0 + c + i) / 4) =
-            make_float4(fmaf(v[i], 1.0f / kSl, acc[c + i]), fmaf(v[i + 1], 1.0f / kSl, acc[c + i + 1]),
-                        fmaf(v[i + 2], 1.0f / kSl, acc[c + i + 2]), fmaf(v[i + 3], 1.0f / kSl, acc[c + i + 3]));
+        for (int i = 0; i < 16; i += 4)
+          *block_of(quarter + lane, (c0 + c + i) / 4) =
+              make_float4(fmaf(v[i], 1.0f / kSl, acc[c + i]), fmaf(v[i + 1], 1.0f / kSl, acc[c + i + 1]),
+                          fmaf(v[i + 2], 1.0f / kSl, acc[c + i + 2]), fmaf(v[i + 3], 1.0f / kSl, acc[c + i + 3]));
+      }
+      tc::fence_before_sync();
     }
-    tc::fence_before_sync();
   }
+  if (!ok) mark_bad(bad, joined ? a.S : 1);
   if constexpr (joined) cluster_sync();  // the sums of all CTAs of the cluster are in their buffers
   else __syncthreads();
+  const bool store = *reinterpret_cast<volatile int*>(bad) == 0;
   // 16 bytes of the tile, over all parts of K
   auto sum_of = [&](int r, int block) {
     float4 v = *block_of(r, block);
@@ -568,7 +601,7 @@ __global__ void __launch_bounds__(kProductThreads, 1)
     }
     return v;
   };
-  if (warp < kDrainWarps && ok) {
+  if (warp < kDrainWarps && store) {
     const size_t pa = (size_t)s.nm * s.Rp * s.Rp, px = (size_t)s.nm * s.Rp * s.Lp;
     const size_t tensor = (size_t)(mi % s.groups) * s.rows * s.cols;
     if (PAIR && MODE == kSymmetric && a.S > 1) {
@@ -632,6 +665,10 @@ __global__ void __launch_bounds__(kProductThreads, 1)
         }
       }
     }
+  }
+  if (!store) {
+    if (threadIdx.x == 0) *reinterpret_cast<volatile int*>(a.fail) = 1;
+    tc::give_up();
   }
   // no CTA leaves before another's last arrival, MMA or read
   all_sync();
@@ -702,6 +739,7 @@ struct SmallArgs {
   float a, b, c;
   double eps;
   int steps, S, nc, max_chunks;
+  unsigned long long hold_ns;  // self test: the first CTA withholds its first product, and waits are given up after this
 };
 
 // Byte offsets of a CTA's shared memory.
@@ -779,6 +817,7 @@ __global__ void __launch_bounds__(kSmallThreads, 1)
   double* warps = norms + kSmallMaxCluster;                    // [16]
   uint64_t* done = reinterpret_cast<uint64_t*>(warps + kSmallThreads / 32);
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(done + 1);
+  int* bad = reinterpret_cast<int*>(tmem_slot + 1);  // a wait ran out somewhere in the cluster
   const Shape& s = a.s;
   const int t = threadIdx.x, warp = t >> 5, lane = t & 31;
   const int S = a.S, q = S > 1 ? (int)cluster_rank() : 0, mi = blockIdx.x / S;
@@ -790,6 +829,7 @@ __global__ void __launch_bounds__(kSmallThreads, 1)
   if (t == 0) {
     tc::mbar_init(done, 1);
     tc::fence_barrier_init();
+    *bad = 0;
   }
   if (warp == 0) {
     tc::tmem_alloc(tmem_slot, 512);
@@ -915,10 +955,11 @@ __global__ void __launch_bounds__(kSmallThreads, 1)
 
   uint32_t phase = 0;
   bool ok = true;
+  const unsigned long long limit = a.hold_ns ? a.hold_ns : tc::kWaitNs;
   const uint32_t sxh = tc::smem_u32(xh), sxl = tc::smem_u32(xl), sah = tc::smem_u32(ah), sal = tc::smem_u32(al);
   const uint32_t tw = tmem + ((uint32_t)quarter << 16);
-  auto finish = [&]() {  // the issued products are done and visible
-    ok = tc::mbar_wait(done, phase) && ok;
+  auto finish = [&]() {  // the issued products are done and visible; a warp waits in vain once
+    ok = ok && __all_sync(~0u, tc::mbar_wait(done, phase, limit));
     phase ^= 1;
     tc::fence_after_sync();
   };
@@ -964,7 +1005,7 @@ __global__ void __launch_bounds__(kSmallThreads, 1)
   constexpr float kToA = kSa / (kSx * kSx);
   const int shift = 31 - __clz(RP / S);  // log2 of a block of A's columns
   for (int step = 0; step < a.steps; ++step) {
-    if (t == 0) square(sxh, sxl, mine);
+    if (t == 0 && ok && !(a.hold_ns && step == 0 && q == 0)) square(sxh, sxl, mine);
     __syncwarp();
     finish();
     if (S > 1) {
@@ -1036,7 +1077,7 @@ __global__ void __launch_bounds__(kSmallThreads, 1)
       }
       settle();
     }
-    if (t == 0) square(sah, sal, RP / 64);
+    if (t == 0 && ok) square(sah, sal, RP / 64);
     __syncwarp();
     finish();
     if (live) {
@@ -1064,7 +1105,7 @@ __global__ void __launch_bounds__(kSmallThreads, 1)
     const bool last = step + 1 == a.steps;
     for (int g0 = 0; g0 < mine; g0 += 4) {  // up to 256 columns at a time
       const int cols = min(4, mine - g0) * 64;
-      if (t == 0) {
+      if (t == 0 && ok) {
         const uint32_t idesc = idesc_f16(128, cols, false, true);
         for (int k = 0; k < RP / 16; ++k) {
           const uint32_t poff = (uint32_t)(k >> 2) * kChunk + (k & 3) * 32, qoff = (uint32_t)g0 * kChunk + k * 2048;
@@ -1078,6 +1119,10 @@ __global__ void __launch_bounds__(kSmallThreads, 1)
       }
       __syncwarp();
       finish();
+      if (last && g0 + 4 >= mine) {  // the last wait
+        if (!ok) mark_bad(bad, S);
+        if (S > 1) cluster_arrive();
+      }
       if (live) {
         for (int c = side * (cols / kSides); c < (side + 1) * (cols / kSides); c += 16) {
           float v[16];
@@ -1099,7 +1144,9 @@ __global__ void __launch_bounds__(kSmallThreads, 1)
       settle();
     }
   }
-  if (ok) {
+  if (S > 1) cluster_wait();
+  const bool store = *reinterpret_cast<volatile int*>(bad) == 0;
+  if (store) {
     T* out = static_cast<T*>(ptr.out[tn]) + base;
     const T* w = a.r.step ? static_cast<const T*>(ptr.w[tn]) + base : nullptr;
 #pragma unroll 2
@@ -1117,6 +1164,7 @@ __global__ void __launch_bounds__(kSmallThreads, 1)
       store_wide(out + x.at, x.here, v);
     }
   }
+  if (!store) tc::give_up();
   if (warp == 0) tc::tmem_dealloc(tmem, 512);
 }
 
@@ -1417,7 +1465,7 @@ size_t align256(size_t v) { return (v + 255) & ~size_t(255); }
 constexpr int kMostSms = 160;  // what the workspace provides for
 
 struct Layout {
-  size_t x[2], a, b, part, norm, total;
+  size_t x[2], a, b, part, norm, fail, total;
 };
 
 Layout layout_of(const Shape& s) {
@@ -1438,6 +1486,7 @@ Layout layout_of(const Shape& s) {
     l.part = take(4 * na * std::max(splits_of(s, t, s.Lp, kMostSms), splits_of(s, t, s.Rp, kMostSms)));
   }
   l.norm = take(sizeof(double) * s.nm * kNormBlocks);
+  l.fail = take(sizeof(int));
   l.total = at;
   return l;
 }
@@ -1598,7 +1647,7 @@ cudaError_t run_chunk(const MuonArgs& a, int t0, int n, char* ws, int sms, cudaS
   }
   const SmallPlan sp = small_plan(s, sms);
   if (sp.ok) {
-    const SmallArgs g{s, r, a.a, a.b, a.c, a.eps, a.steps, sp.S, sp.nc, sp.max_chunks};
+    const SmallArgs g{s, r, a.a, a.b, a.c, a.eps, a.steps, sp.S, sp.nc, sp.max_chunks, a.hold_ns};
     return sp.rp == 64 ? run_small<T, 64>(ptr, g, sp.smem, st) : run_small<T, 128>(ptr, g, sp.smem, st);
   }
   __half* x[2] = {reinterpret_cast<__half*>(ws + l.x[0]), reinterpret_cast<__half*>(ws + l.x[1])};
@@ -1606,13 +1655,14 @@ cudaError_t run_chunk(const MuonArgs& a, int t0, int n, char* ws, int sms, cudaS
   __half* bm = reinterpret_cast<__half*>(ws + l.b);
   float* part = reinterpret_cast<float*>(ws + l.part);
   double* norm = reinterpret_cast<double*>(ws + l.norm);
+  int* fail = reinterpret_cast<int*>(ws + l.fail);
   CUtensorMap mx[2], ma, mb;
   if (!plane_map(&mx[0], x[0], s.Lp, s.Rp, 2 * s.nm) || !plane_map(&mx[1], x[1], s.Lp, s.Rp, 2 * s.nm) ||
       !plane_map(&ma, am, s.Rp, s.Rp, 2 * s.nm) || !plane_map(&mb, bm, s.Rp, s.Rp, 2 * s.nm))
     return cudaErrorInvalidValue;
   cudaError_t e;
   const int blocks = (int)std::min<size_t>(kNormBlocks, ((size_t)a.rows * a.cols + 256 * kWide - 1) / (256 * kWide));
-  ns_norm_kernel<T><<<dim3(blocks, s.nm), 256, 0, st>>>(ptr, s, r, norm);
+  ns_norm_kernel<T><<<dim3(blocks, s.nm), 256, 0, st>>>(ptr, s, r, norm, fail);
   count_launch();
   if ((e = cudaGetLastError()) != cudaSuccess) return e;
   if ((e = chain(ns_load_kernel<T>, dim3(s.Lp / 64, s.Rp / 64, s.nm), 1, 256, 0, st, ptr, s, r, a.eps,
@@ -1622,6 +1672,7 @@ cudaError_t run_chunk(const MuonArgs& a, int t0, int n, char* ws, int sms, cudaS
   g.s = s;
   g.r = r;
   g.part = part;
+  g.fail = fail;
   const dim3 red(s.Rp / 64, s.Rp / 64, s.nm);
   // P P^T into dst, as `f` says
   auto square = [&](const CUtensorMap& p, int k, const Becomes& f, __half* dst) {
@@ -1637,7 +1688,9 @@ cudaError_t run_chunk(const MuonArgs& a, int t0, int n, char* ws, int sms, cudaS
   };
   for (int k = 0; k < a.steps; ++k) {
     const int now = k & 1;
+    g.hold_ns = k == 0 ? a.hold_ns : 0;
     if ((e = square(mx[now], s.Lp, Becomes{a.a, a.b, a.c, nullptr}, am)) != cudaSuccess) return e;
+    g.hold_ns = 0;
     if ((e = square(ma, s.Rp, Becomes{a.a, a.b, a.c, am}, bm)) != cudaSuccess) return e;
     g.upper = true;
     g.chunks = s.Rp / kBk;

@@ -24,6 +24,7 @@ struct MuonArgs {
   float keep, rate;       // w' = keep * w - rate * X
   float momentum;
   bool nesterov;
+  unsigned long long hold_ns;  // self test: a first product whose waits run out after this (0: none)
 };
 
 // 0 where a matrix fits the one-launch forms.

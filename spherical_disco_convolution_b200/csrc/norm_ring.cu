@@ -300,13 +300,6 @@ __device__ __forceinline__ void release(const RingArgs& a, const CUtensorMap* ma
   }
 }
 
-// After a wait that ran out (the status word says so, the results are void) a warp waits and loads
-// no more, which ends the kernel soon; the copies in flight get 2 ms to land before the CTA goes.
-__device__ __noinline__ void give_up() {
-  const unsigned long long t0 = tc::globaltimer();
-  while (tc::globaltimer() - t0 < 2000000ull) __nanosleep(1000);
-}
-
 template <typename F, bool BWD>
 __device__ __forceinline__ void fill_ring(const RingArgs& a, const CUtensorMap* map_x, const CUtensorMap* map_d,
                                           const Ring& r, int group, int lane, int w) {
@@ -468,7 +461,9 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
     }
   }
-  if (F::kTma && !ok) give_up();
+  // after a wait that ran out (the status word says so, the results are void) a warp waits and loads no
+  // more, which ends the kernel soon
+  if (F::kTma && !ok) tc::give_up();
 }
 
 template <typename F>
@@ -667,7 +662,9 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
     }
   }
-  if (F::kTma && !ok) give_up();
+  // after a wait that ran out (the status word says so, the results are void) a warp waits and loads no
+  // more, which ends the kernel soon
+  if (F::kTma && !ok) tc::give_up();
   if (!a.part) return;
   flush();
   __syncthreads();

@@ -67,14 +67,14 @@ __device__ __forceinline__ bool mbar_try_wait(uint64_t* bar, uint32_t parity) {
 }
 
 // Waits for the phase with the given parity to complete; false (and the status word set)
-// when kWaitNs passes first.
-__device__ __forceinline__ bool mbar_wait(uint64_t* bar, uint32_t parity) {
+// when limit_ns passes first.
+__device__ __forceinline__ bool mbar_wait(uint64_t* bar, uint32_t parity, unsigned long long limit_ns = kWaitNs) {
   if (mbar_try_wait(bar, parity)) return true;
   const unsigned long long t0 = globaltimer();
   while (true) {
     for (int i = 0; i < 64; ++i)
       if (mbar_try_wait(bar, parity)) return true;
-    if (globaltimer() - t0 > kWaitNs) {
+    if (globaltimer() - t0 > limit_ns) {
       atomicExch(&g_device_status, 5);
       return false;
     }
@@ -113,6 +113,13 @@ __device__ __forceinline__ bool mbar_wait_sleep(uint64_t* bar, uint32_t parity, 
       return false;
     }
   }
+}
+
+// What a CTA does before it ends after a wait that ran out: its copies and MMAs in flight get 2 ms to
+// land, so that none writes into shared or tensor memory that it no longer has.
+static __device__ __noinline__ void give_up() {
+  const unsigned long long t0 = globaltimer();
+  while (globaltimer() - t0 < 2000000ull) __nanosleep(1000);
 }
 
 // 2D / 3D tiled TMA loads into shared memory, completion counted on `bar`.

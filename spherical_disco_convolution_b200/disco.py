@@ -121,6 +121,8 @@ def _load():
         "disco_orthogonalize": [I, I, I, I, I, ctypes.POINTER(disco_newton_schulz_t), PP, PP, P, Z, P],
         "disco_muon": [I, I, I, I, I, ctypes.POINTER(disco_newton_schulz_t), ctypes.c_double, ctypes.c_double, I,
                        ctypes.c_double, PP, PP, PP, PP, PP, P, Z, P],
+        "disco_muon_wait_selftest": [ctypes.c_uint, I, I, I, I, I, ctypes.POINTER(disco_newton_schulz_t), ctypes.c_double,
+                                     ctypes.c_double, I, ctypes.c_double, PP, PP, PP, PP, PP, P, Z, P],
         "disco_plan_info": [P, I, IP],
         "disco_sync_status": [P],
         "disco_wait_selftest": [ctypes.c_uint, P],
@@ -414,3 +416,11 @@ def disco_muon(groups, rows, cols, dtype, ns, lr, momentum, nesterov, weight_dec
     _check(_lib.disco_muon(len(w), groups, rows, cols, dtype, ctypes.byref(ns), float(lr), float(momentum),
                            int(nesterov), float(weight_decay), _pointers(w), _pointers(grad), _pointers(m), _pointers(w_out),
                            _pointers(m_out), workspace, ws_bytes, stream))
+
+
+def disco_muon_wait_selftest(limit_us, groups, rows, cols, dtype, ns, lr, momentum, nesterov, weight_decay, w, grad, m,
+                             w_out, m_out, workspace, ws_bytes, stream) -> None:
+    _check(_lib.disco_muon_wait_selftest(limit_us, len(w), groups, rows, cols, dtype, ctypes.byref(ns), float(lr),
+                                         float(momentum), int(nesterov), float(weight_decay), _pointers(w),
+                                         _pointers(grad), _pointers(m), _pointers(w_out), _pointers(m_out), workspace,
+                                         ws_bytes, stream))

@@ -10,6 +10,7 @@ Frobenius norm of each matrix.  The store adds half a step of the type, relative
 """
 
 import math
+import time
 from concurrent.futures import ThreadPoolExecutor
 
 import pytest
@@ -618,3 +619,46 @@ def test_bad_values_spread_over_their_own_matrix_only(shape, groups, cuda):
     assert torch.equal(got[0], want[0]) and torch.isnan(got[1]).any()
     rows = shape[0] // groups
     assert torch.equal(got[1][rows:], want[1][rows:])
+
+
+# ------------------------------------------------------------------ a wait that runs out
+
+def test_the_wait_self_test_refuses():
+    def call(limit=1000, rows=64, cols=192, w=(P,)):
+        D.disco_muon_wait_selftest(limit, 1, rows, cols, 0, D.newton_schulz(5, NS, 1e-7), 0.1, 0.9, True, 0.0, list(w), [P],
+                                   [P], list(w), [P], P, 1 << 40, None)
+
+    assert _status(lambda: call(limit=0)) == D.DISCO_ERR_INVALID_ARG
+    assert _status(lambda: call(limit=1000001)) == D.DISCO_ERR_INVALID_ARG
+    assert _status(lambda: call(rows=32)) == D.DISCO_ERR_UNSUPPORTED
+    assert _status(lambda: call(w=(None,))) == D.DISCO_ERR_INVALID_ARG
+
+
+@gpu
+@pytest.mark.parametrize("steps", [1, 5, 32])
+@pytest.mark.parametrize("count,shape", [(1, (64, 192)), (3, (100, 2000)), (1, (140, 260)), (1, (512, 1000)), (1, (400, 500)),
+                                         (1, (1024, 4608)), (66, (300, 513))])
+def test_after_a_wait_that_ran_out_no_weight_is_written(count, shape, steps, cuda):
+    """The first product withheld, waits of 1 ms: the call ends soon whatever the number of steps (each of
+    its kernels may take the 2 ms in which copies land), says so once, and the weights stay."""
+    n, st = count, torch.cuda.current_stream().cuda_stream
+    ws = [torch.randn(shape, device=cuda) for _ in range(n)]
+    gs, ms = [update(shape, F32, 95, cuda)] * n, [torch.zeros(shape, device=cuda) for _ in range(n)]
+    want = muon.muon_update(ws, gs, ms, 0.1, steps=steps)
+    w0 = [w.clone() for w in ws]
+    nb = D.disco_orthogonalize_workspace_size(n, 1, *shape)
+    work = torch.full((nb + 256,), 0xff, dtype=torch.uint8, device=cuda)
+    wp, gp, mp = ([t.data_ptr() for t in ts] for ts in (ws, gs, ms))
+    D.disco_sync_status(st)
+    t0 = time.perf_counter()
+    D.disco_muon_wait_selftest(1000, 1, *shape, D.DISCO_F32, D.newton_schulz(steps, NS, 1e-7), 0.1, 0.95, True, 0.0, wp, gp,
+                               mp, wp, mp, work.data_ptr(), nb, st)
+    with pytest.raises(D.DiscoError) as e:
+        D.disco_sync_status(st)
+    assert e.value.status == D.DISCO_ERR_TIMEOUT and time.perf_counter() - t0 < 2.0
+    D.disco_sync_status(st)
+    assert all(torch.equal(a, b) for a, b in zip(ws, w0)) and all(torch.equal(a, b) for a, b in zip(ms, want[1]))
+    assert (work[nb:] == 0xff).all()
+    got = muon.muon_update(ws, gs, [torch.zeros_like(m) for m in ms], 0.1, steps=steps)
+    assert all(torch.equal(a, b) for x, y in zip(got, want) for a, b in zip(x, y))
+    D.disco_sync_status(st)
