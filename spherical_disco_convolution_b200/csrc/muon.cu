@@ -1425,14 +1425,15 @@ Shape shape_of(int n, int groups, int rows, int cols) {
 // unless the second kernel that they need (7 us) costs more than the chunks (1 us) that they save.
 // Single CTAs: a cluster as large as there are SMs for all tiles', for 512 values at least (a chunk takes
 // 0.75 us, the exchange 3 us; 300 x 513 in 144 us, without clusters 155; at 256 values 12 of 200 x 300
-// take 140 us instead of 134); of clusters of 8, 4 and 2 some 16, 32 and 70 run at a time.
+// take 140 us instead of 134).  148 SMs run some 16 clusters of 8, 32 of 4 and 70 of 2 at a time, and other
+// devices their share of that.
 int splits_of(const Shape& s, long long tiles, int k, int sms) {
   const int chunks = k / kBk;
   if (s.tile == 256) {
     const int S = std::max(1, std::min({(int)std::max<long long>(1, sms / 2 / tiles), chunks / 4, kMaxSplits}));
     return chunks - chunks / S < 7 ? 1 : S;
   }
-  return chunks < kLeastJoin ? 1 : tiles <= 16 && chunks >= 8 ? 8 : tiles <= 32 ? 4 : tiles <= 70 ? 2 : 1;
+  return chunks < kLeastJoin ? 1 : 9 * tiles <= sms ? 8 : 9 * tiles <= 2 * sms ? 4 : 19 * tiles <= 9 * sms ? 2 : 1;
 }
 long long symmetric_tiles(const Shape& s) {
   const long long nt = s.Rp / s.tile;
