@@ -73,18 +73,25 @@ def _workspace(x, n, groups, rows, cols):
 def _outputs(x, n, dtype=None):
     """n tensors like x, each with memory of its own: views of one allocation would share a version
     counter, and an in-place change of one would spoil what autograd saved of the others."""
-    return [x.new_empty(x.shape, dtype=dtype) for _ in range(n)]
+    return [torch.empty_like(x, dtype=dtype) for _ in range(n)]
 
 
-def _pointers(ts, x, what, dtype=None):
+def _pointers(ts, what):
+    """Pointers of tensors of one bucket, which are dense."""
+    if not all([t.is_contiguous() for t in ts]):
+        raise ValueError(f"{what} is contiguous")
+    return [t.data_ptr() for t in ts]
+
+
+def _pointers_like(ts, x, what, dtype=None):
     """Pointers of dense tensors of x's shape and device, and of its type or the one given."""
     shape, device, dtype = x.shape, x.device, dtype or x.dtype
     for t in ts:
         if t.dtype != dtype:
             raise TypeError(f"{what} is {dtype} here, not {t.dtype}")
-        if t.shape != shape or t.device != device or not t.is_contiguous():
-            raise ValueError(f"{what} is contiguous, of shape {tuple(shape)}, on {device}")
-    return [t.data_ptr() for t in ts]
+        if t.shape != shape or t.device != device:
+            raise ValueError(f"{what} is of shape {tuple(shape)}, on {device}")
+    return _pointers(ts, what)
 
 
 def orthogonalize(update, groups: int = 1, steps: int = 5, coefficients=COEFFICIENTS, eps: float = 1e-7):
@@ -97,7 +104,7 @@ def orthogonalize(update, groups: int = 1, steps: int = 5, coefficients=COEFFICI
         x = ts[at[0]]
         code = dense(x, "update")
         rows, cols = _matrix(x, groups)
-        u = _pointers([ts[i] for i in at], x, "update")
+        u = _pointers([ts[i] for i in at], "update")
         out = _outputs(x, len(at))
         ws, p, nb = _workspace(x, len(at), groups, rows, cols)
         launch(x, D.disco_orthogonalize, groups, rows, cols, code, ns, u, [o.data_ptr() for o in out], p, nb)
@@ -124,9 +131,9 @@ def muon_update(weight, grad, momentum_buffer, lr: float, momentum: float = 0.95
         x = ws[at[0]]
         code = dense(x, "weight")
         rows, cols = _matrix(x, groups)
-        w = _pointers([ws[i] for i in at], x, "weight")
-        g = _pointers([gs[i] for i in at], x, "grad")
-        m = _pointers([ms[i] for i in at], x, "momentum_buffer", torch.float32)
+        w = _pointers([ws[i] for i in at], "weight")
+        g = _pointers_like([gs[i] for i in at], x, "grad")
+        m = _pointers_like([ms[i] for i in at], x, "momentum_buffer", torch.float32)
         calls.append((at, x, code, rows, cols, w, g, m))
     if inplace and len({p for c in calls for p in c[5] + c[7]}) < 2 * len(ws):
         raise ValueError("a tensor is given twice: each is updated once")
