@@ -662,3 +662,24 @@ def test_after_a_wait_that_ran_out_no_weight_is_written(count, shape, steps, cud
     got = muon.muon_update(ws, gs, [torch.zeros_like(m) for m in ms], 0.1, steps=steps)
     assert all(torch.equal(a, b) for x, y in zip(got, want) for a, b in zip(x, y))
     D.disco_sync_status(st)
+
+
+@gpu
+@pytest.mark.parametrize("shape", [(4, 12), (16, 40), (30, 4000), (60, 300), (100, 2000), (200, 300), (300, 6000), (500, 40)])
+@pytest.mark.parametrize("top", [1e38, 3e38])
+def test_updates_near_the_largest_numbers(shape, top, cuda):
+    """1 / |U| is below fp32's normal numbers here."""
+    u = update(shape, F32, 96, cuda)
+    u = (u.double() * (top / float(u.abs().max()))).float()  # the factor is beyond fp32
+    want, tol = oracle(u)
+    check(muon.orthogonalize(u), want, tol, F32, 1, f"{shape}")
+
+
+@gpu
+@pytest.mark.parametrize("shape", [(12, 30), (40, 70), (140, 300)])
+def test_iterates_within_the_pairs_range(shape, cuda):
+    """Coefficients that let X grow: singular values of up to 4 before a step, entries of B of up to 100."""
+    u = update(shape, F32, 97, cuda)
+    for steps, coef in ((3, (2.0, 0.0, 0.0)), (1, (32.0, 32.0, 32.0)), (2, (1.0, 1.0, 1.0))):
+        want, tol = oracle(u, 1, steps, coef)
+        check(muon.orthogonalize(u, 1, steps, coef), want, tol, F32, 1, f"{shape} {coef}")
