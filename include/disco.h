@@ -313,11 +313,14 @@ disco_status disco_norm_backward(int B, int C, long long npts, disco_dtype dtype
  * update, out, w, grad and w_out are in `dtype`, m and m_out fp32.  The pointer arrays are HOST
  * arrays of n device pointers, read before the call returns.  out[i] may be update[i], w_out[i]
  * may be w[i] and m_out[i] may be m[i]; no other overlap.  The iterates are fp32 for matrices
- * with a side of at most 32 and fp16 pairs (hi + lo, 22 bits) for others, products are summed in
- * fp32 and the Frobenius norm in fp64: fp32 results are as close to the exact ones as fp32 matrix
- * products would leave them.  An update of zeros gives zeros; infinities and NaN spread over their
- * own matrix only; an iterate above 16 in magnitude (coefficients that diverge) may end as
- * infinities or NaN.
+ * with a side of at most 32 whose other side is at most 4376 (10648 for a side of at most 16, 18896
+ * for 8, 28784 for 4: what a cluster's shared memory holds), and fp16 pairs (hi + lo, 22 bits) for all
+ * others; products are summed in fp32 and the Frobenius norm in fp64.  fp32 results are as close to
+ * the exact ones as fp32 matrix products would leave them, except that a pair has a fixed last place:
+ * entries of X are good to 2^-48 at best, which shows where |U| is below 1e-7 of eps.  An update of
+ * zeros gives zeros; infinities and NaN spread over their own matrix only.  Pairs hold entries of X
+ * below 16, of X X^T below 32 and of a I + b X X^T + c (X X^T)^2 below 128: with coefficients that let
+ * a singular value grow above 5.6 before a step, results may be infinities or NaN.
  * Pointers need the alignment of their elements only.  Scratch comes in through `workspace`, at
  * least disco_orthogonalize_workspace_size bytes for the same n, groups, rows and cols, 256-byte
  * aligned (NULL where that is 0, as for matrices of few rows).  Both calls are asynchronous on

@@ -11,11 +11,12 @@
 // the later ones, so that no weight is overwritten from void products.
 //
 // Three forms, by R alone unless the columns do not fit:
-//   up to 32 rows      one launch, fp32 on the CUDA cores, a cluster of CTAs per matrix;
+//   up to 32 rows      one launch, fp32 on the CUDA cores, a cluster of CTAs per matrix (of 32 rows up to
+//                      4376 columns; longer ones take the next forms);
 //   33 to 128 rows     one launch, tensor cores, X in shared memory for all steps, a cluster per matrix;
 //   more               a chain of tiled products on tensor cores, operands in global memory (L2).
-// Measured in fp32 (a call's time on the GPU): 4 x 12 in 6.6 us, 32 x 96 in 18.5, 64 x 192 in 33, eight 128 x 576 in 62,
-// 256 x 2304 in 140, four 512 x 4608 in 379, 1024 x 9216 in 530.
+// Measured in fp32 (a call's time on the GPU): 4 x 12 in 6.7 us, 32 x 96 in 18.4, 64 x 192 in 34, eight 128 x 576 in 63,
+// 256 x 2304 in 142, four 512 x 4608 in 387, 1024 x 9216 in 517, 32 x 9216 in 185.
 //
 // Numbers of the tensor-core forms.  A small singular value is multiplied by `a` in every step, and a
 // rounding error of X in its direction with it: an X rounded to 8 or 11 bits would leave the weak
@@ -1413,7 +1414,7 @@ Shape shape_of(int n, int groups, int rows, int cols) {
   s.L = std::max(rows, cols);
   s.nm = n * groups;
   // pairs of CTAs where there is a tile for nearly every one of them and more than one along R
-  // (1024 x 4608: 327 us on pairs, 388 on single CTAs; 24 of 256 x 768: 207 and 196)
+  // (1024 x 4608: 341 us on pairs, 427 on single CTAs; 24 of 256 x 768: 215 and 201)
   s.tile = s.R > 256 && (long long)s.nm * up(s.R, 256) * up(s.L, 256) / (256 * 256) >= 64 ? 256 : 128;
   s.Rp = up(s.R, s.tile);
   s.Lp = up(s.L, s.tile);
@@ -1424,8 +1425,8 @@ Shape shape_of(int n, int groups, int rows, int cols) {
 // Pairs (symmetric products only): as many as give every two SMs a pair, each of 256 values at least,
 // unless the second kernel that they need (7 us) costs more than the chunks (1 us) that they save.
 // Single CTAs: a cluster as large as there are SMs for all tiles', for 512 values at least (a chunk takes
-// 0.75 us, the exchange 3 us; 300 x 513 in 144 us, without clusters 155; at 256 values 12 of 200 x 300
-// take 140 us instead of 134).  148 SMs run some 16 clusters of 8, 32 of 4 and 70 of 2 at a time, and other
+// 0.75 us, the exchange 3 us; 300 x 513 in 147 us, without clusters 157, and from 256 values on 142 with 12 of
+// 200 x 300 in 126 either way).  148 SMs run some 16 clusters of 8, 32 of 4 and 70 of 2 at a time, and other
 // devices their share of that.
 int splits_of(const Shape& s, long long tiles, int k, int sms) {
   const int chunks = k / kBk;
@@ -1532,7 +1533,7 @@ struct SmallPlan {
 
 // The one-launch form serves up to 128 rows whose columns fit the shared memory of a cluster.  A
 // step costs as much as three chunks besides its CTA's own, and the exchange between CTAs one more
-// (measured: 48 matrices of 64 x 576 in 74, 55 and 81 us on clusters of 1, 2 and 4).
+// (measured: 48 matrices of 64 x 576 in 77, 58 and 85 us on clusters of 1, 2 and 4).
 SmallPlan small_plan(const Shape& s, int sms) {
   SmallPlan p;
   if (s.R > 128) return p;
@@ -1588,7 +1589,7 @@ struct ThinPlan {
 };
 
 // Up to 32 rows: the smallest cluster whose CTAs have little enough to do (24 columns of 32 rows or as
-// much work of fewer: 32 x 96 takes 22 us on one CTA and 18.5 on four, 9 x 2000 takes 43 on one, 28 on
+// much work of fewer: 32 x 96 takes 22 us on one CTA and 18.2 on four, 9 x 2000 takes 50 on one, 43 on
 // two and 21 on eight) and fit shared memory, as far as there are SMs for all matrices.
 ThinPlan thin_plan(const Shape& s, int sms) {
   ThinPlan p;

@@ -9,7 +9,10 @@
 //
 // This is the form for planes shorter than 64 points and for more channels than the tiles of
 // norm_ring.cu hold (1024 forward, 512 backward); long planes with fewer go there (the 64 channels of
-// 721 x 1440 points in bf16 took 107 us forward and 266 backward here, and take 56 and 90 there).
+// 721 x 1440 points in bf16 took 107 us forward and 266 backward here, and take 52 and 93 there).
+// Measured (forward, backward): 1500 channels of 91 x 180 points in bf16 45 and 87 us, in fp32 75 and 114
+// (their bytes once: 15 and 23, 30 and 45); 1500 x 9 points, 4000 fields, bf16 275 and 313 (33 and 50);
+// (20000, 64) in fp32 12 and 20, (20000, 256) in bf16 30 and 88: points of a single-point plane lie C apart.
 //
 // The channels of a point lie P elements apart, so a warp reads runs of consecutive points of
 // one channel (16 bytes a lane where the alignment allows) and the sums over channels cross the
@@ -136,7 +139,7 @@ __device__ __forceinline__ void tile_stats(const NormShape& g, float eps, float2
 }
 
 // NC = 0: any number of channels, read twice (the second time mostly from L2); at 98 registers, one CTA an
-// SM, 1500 bf16 channels of 4000 x 9 points took 318 us, at 64 they take 268.
+// SM, 1500 bf16 channels of 4000 x 9 points took 318 us, at 64 they take 275.
 template <typename T, int VEC, int NC>
 __global__ void __launch_bounds__(kMaxThreads, NC == 0 ? 2 : 0) norm_fwd_kernel(NormShape g, const T* __restrict__ x, const T* __restrict__ gain,
                                 const T* __restrict__ bias, float eps, T* __restrict__ out, float* stats) {
