@@ -113,6 +113,22 @@ def orthogonalize(update, groups: int = 1, steps: int = 5, coefficients=COEFFICI
     return outs[0] if single else outs
 
 
+def _checked(ws, gs, ms, groups):
+    """The calls that one step takes, a bucket each: everything but the scalars is checked here,
+    before anything is written."""
+    calls = []
+    for at in _buckets(ws):
+        x = ws[at[0]]
+        code = dense(x, "weight")
+        rows, cols = _matrix(x, groups)
+        w = _pointers([ws[i] for i in at], "weight")
+        g = _pointers_like([gs[i] for i in at], x, "grad")
+        m = _pointers_like([ms[i] for i in at], x, "momentum_buffer", torch.float32)
+        _workspace_size(len(at), groups, rows, cols)  # refuses the sizes that the library does not take
+        calls.append((at, x, code, rows, cols, w, g, m))
+    return calls
+
+
 def muon_update(weight, grad, momentum_buffer, lr: float, momentum: float = 0.95, nesterov: bool = True,
                 weight_decay: float = 0.0, groups: int = 1, steps: int = 5, coefficients=COEFFICIENTS,
                 eps: float = 1e-7, inplace: bool = False):
@@ -126,15 +142,7 @@ def muon_update(weight, grad, momentum_buffer, lr: float, momentum: float = 0.95
     if not len(ws) == len(gs) == len(ms):
         raise ValueError(f"{len(ws)} weights, {len(gs)} gradients and {len(ms)} momentum buffers")
     ns = _rule(steps, coefficients, eps)
-    calls = []
-    for at in _buckets(ws):  # everything is checked before anything is written
-        x = ws[at[0]]
-        code = dense(x, "weight")
-        rows, cols = _matrix(x, groups)
-        w = _pointers([ws[i] for i in at], "weight")
-        g = _pointers_like([gs[i] for i in at], x, "grad")
-        m = _pointers_like([ms[i] for i in at], x, "momentum_buffer", torch.float32)
-        calls.append((at, x, code, rows, cols, w, g, m))
+    calls = _checked(ws, gs, ms, groups)
     if inplace and len({p for c in calls for p in c[5] + c[7]}) < 2 * len(ws):
         raise ValueError("a tensor is given twice: each is updated once")
     w_out, m_out = (ws, ms) if inplace else ([None] * len(ws), [None] * len(ws))
@@ -185,6 +193,7 @@ class Muon(torch.optim.Optimizer):
         if closure is not None:
             with torch.enable_grad():
                 loss = closure()
+        steps = []
         for group in self.param_groups:
             ps = [p for p in group["params"] if p.grad is not None]
             if not ps:
@@ -194,9 +203,13 @@ class Muon(torch.optim.Optimizer):
                     if torch.cuda.is_current_stream_capturing():  # a replay would start from zeros every time
                         raise RuntimeError("run one step of Muon before a CUDA graph captures it: it makes the momentum")
                     self.state[p]["momentum_buffer"] = torch.zeros_like(p, dtype=torch.float32)
-            muon_update(ps, [p.grad.contiguous() for p in ps], [self.state[p]["momentum_buffer"] for p in ps],
-                        group["lr"], group["momentum"], group["nesterov"], group["weight_decay"], group["groups"],
-                        group["steps"], group["coefficients"], group["eps"], inplace=True)
+            steps.append((group, ps, [p.grad.contiguous() for p in ps], [self.state[p]["momentum_buffer"] for p in ps]))
+        if len(steps) > 1:  # a group that is refused leaves the others' weights as they were, too
+            for group, *tensors in steps:
+                _checked(*tensors, group["groups"])
+        for group, ps, gs, ms in steps:
+            muon_update(ps, gs, ms, group["lr"], group["momentum"], group["nesterov"], group["weight_decay"],
+                        group["groups"], group["steps"], group["coefficients"], group["eps"], inplace=True)
         return loss
 
     def load_state_dict(self, state_dict):

@@ -683,3 +683,22 @@ def test_iterates_within_the_pairs_range(shape, cuda):
     for steps, coef in ((3, (2.0, 0.0, 0.0)), (1, (32.0, 32.0, 32.0)), (2, (1.0, 1.0, 1.0))):
         want, tol = oracle(u, 1, steps, coef)
         check(muon.orthogonalize(u, 1, steps, coef), want, tol, F32, 1, f"{shape} {coef}")
+
+
+@gpu
+def test_nothing_is_written_where_one_tensor_is_refused(cuda):
+    """A list of two shapes, the second beyond the library's sides: the first is left as it was."""
+    ws = [torch.randn(8, 12, device=cuda), torch.randn(32769, 2, device=cuda)]
+    gs, ms = [torch.randn_like(w) for w in ws], [torch.zeros_like(w) for w in ws]
+    kept = [w.clone() for w in ws]
+    with pytest.raises(D.DiscoError) as e:
+        muon.muon_update(ws, gs, ms, 0.1, inplace=True)
+    assert e.value.status == D.DISCO_ERR_UNSUPPORTED
+    assert all(torch.equal(w, k) for w, k in zip(ws, kept)) and not ms[0].any()
+    ps = [torch.nn.Parameter(w.clone()) for w in ws]
+    for p, g in zip(ps, gs):
+        p.grad = g
+    opt = muon.Muon([{"params": [ps[0]]}, {"params": [ps[1]]}])
+    with pytest.raises(D.DiscoError):
+        opt.step()
+    assert torch.equal(ps[0].detach(), ws[0])
