@@ -722,3 +722,24 @@ def check_forward_at(out, stats, x, gain, bias):
     if stats is not None:
         check(stats[0].unsqueeze(1), mean, (n + 1) * U * x.double().abs().amax(1, keepdim=True) + 1e-37, "mean")
         check(stats[1].unsqueeze(1), r, ((n + 1) * U * A + (n + 1) * U) * r, "1 / deviation")
+
+
+@gpu
+@pytest.mark.parametrize("size", [3e18, 1e20, 1e33])
+@pytest.mark.parametrize("shape", [s for s in FORMS if s[1] > 1])
+def test_squares_beyond_fp32_leave_the_bias(shape, size, cuda):
+    """Deviations whose squares overflow: the variance is infinite, r is 0 and out the bias in every
+    form, as 1 / sqrt(inf) has it; at 3e18 squares and the sum over a few channels still fit.  (Above
+    3e38 / C the sum of the channels itself may overflow.)"""
+    x = field(shape, F32, 73, cuda) * size
+    bias = field((1, shape[1]), F32, 74, cuda)[0]
+    out, stats = norm.layer_norm(x, None, bias)
+    over = ((x.double() - x.double().mean(1, keepdim=True)) ** 2).sum(1) > 1e39
+    assert not stats.isnan().any() and not out.isnan().any()
+    assert (stats[1][over] == 0).all()
+    hit = over.unsqueeze(1).expand_as(out)
+    assert torch.equal(out[hit], col(bias, x).float().expand_as(out)[hit])
+    if size == 3e18 and shape[1] < 7:
+        check_forward(x, None, bias, 1e-5)
+    dx = norm.layer_norm_backward(field(shape, F32, 75, cuda), x, stats)[0]
+    assert (dx[hit] == 0).all()
